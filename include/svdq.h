@@ -424,6 +424,70 @@ svdq_status svdq_selftest_wait_timeout(const svdq_layer* layer, unsigned budget_
 svdq_status svdq_linear_forward_static(const svdq_layer* layer, const void* X, int M, void* Y,
                                        void* stream, unsigned flags);
 
+/* ------------------------------------------------------- around the layer */
+
+/* The normalisation in front of a layer, with the residual stream's addition
+ * and an adaptive-norm modulation (a block of a diffusion transformer: the
+ * adaptive-norm linear gives shift, scale and gate rows, see SVDQ_W4A16_INT4).
+ * For each token row:
+ *
+ *     h = bf16(x + residual)                        (h = x without a residual)
+ *     n = (h - mu) / sqrt(mean((h - mu)^2) + eps)   (mu = mean(h) with
+ *                                                    SVDQ_NORM_CENTER, else 0)
+ *     y = bf16(n * weight * (1 + scale) + shift)
+ *
+ * with FP32 sums and products.  All pointers are device memory of the layer's
+ * device, BF16, 16-byte aligned; NULL leaves that step out.
+ *   residual      [M][K] added to X.
+ *   sum           [M][K], receives h; may be X or residual themselves, but not
+ *                 overlap them otherwise.
+ *   weight        [K].
+ *   scale, shift  rows of K values, mod_stride elements apart (a multiple of
+ *                 8; both may point into one wider row of modulation values).
+ *                 Token m uses row m / rows_per_mod, or row 0 when
+ *                 rows_per_mod is 0.
+ *   eps           finite and > 0.
+ *   flags         SVDQ_NORM_CENTER: layer norm; 0: RMS norm. */
+#define SVDQ_NORM_CENTER 0x1u
+
+typedef struct {
+  const void* residual;
+  void* sum;
+  const void* weight;
+  const void* scale;
+  const void* shift;
+  int64_t mod_stride;
+  int rows_per_mod;
+  float eps;
+  unsigned flags;
+} svdq_norm;
+
+/* svdq_norm_quantize_act -- normalisation and the first kernel in one pass:
+ * writes what svdq_quantize_act(layer, y, M, codes, scales, xl, stream, 0)
+ * would write for the normalised rows y, without y going through memory.  Codes
+ * and scales are bit for bit those of that call on the same y; XL = bf16(y L1d)
+ * (and bf16(y A) with an adapter) sums in another FP32 order and may differ by
+ * a BF16 rounding.
+ *   norm        as above; read during the call only.
+ *   X           device, [M][K] BF16, 16-byte aligned.
+ *   codes, scales, xl   as for svdq_quantize_act.
+ *   Y           device, [M][K] BF16 receiving y itself, or NULL; must not
+ *               overlap X, the residual or the sum.
+ * One kernel for every format (no per-token scale pass).  Errors: SVDQ_EINVAL
+ * (NULL norm, X, codes, scales, or xl where the layer has a branch; alignment,
+ * overlap, eps, mod_stride or rows_per_mod out of range; unknown flags),
+ * SVDQ_EUNSUPPORTED (a SVDQ_W4A16_INT4 layer; K above 16384), SVDQ_ESTATE,
+ * SVDQ_ECUDA. */
+svdq_status svdq_norm_quantize_act(const svdq_layer* layer, const svdq_norm* norm, const void* X, int M,
+                                   void* codes, void* scales, void* xl, void* Y, void* stream);
+
+/* svdq_norm_linear_forward -- svdq_norm_quantize_act, then the layer's GEMM:
+ * Y = layer(y) (device, [M][N] BF16; must not overlap X, the residual or the
+ * sum).  Workspace as for svdq_linear_forward.  flags: SVDQ_FWD_GELU,
+ * SVDQ_FWD_CHECK (others: SVDQ_EUNSUPPORTED). */
+svdq_status svdq_norm_linear_forward(const svdq_layer* layer, const svdq_norm* norm, const void* X, int M, void* Y,
+                                     void* workspace, size_t workspace_bytes, void* stream, unsigned flags);
+
 #ifdef __cplusplus
 }
 #endif

@@ -40,6 +40,8 @@ TENSORS = {
 }
 # preparation flags (svdq_config.flags)
 PREP_GPTQ, PREP_KEEP_GPTQ_FACTOR = 0x1, 0x2
+# normalisation flags (svdq_norm.flags)
+NORM_CENTER = 0x1
 
 EXPORTED = [
     "svdq_prepare", "svdq_destroy", "svdq_get_info", "svdq_tensor_bytes", "svdq_export",
@@ -48,6 +50,7 @@ EXPORTED = [
     "svdq_linear_forward_static", "svdq_act_code_bytes", "svdq_act_codes_to_logical",
     "svdq_selftest_wait_timeout", "svdq_mlp_workspace_bytes", "svdq_mlp_fc1", "svdq_mlp_forward",
     "svdq_set_lora", "svdq_serialized_bytes", "svdq_serialize", "svdq_deserialize",
+    "svdq_norm_quantize_act", "svdq_norm_linear_forward",
 ]
 STATIC_WORKSPACE_BYTES = 16 << 20   # SVDQ_STATIC_WORKSPACE_BYTES
 
@@ -67,6 +70,12 @@ class LayerInfo(ctypes.Structure):
     _fields_ = [("K", ctypes.c_int), ("N", ctypes.c_int), ("rank", ctypes.c_int), ("format", ctypes.c_int),
                 ("device", ctypes.c_int), ("g_x_exp", ctypes.c_int), ("g_w_exp", ctypes.c_int),
                 ("svd_iterations", ctypes.c_int), ("svd_tail_energy", ctypes.c_double)]
+
+
+class NormStruct(ctypes.Structure):
+    _fields_ = [("residual", ctypes.c_void_p), ("sum", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("shift", ctypes.c_void_p), ("mod_stride", ctypes.c_int64),
+                ("rows_per_mod", ctypes.c_int), ("eps", ctypes.c_float), ("flags", ctypes.c_uint)]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -107,6 +116,8 @@ def load() -> ctypes.CDLL:
         "svdq_serialized_bytes": (SZ, [P]),
         "svdq_serialize": (I, [P, P, SZ]),
         "svdq_deserialize": (I, [P, SZ, I, ctypes.POINTER(P)]),
+        "svdq_norm_quantize_act": (I, [P, P, P, I, P, P, P, P, P]),
+        "svdq_norm_linear_forward": (I, [P, P, P, I, P, P, SZ, P, U]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -170,6 +181,82 @@ def _stream(s) -> Optional[int]:
 def _check(status: int, what: str):
     if status != OK:
         raise SvdqError(status, what)
+
+
+def _is_tensor(x) -> bool:
+    return hasattr(x, "is_cuda") and hasattr(x, "stride")
+
+
+def _bf16_tensor(x, what: str):
+    if not x.is_cuda:
+        raise ValueError(f"{what}: must be a CUDA tensor")
+    if x.element_size() != 2 or not x.dtype.is_floating_point or str(x.dtype) != "torch.bfloat16":
+        raise ValueError(f"{what}: must be BF16, got {x.dtype}")
+
+
+class _Rows:
+    """Rows of BF16 values shared by runs of tokens (modulation scale and
+    shift, a gate): a 1D tensor is one row for all tokens, a 2D tensor -- a
+    column range of a wider one too -- row m // rows_per_row for token m.  A
+    raw address takes its stride from the caller and is not checked."""
+
+    def __init__(self, x, what: str, stride: Optional[int]):
+        self.what, self.x, self.rows, self.cols = what, x, None, None
+        self.stride = stride
+        if _is_tensor(x):
+            _bf16_tensor(x, what)
+            if x.dim() not in (1, 2) or x.stride(-1) != 1:
+                raise ValueError(f"{what}: must be [columns] or [rows][columns] with contiguous columns")
+            self.rows, self.cols = (1, x.shape[0]) if x.dim() == 1 else (x.shape[0], x.shape[1])
+            # the stride of a single row says nothing
+            if self.rows > 1:
+                self.stride = x.stride(0)
+            elif stride is None:
+                self.stride = self.cols
+
+    def need(self, M: int, cols: int, per: int):
+        if self.rows is None:
+            return
+        if self.cols < cols:
+            raise ValueError(f"{self.what}: {self.cols} columns, the call reads {cols}")
+        need = 1 if per <= 0 else -(-M // per)
+        if self.rows < need:
+            raise ValueError(f"{self.what}: {self.rows} rows, the call reads {need}")
+
+
+class Norm:
+    """A normalisation in front of a layer (svdq_norm): optional residual
+    addition (``sum`` receives it), RMS norm -- or layer norm with ``center`` --
+    times ``weight`` and modulated by rows of ``scale`` and ``shift``, of which
+    token m uses row m // rows_per_mod (0: row 0).  Holds references to its
+    tensors; one object can be used for any number of calls."""
+
+    def __init__(self, residual=None, sum=None, weight=None, scale=None, shift=None, rows_per_mod: int = 0,
+                 mod_stride: Optional[int] = None, eps: float = 1e-6, center: bool = False):
+        for t, what in ((residual, "residual"), (sum, "sum"), (weight, "weight")):
+            if _is_tensor(t):
+                _bf16_tensor(t, what)
+        rows = [_Rows(t, what, mod_stride) for t, what in ((scale, "scale"), (shift, "shift")) if t is not None]
+        strides = {r.stride for r in rows if r.rows != 1 or mod_stride is not None}
+        if len(strides) > 1:
+            raise ValueError("scale and shift: their rows must be the same distance apart")
+        stride = strides.pop() if strides else 0
+        self._keep = (residual, sum, weight, scale, shift)
+        self._rows, self._per = rows, int(rows_per_mod)
+        self._c = NormStruct(_ptr(residual), _ptr(sum), _ptr(weight), _ptr(scale), _ptr(shift), int(stride or 0),
+                             int(rows_per_mod), float(eps), NORM_CENTER if center else 0)
+        self._ref = ctypes.addressof(self._c)
+
+    def _need(self, M: int, K: int):
+        residual, total, weight = self._keep[:3]
+        if residual is not None:
+            _need(residual, M * K * 2, "residual")
+        if total is not None:
+            _need(total, M * K * 2, "sum")
+        if weight is not None:
+            _need(weight, K * 2, "weight")
+        for r in self._rows:
+            r.need(M, K, self._per)
 
 
 class Layer:
@@ -340,6 +427,26 @@ class Layer:
         self._need_act(M, Y=Y, codes=codes, scales=scales, xl=xl)
         _check(load().svdq_gemm(self._h, _ptr(codes), _ptr(scales), _ptr(xl), M, _ptr(Y), _stream(stream),
                                 flags), "svdq_gemm")
+
+    def norm_quantize_act(self, norm: Norm, X, M: int, codes, scales, xl, stream=None, Y=None):
+        """Normalisation and the first kernel in one pass (svdq_norm_quantize_act);
+        Y, if given, receives the normalised rows."""
+        self._need_act(M, X=X, codes=codes, scales=scales, xl=xl)
+        if M > 0:
+            norm._need(M, self._K)
+            if Y is not None:
+                _need(Y, M * self._K * 2, "Y")
+        _check(load().svdq_norm_quantize_act(self._h, norm._ref, _ptr(X), M, _ptr(codes), _ptr(scales), _ptr(xl),
+                                             _ptr(Y), _stream(stream)), "svdq_norm_quantize_act")
+
+    def norm_forward(self, norm: Norm, X, M: int, Y, workspace, workspace_bytes: int, stream=None, flags: int = 0):
+        """Normalisation, then the layer (svdq_norm_linear_forward)."""
+        self._need_act(M, X=X, Y=Y)
+        if M > 0:
+            norm._need(M, self._K)
+        _need(workspace, workspace_bytes, "workspace")
+        _check(load().svdq_norm_linear_forward(self._h, norm._ref, _ptr(X), M, _ptr(Y), _ptr(workspace),
+                                               workspace_bytes, _stream(stream), flags), "svdq_norm_linear_forward")
 
     def act_scales_to_logical(self, device_layout: np.ndarray, M: int) -> np.ndarray:
         """NVFP4: uint8 [M][K/16] E4M3 bytes; INT4: uint16 [M][K/64] BF16 bits;

@@ -736,6 +736,74 @@ svdq_status run_chain_fc1(const svdq_layer* L1, const svdq_layer* L2, const void
   return SVDQ_OK;
 }
 
+// ------------------------------------------------------------------ normalisation
+
+bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
+
+// Whether [a, a + na) and [b, b + nb) share a byte (NULL shares none).
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  if (!a || !b) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+svdq_status check_norm(const svdq_layer* L, const svdq_norm* n, const void* X, int M) {
+  if (!n || misaligned(n->residual) || misaligned(n->sum) || misaligned(n->weight) || misaligned(n->scale) ||
+      misaligned(n->shift))
+    return SVDQ_EINVAL;
+  if (n->flags & ~SVDQ_NORM_CENTER) return SVDQ_EINVAL;
+  if (!(n->eps > 0.0f) || !std::isfinite(n->eps)) return SVDQ_EINVAL;
+  if ((n->scale || n->shift) && (n->rows_per_mod < 0 || n->mod_stride < 0 || n->mod_stride % 8)) return SVDQ_EINVAL;
+  const size_t act = (size_t)M * L->host.K * 2;
+  if (n->sum != X && overlap(n->sum, act, X, act)) return SVDQ_EINVAL;
+  if (n->sum != n->residual && overlap(n->sum, act, n->residual, act)) return SVDQ_EINVAL;
+  if (!w4a4(L) || !norm_supported(L->host.K)) return SVDQ_EUNSUPPORTED;
+  return SVDQ_OK;
+}
+
+svdq_status run_norm(const svdq_layer* L, const svdq_norm* n, const void* X, int M, void* codes, void* scales,
+                     void* xl, void* y, cudaStream_t stream) {
+  const HostPrep& h = L->host;
+  const K1Params k = k1_params(L, M, codes, scales, xl);
+  NormParams p = {};
+  p.M = M;
+  p.K = h.K;
+  p.mpad = k.mpad;
+  p.nst = w8a8(h) ? int8_stages(h.K) : k.nst;
+  p.x = static_cast<const __nv_bfloat16*>(X);
+  p.residual = static_cast<const __nv_bfloat16*>(n->residual);
+  p.sum = static_cast<__nv_bfloat16*>(n->sum);
+  p.weight = static_cast<const __nv_bfloat16*>(n->weight);
+  p.scale = static_cast<const __nv_bfloat16*>(n->scale);
+  p.shift = static_cast<const __nv_bfloat16*>(n->shift);
+  p.mod_stride = n->mod_stride;
+  p.rows_per_mod = n->scale || n->shift ? n->rows_per_mod : 0;
+  p.center = (n->flags & SVDQ_NORM_CENTER) ? 1 : 0;
+  p.eps = n->eps;
+  p.y = static_cast<__nv_bfloat16*>(y);
+  p.c_x = k.c_x;
+  p.g_x_exp = k.g_x_exp;
+  for (int i = 0; i < 16; ++i) p.rcp[i] = k.rcp[i];
+  p.inv_lam = k.inv_lam;
+  p.codes = k.codes;
+  p.scales = k.scales;
+  p.xl = k.xl;
+  p.xl_stride = k.xl_stride;
+  // rank 32 is two blocks of 16 columns, W8A8's rank 16 one (its XL columns
+  // 16..31 are zero), an adapter two more
+  for (int i = 0; i < (h.rank + 15) / 16; ++i, ++p.nmt) {
+    p.amat[p.nmt] = L->d_l1t + (size_t)16 * i * h.K;
+    p.xl_col[p.nmt] = 16 * i;
+  }
+  p.xl_zero = h.rank == 16 ? 16 : 0;
+  for (int i = 0; h.lora_r > 0 && i < 2; ++i, ++p.nmt) {
+    p.amat[p.nmt] = L->d_lora_l1t + (size_t)16 * i * h.K;
+    p.xl_col[p.nmt] = 32 + 16 * i;
+  }
+  const int fmt = h.format == SVDQ_NVFP4 ? kFmtNvfp4 : w8a8(h) ? kFmtInt8 : kFmtInt4;
+  return launch_norm_quant(p, fmt, L->num_sms, stream) == cudaSuccess ? SVDQ_OK : SVDQ_ECUDA;
+}
+
 // The second kernel (the adapter, if any, is added inside it).
 svdq_status run_gemm_stage(const svdq_layer* L, const void* codes, const void* scales, const void* xl, int M,
                            void* Y, cudaStream_t s, bool branch, bool gelu, bool lora_on) {
@@ -1298,6 +1366,49 @@ svdq_status svdq_check(const svdq_layer* L, void* stream) {
     return SVDQ_ETIMEOUT;
   }
   return SVDQ_OK;
+}
+
+svdq_status svdq_norm_quantize_act(const svdq_layer* L, const svdq_norm* norm, const void* X, int M, void* codes,
+                                   void* scales, void* xl, void* Y, void* stream) {
+  if (misaligned(scales) || misaligned(xl) || misaligned(Y)) return SVDQ_EINVAL;
+  svdq_status st = check_forward_args(L, X, M, codes);
+  if (st == SVDQ_EINVAL) return st;
+  if (!scales) return SVDQ_EINVAL;
+  const svdq_status sn = check_norm(L, norm, X, M);
+  if (sn != SVDQ_OK) return sn;
+  if (st != SVDQ_OK) return st;
+  if ((L->host.rank > 0 || L->host.lora_r > 0) && !xl) return SVDQ_EINVAL;
+  const size_t act = (size_t)M * L->host.K * 2;
+  if (overlap(Y, act, X, act) || overlap(Y, act, norm->residual, act) || overlap(Y, act, norm->sum, act))
+    return SVDQ_EINVAL;
+  DeviceGuard g(L->device);
+  if (!g.ok) return SVDQ_ECUDA;
+  return run_norm(L, norm, X, M, codes, scales, xl, Y, static_cast<cudaStream_t>(stream));
+}
+
+svdq_status svdq_norm_linear_forward(const svdq_layer* L, const svdq_norm* norm, const void* X, int M, void* Y,
+                                     void* workspace, size_t workspace_bytes, void* stream, unsigned flags) {
+  svdq_status st = check_forward_args(L, X, M, Y);
+  if (st == SVDQ_EINVAL) return st;
+  const svdq_status sn = check_norm(L, norm, X, M);
+  if (sn != SVDQ_OK) return sn;
+  if (flags & ~(SVDQ_FWD_GELU | SVDQ_FWD_CHECK)) return SVDQ_EUNSUPPORTED;
+  const WsLayout w = ws_layout(L->host, M);
+  if (!workspace || workspace_bytes < w.total || (reinterpret_cast<uintptr_t>(workspace) & 255)) return SVDQ_EINVAL;
+  const size_t act = (size_t)M * L->host.K * 2, out = (size_t)M * L->host.N * 2;
+  if (overlap(Y, out, X, act) || overlap(Y, out, norm->residual, act) || overlap(Y, out, norm->sum, act))
+    return SVDQ_EINVAL;
+  if (st != SVDQ_OK) return st;
+  DeviceGuard g(L->device);
+  if (!g.ok) return SVDQ_ECUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  st = run_norm(L, norm, X, M, ws + w.codes, ws + w.scales, ws + w.xl, nullptr, s);
+  if (st == SVDQ_OK)
+    st = run_gemm_stage(L, ws + w.codes, ws + w.scales, ws + w.xl, M, Y, s, L->host.rank > 0,
+                        (flags & SVDQ_FWD_GELU) != 0, L->host.lora_r > 0);
+  if (st == SVDQ_OK && (flags & SVDQ_FWD_CHECK)) st = svdq_check(L, stream);
+  return st;
 }
 
 }  // extern "C"

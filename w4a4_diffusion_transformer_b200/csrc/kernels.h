@@ -141,6 +141,40 @@ int k1_rows_per_cta();
 cudaError_t launch_rowscale(const __nv_bfloat16* x, const float* inv_lam, int M, int K, int mpad, float* sx,
                             float* inv_sx, cudaStream_t stream);
 
+// Normalisation fused with the first kernel's outputs (norm_quant.cu).
+struct NormParams {
+  int M, K;
+  int mpad;                     // M rounded up to 128: rows of the scale layouts (and of tiled codes)
+  int nst;                      // stages of the tiled code layouts (NVFP4: 256 codes, INT8: 128)
+  const __nv_bfloat16* x;       // [M][K]
+  const __nv_bfloat16* residual;  // [M][K] or null
+  __nv_bfloat16* sum;           // [M][K] or null
+  const __nv_bfloat16* weight;  // [K] or null
+  const __nv_bfloat16* scale;   // rows of K, mod_stride elements apart, or null
+  const __nv_bfloat16* shift;
+  long long mod_stride;
+  int rows_per_mod;             // 0: one row for all tokens
+  int center;                   // 1: layer norm, 0: RMS norm
+  float eps;
+  __nv_bfloat16* y;             // [M][K] or null: the normalised rows themselves
+  float c_x;                    // the quantizer's constants, as in K1Params
+  int g_x_exp;
+  float rcp[16];
+  const float* inv_lam;         // [K]
+  uint8_t* codes;
+  uint8_t* scales;
+  __nv_bfloat16* xl;            // row stride xl_stride elements
+  int xl_stride;
+  int nmt;                      // blocks of 16 branch columns to project (0..4)
+  const __nv_bfloat16* amat[4]; // [16][K] each: rows of L1d^T, then of the adapter's A^T
+  int xl_col[4];                // XL column of each block's first
+  int xl_zero;                  // > 0: 16 XL columns from here are zero (W8A8's padding)
+};
+constexpr int kNormMaxK = 16384;
+constexpr size_t kNormMaxSmem = 232448;
+bool norm_supported(int K);
+cudaError_t launch_norm_quant(const NormParams& p, int fmt, int num_sms, cudaStream_t stream);
+
 // NVFP4 GEMM: operands from p.acodes / p.sfa (the first kernel's layouts) and
 // p.wmerged; tm_xl / tm_l2 the branch tiles, tm_y the output; with p.lora,
 // tm_xla / tm_l2a the LoRA tiles (XL_lora [M][32], (s B / alpha)^T [N][32]; the
