@@ -488,6 +488,79 @@ svdq_status svdq_norm_quantize_act(const svdq_layer* layer, const svdq_norm* nor
 svdq_status svdq_norm_linear_forward(const svdq_layer* layer, const svdq_norm* norm, const void* X, int M, void* Y,
                                      void* workspace, size_t workspace_bytes, void* stream, unsigned flags);
 
+/* Rotary positions with several axes (time, height, width; FLUX.1: 16 + 56 +
+ * 56 values of a head of 128).  A head of head_dim values rotates its first
+ * R = dim[0] + ... + dim[axes - 1]; the others pass.  Pair p < R/2 belongs to
+ * the axis whose share of the pairs holds it and turns by
+ *
+ *     position[axis] * theta^(-2 i / d),
+ *
+ * i the pair's index in its axis and d the axis' dim; with SVDQ_ROPE_SPAN i = p
+ * and d = R.  Pairs are neighbours (values 2p, 2p + 1) or, with SVDQ_ROPE_HALF,
+ * half the span apart (p, p + R/2).  With SVDQ_ROPE_NORM each head is first
+ * divided by sqrt(mean(x^2) + eps) over all of its head_dim values and
+ * multiplied by its tensor's weight.  Angles are formed in float64, the rest in
+ * FP32; one rounding to BF16.
+ *   axes      1 .. 4;  dim: even, > 0.
+ *   head_dim  a multiple of 8, 8 .. 256, at least R; R a multiple of 16 with
+ *             SVDQ_ROPE_HALF (else SVDQ_EUNSUPPORTED).
+ *   theta     finite, > 0;  eps: finite, > 0 with SVDQ_ROPE_NORM. */
+#define SVDQ_ROPE_HALF 0x1u
+#define SVDQ_ROPE_SPAN 0x2u
+#define SVDQ_ROPE_NORM 0x4u
+
+typedef struct {
+  int axes;
+  int dim[4];
+  int head_dim;
+  double theta;
+  float eps;
+  unsigned flags;
+} svdq_rope;
+
+/* The heads of one tensor, [batch][token][head][head_dim] BF16 with any order
+ * of strides: value (b, t, h, i) at in + b in_batch + t in_token + h in_head + i,
+ * strides in elements, >= 0, multiples of 8, pointers 16-byte aligned.  out may
+ * be in with the same strides (in place); otherwise the two must not overlap.
+ * No two values of out may share an address.  weight: [head_dim] BF16 or NULL
+ * (ones); not read without SVDQ_ROPE_NORM. */
+typedef struct {
+  const void* in;
+  void* out;
+  int heads;
+  int64_t in_batch, in_token, in_head;
+  int64_t out_batch, out_token, out_head;
+  const void* weight;
+} svdq_heads;
+
+/* svdq_rope_heads -- normalise and rotate the heads of q and, unless NULL, k
+ * (which may have fewer heads) of `batch` sequences of T tokens, in one kernel.
+ *   positions  device, float [T][axes], or [batch][T][axes] with pos_batch
+ *              elements between sequences (0: shared).  A non-finite position
+ *              gives NaN in the pairs that use it.
+ * Runs on the device that holds q->in, whichever is current.  Errors:
+ * SVDQ_EINVAL (NULL rope, q, positions or a tensor's pointers, sizes below 1,
+ * strides, alignment, overlap, flags, theta or eps out of range, memory that is
+ * not device memory), SVDQ_EUNSUPPORTED (head_dim, dims as above), SVDQ_ECUDA. */
+svdq_status svdq_rope_heads(const svdq_rope* rope, const svdq_heads* q, const svdq_heads* k, int batch, int T,
+                            const float* positions, int64_t pos_batch, void* stream);
+
+/* svdq_qkv_forward -- a fused QKV projection with its norms and rotation:
+ * [svdq_norm] -> layer -> svdq_rope_heads in place on the first q_heads heads
+ * of each row of Y and on the k_heads behind them; what follows (V) stays as
+ * the layer gives it.
+ *   norm       as for svdq_norm_quantize_act, or NULL: X is the layer's input.
+ *   X, Y       device, [batch * T][K] and [batch * T][N] BF16, N >= (q_heads +
+ *              k_heads) * head_dim; Y must not overlap X, the norm's residual
+ *              or its sum.
+ *   q_weight, k_weight   [head_dim] BF16 or NULL.
+ *   workspace  as for svdq_linear_forward over batch * T tokens.
+ *   flags      SVDQ_FWD_CHECK only. */
+svdq_status svdq_qkv_forward(const svdq_layer* layer, const svdq_norm* norm, const void* X, int batch, int T,
+                             const svdq_rope* rope, int q_heads, int k_heads, const void* q_weight,
+                             const void* k_weight, const float* positions, int64_t pos_batch, void* Y,
+                             void* workspace, size_t workspace_bytes, void* stream, unsigned flags);
+
 #ifdef __cplusplus
 }
 #endif

@@ -42,6 +42,8 @@ TENSORS = {
 PREP_GPTQ, PREP_KEEP_GPTQ_FACTOR = 0x1, 0x2
 # normalisation flags (svdq_norm.flags)
 NORM_CENTER = 0x1
+# rotary position flags (svdq_rope.flags)
+ROPE_HALF, ROPE_SPAN, ROPE_NORM = 0x1, 0x2, 0x4
 
 EXPORTED = [
     "svdq_prepare", "svdq_destroy", "svdq_get_info", "svdq_tensor_bytes", "svdq_export",
@@ -50,7 +52,7 @@ EXPORTED = [
     "svdq_linear_forward_static", "svdq_act_code_bytes", "svdq_act_codes_to_logical",
     "svdq_selftest_wait_timeout", "svdq_mlp_workspace_bytes", "svdq_mlp_fc1", "svdq_mlp_forward",
     "svdq_set_lora", "svdq_serialized_bytes", "svdq_serialize", "svdq_deserialize",
-    "svdq_norm_quantize_act", "svdq_norm_linear_forward",
+    "svdq_norm_quantize_act", "svdq_norm_linear_forward", "svdq_rope_heads", "svdq_qkv_forward",
 ]
 STATIC_WORKSPACE_BYTES = 16 << 20   # SVDQ_STATIC_WORKSPACE_BYTES
 
@@ -76,6 +78,18 @@ class NormStruct(ctypes.Structure):
     _fields_ = [("residual", ctypes.c_void_p), ("sum", ctypes.c_void_p), ("weight", ctypes.c_void_p),
                 ("scale", ctypes.c_void_p), ("shift", ctypes.c_void_p), ("mod_stride", ctypes.c_int64),
                 ("rows_per_mod", ctypes.c_int), ("eps", ctypes.c_float), ("flags", ctypes.c_uint)]
+
+
+class RopeStruct(ctypes.Structure):
+    _fields_ = [("axes", ctypes.c_int), ("dim", ctypes.c_int * 4), ("head_dim", ctypes.c_int),
+                ("theta", ctypes.c_double), ("eps", ctypes.c_float), ("flags", ctypes.c_uint)]
+
+
+class HeadsStruct(ctypes.Structure):
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int),
+                ("in_batch", ctypes.c_int64), ("in_token", ctypes.c_int64), ("in_head", ctypes.c_int64),
+                ("out_batch", ctypes.c_int64), ("out_token", ctypes.c_int64), ("out_head", ctypes.c_int64),
+                ("weight", ctypes.c_void_p)]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -118,6 +132,8 @@ def load() -> ctypes.CDLL:
         "svdq_deserialize": (I, [P, SZ, I, ctypes.POINTER(P)]),
         "svdq_norm_quantize_act": (I, [P, P, P, I, P, P, P, P, P]),
         "svdq_norm_linear_forward": (I, [P, P, P, I, P, P, SZ, P, U]),
+        "svdq_rope_heads": (I, [P, P, P, I, I, P, ctypes.c_int64, P]),
+        "svdq_qkv_forward": (I, [P, P, P, I, I, P, I, I, P, P, P, ctypes.c_int64, P, P, SZ, P, U]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -257,6 +273,78 @@ class Norm:
             _need(weight, K * 2, "weight")
         for r in self._rows:
             r.need(M, K, self._per)
+
+
+class Rope:
+    """Rotary positions with several axes (svdq_rope): dims[a] values of a head
+    belong to axis a; ``half`` pairs values half the span apart instead of
+    neighbours, ``span`` runs the frequencies over the whole span instead of
+    each axis, ``norm`` puts the per-head RMS norm in front."""
+
+    def __init__(self, head_dim: int, dims, theta: float = 10000.0, half: bool = False, span: bool = False,
+                 norm: bool = False, eps: float = 1e-6):
+        dims = tuple(int(d) for d in dims)
+        if not 1 <= len(dims) <= 4:
+            raise ValueError(f"1 to 4 axes, got {len(dims)}")
+        self.head_dim, self.axes = int(head_dim), len(dims)
+        self._c = RopeStruct(len(dims), (ctypes.c_int * 4)(*dims), int(head_dim), float(theta), float(eps),
+                             (ROPE_HALF if half else 0) | (ROPE_SPAN if span else 0) | (ROPE_NORM if norm else 0))
+        self._ref = ctypes.addressof(self._c)
+
+
+class Heads:
+    """The heads of queries or keys (svdq_heads): BF16 CUDA tensors
+    [batch, token, head, head_dim] -- or [token, head, head_dim] -- of any
+    strides over contiguous values; out None is in place.  Holds references to
+    its tensors; one object can be used for any number of calls."""
+
+    def __init__(self, x, out=None, weight=None):
+        out = x if out is None else out
+        shapes = []
+        for t, what in ((x, "x"), (out, "out")):
+            _bf16_tensor(t, what)
+            if t.dim() not in (3, 4) or t.stride(-1) != 1:
+                raise ValueError(f"{what}: must be [batch, token, head, head_dim] with contiguous values")
+            shapes.append(tuple(t.shape) if t.dim() == 4 else (1,) + tuple(t.shape))
+        if shapes[0] != shapes[1]:
+            raise ValueError(f"x and out differ in shape: {shapes[0]} and {shapes[1]}")
+        self.batch, self.tokens, self.heads, self.head_dim = shapes[0]
+        if weight is not None:
+            if _is_tensor(weight):
+                _bf16_tensor(weight, "weight")
+            _need(weight, self.head_dim * 2, "weight")
+
+        def strides(t):
+            s = tuple(t.stride())[:-1]
+            s = s if t.dim() == 4 else (0,) + s
+            # the stride of an axis of one is not used
+            return [v if n > 1 else 0 for v, n in zip(s, shapes[0])]
+        self._keep = (x, out, weight)
+        self._c = HeadsStruct(_ptr(x), _ptr(out), self.heads, *strides(x), *strides(out), _ptr(weight))
+        self._ref = ctypes.addressof(self._c)
+
+
+def _positions(rope: Rope, positions, batch: int, tokens: int) -> int:
+    """Elements between the positions of two sequences (0: shared)."""
+    if not _is_tensor(positions):
+        return 0
+    if not positions.is_cuda or str(positions.dtype) != "torch.float32" or not positions.is_contiguous():
+        raise ValueError("positions: must be a contiguous float32 CUDA tensor")
+    shape = tuple(positions.shape)
+    if shape not in ((tokens, rope.axes), (1, tokens, rope.axes), (batch, tokens, rope.axes)):
+        raise ValueError(f"positions: must be [{tokens}, {rope.axes}] or [{batch}, {tokens}, {rope.axes}], got {shape}")
+    return tokens * rope.axes if len(shape) == 3 and shape[0] > 1 else 0
+
+
+def rope_heads(rope: Rope, q: Heads, k: Optional[Heads], positions, stream=None):
+    """Normalise and rotate the heads of q and k (svdq_rope_heads); positions:
+    float32 [token, axis], or [batch, token, axis]."""
+    for t, what in ((q, "q"), (k, "k")):
+        if t is not None and (t.head_dim != rope.head_dim or (t.batch, t.tokens) != (q.batch, q.tokens)):
+            raise ValueError(f"{what}: [{t.batch}, {t.tokens}, heads, {t.head_dim}] does not fit the others")
+    pos_batch = _positions(rope, positions, q.batch, q.tokens)
+    _check(load().svdq_rope_heads(rope._ref, q._ref, None if k is None else k._ref, q.batch, q.tokens,
+                                  _ptr(positions), pos_batch, _stream(stream)), "svdq_rope_heads")
 
 
 class Layer:
@@ -447,6 +535,27 @@ class Layer:
         _need(workspace, workspace_bytes, "workspace")
         _check(load().svdq_norm_linear_forward(self._h, norm._ref, _ptr(X), M, _ptr(Y), _ptr(workspace),
                                                workspace_bytes, _stream(stream), flags), "svdq_norm_linear_forward")
+
+    def qkv_forward(self, norm: Optional[Norm], X, batch: int, T: int, rope: Rope, q_heads: int, k_heads: int,
+                    positions, Y, workspace, workspace_bytes: int, q_weight=None, k_weight=None, stream=None,
+                    flags: int = 0):
+        """[norm ->] layer -> per-head norm and rotation of the first q_heads +
+        k_heads heads of each row, in place (svdq_qkv_forward)."""
+        M = batch * T
+        self._need_act(M, X=X, Y=Y)
+        pos_batch = 0
+        if batch > 0 and T > 0:
+            if norm is not None:
+                norm._need(M, self._K)
+            pos_batch = _positions(rope, positions, batch, T)
+        for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+            if w is not None:
+                _need(w, rope.head_dim * 2, what)
+        _need(workspace, workspace_bytes, "workspace")
+        _check(load().svdq_qkv_forward(self._h, None if norm is None else norm._ref, _ptr(X), batch, T, rope._ref,
+                                       q_heads, k_heads, _ptr(q_weight), _ptr(k_weight), _ptr(positions), pos_batch,
+                                       _ptr(Y), _ptr(workspace), workspace_bytes, _stream(stream), flags),
+               "svdq_qkv_forward")
 
     def act_scales_to_logical(self, device_layout: np.ndarray, M: int) -> np.ndarray:
         """NVFP4: uint8 [M][K/16] E4M3 bytes; INT4: uint16 [M][K/64] BF16 bits;

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
@@ -804,6 +805,93 @@ svdq_status run_norm(const svdq_layer* L, const svdq_norm* n, const void* X, int
   return launch_norm_quant(p, fmt, L->num_sms, stream) == cudaSuccess ? SVDQ_OK : SVDQ_ECUDA;
 }
 
+// ------------------------------------------------------------------ rotary positions
+
+// Elements that [n0][n1][n2] rows of `inner` values span, or -1 if two of them
+// share an address (strides sorted, each at least what lies inside it).
+int64_t span_of(int64_t inner, const int64_t (&stride)[3], const int64_t (&count)[3], bool distinct) {
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int a, int b) { return stride[a] < stride[b]; });
+  int64_t extent = inner;
+  for (int i : order) {
+    if (count[i] <= 1) continue;
+    if (distinct && stride[i] < extent) return -1;
+    if (stride[i] > (INT64_MAX / 4 - extent) / (count[i] - 1)) return -1;
+    extent += stride[i] * (count[i] - 1);
+  }
+  return extent;
+}
+
+svdq_status check_rope(const svdq_rope* r) {
+  if (!r) return SVDQ_EINVAL;
+  if (r->flags & ~(SVDQ_ROPE_HALF | SVDQ_ROPE_SPAN | SVDQ_ROPE_NORM)) return SVDQ_EINVAL;
+  if (r->axes < 1 || r->axes > 4 || r->head_dim < 1) return SVDQ_EINVAL;
+  if (!(r->theta > 0.0) || !std::isfinite(r->theta)) return SVDQ_EINVAL;
+  if ((r->flags & SVDQ_ROPE_NORM) && (!(r->eps > 0.0f) || !std::isfinite(r->eps))) return SVDQ_EINVAL;
+  int64_t R = 0;
+  for (int a = 0; a < r->axes; ++a) {
+    if (r->dim[a] < 1 || r->dim[a] % 2) return SVDQ_EINVAL;
+    R += r->dim[a];
+  }
+  if (R > r->head_dim) return SVDQ_EINVAL;
+  if (r->head_dim % 8 || r->head_dim > 256 || ((r->flags & SVDQ_ROPE_HALF) && R % 16)) return SVDQ_EUNSUPPORTED;
+  return SVDQ_OK;
+}
+
+svdq_status check_heads(const svdq_rope* r, const svdq_heads* t, int B, int T) {
+  if (!t->in || !t->out || t->heads < 1 || misaligned(t->in) || misaligned(t->out) || misaligned(t->weight))
+    return SVDQ_EINVAL;
+  const int64_t in[3] = {t->in_batch, t->in_token, t->in_head}, out[3] = {t->out_batch, t->out_token, t->out_head};
+  const int64_t n[3] = {B, T, t->heads};
+  bool same = t->in == t->out;
+  for (int i = 0; i < 3; ++i) {
+    if (in[i] < 0 || out[i] < 0 || in[i] % 8 || out[i] % 8) return SVDQ_EINVAL;
+    if (n[i] > 1 && in[i] != out[i]) same = false;
+  }
+  const int64_t si = span_of(r->head_dim, in, n, false), so = span_of(r->head_dim, out, n, true);
+  if (si < 0 || so < 0) return SVDQ_EINVAL;
+  if (!same && overlap(t->in, (size_t)si * 2, t->out, (size_t)so * 2)) return SVDQ_EINVAL;
+  return SVDQ_OK;
+}
+
+RopeTensor rope_tensor(const svdq_heads* t) {
+  RopeTensor o = {};
+  o.in = static_cast<const __nv_bfloat16*>(t->in);
+  o.out = static_cast<__nv_bfloat16*>(t->out);
+  o.in_batch = t->in_batch;
+  o.in_token = t->in_token;
+  o.in_head = t->in_head;
+  o.out_batch = t->out_batch;
+  o.out_token = t->out_token;
+  o.out_head = t->out_head;
+  o.weight = static_cast<const __nv_bfloat16*>(t->weight);
+  o.heads = t->heads;
+  return o;
+}
+
+svdq_status run_rope(const svdq_rope* r, const svdq_heads* q, const svdq_heads* k, int B, int T, const float* positions,
+                     int64_t pos_batch, int num_sms, cudaStream_t stream) {
+  RopeParams p = {};
+  p.q = rope_tensor(q);
+  if (k) p.k = rope_tensor(k);
+  p.B = B;
+  p.T = T;
+  p.D = r->head_dim;
+  p.axes = r->axes;
+  for (int a = 0; a < r->axes; ++a) {
+    p.dim[a] = r->dim[a];
+    p.R += r->dim[a];
+  }
+  p.half = (r->flags & SVDQ_ROPE_HALF) ? 1 : 0;
+  p.span = (r->flags & SVDQ_ROPE_SPAN) ? 1 : 0;
+  p.norm = (r->flags & SVDQ_ROPE_NORM) ? 1 : 0;
+  p.eps = r->eps;
+  p.log2_theta = std::log2(r->theta);
+  p.positions = positions;
+  p.pos_batch = pos_batch;
+  return launch_rope(p, num_sms, stream) == cudaSuccess ? SVDQ_OK : SVDQ_ECUDA;
+}
+
 // The second kernel (the adapter, if any, is added inside it).
 svdq_status run_gemm_stage(const svdq_layer* L, const void* codes, const void* scales, const void* xl, int M,
                            void* Y, cudaStream_t s, bool branch, bool gelu, bool lora_on) {
@@ -1407,6 +1495,64 @@ svdq_status svdq_norm_linear_forward(const svdq_layer* L, const svdq_norm* norm,
   if (st == SVDQ_OK)
     st = run_gemm_stage(L, ws + w.codes, ws + w.scales, ws + w.xl, M, Y, s, L->host.rank > 0,
                         (flags & SVDQ_FWD_GELU) != 0, L->host.lora_r > 0);
+  if (st == SVDQ_OK && (flags & SVDQ_FWD_CHECK)) st = svdq_check(L, stream);
+  return st;
+}
+
+svdq_status svdq_rope_heads(const svdq_rope* rope, const svdq_heads* q, const svdq_heads* k, int batch, int T,
+                            const float* positions, int64_t pos_batch, void* stream) {
+  if (!q || !positions || batch < 1 || T < 1 || (int64_t)batch * T > INT_MAX || pos_batch < 0 ||
+      (reinterpret_cast<uintptr_t>(positions) & 3))
+    return SVDQ_EINVAL;
+  svdq_status st = check_rope(rope);
+  if (st == SVDQ_OK) st = check_heads(rope, q, batch, T);
+  if (st == SVDQ_OK && k) st = check_heads(rope, k, batch, T);
+  if (st != SVDQ_OK) return st;
+  cudaPointerAttributes at = {};
+  if (cudaPointerGetAttributes(&at, q->in) != cudaSuccess) return SVDQ_ECUDA;
+  if (at.type != cudaMemoryTypeDevice && at.type != cudaMemoryTypeManaged) return SVDQ_EINVAL;
+  DeviceGuard g(at.device);
+  if (!g.ok) return SVDQ_ECUDA;
+  int sms = 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, at.device) != cudaSuccess) return SVDQ_ECUDA;
+  return run_rope(rope, q, k, batch, T, positions, pos_batch, sms, static_cast<cudaStream_t>(stream));
+}
+
+svdq_status svdq_qkv_forward(const svdq_layer* L, const svdq_norm* norm, const void* X, int batch, int T,
+                             const svdq_rope* rope, int q_heads, int k_heads, const void* q_weight,
+                             const void* k_weight, const float* positions, int64_t pos_batch, void* Y,
+                             void* workspace, size_t workspace_bytes, void* stream, unsigned flags) {
+  if (!L || !X || !Y || !positions || batch < 1 || T < 1 || (int64_t)batch * T > INT_MAX || pos_batch < 0 ||
+      (reinterpret_cast<uintptr_t>(positions) & 3) || q_heads < 1 || k_heads < 0)
+    return SVDQ_EINVAL;
+  svdq_status st = check_rope(rope);
+  if (st != SVDQ_OK) return st;
+  const int D = rope->head_dim, N = L->host.N, M = batch * T;
+  if (((int64_t)q_heads + k_heads) * D > N) return SVDQ_EINVAL;
+  svdq_heads h[2] = {};
+  for (int i = 0; i < 2; ++i) {
+    h[i].out = static_cast<__nv_bfloat16*>(Y) + (size_t)i * q_heads * D;
+    h[i].in = h[i].out;
+    h[i].heads = i ? k_heads : q_heads;
+    h[i].in_batch = h[i].out_batch = (int64_t)T * N;
+    h[i].in_token = h[i].out_token = N;
+    h[i].in_head = h[i].out_head = D;
+    h[i].weight = i ? k_weight : q_weight;
+  }
+  for (int i = 0; i < (k_heads ? 2 : 1) && st == SVDQ_OK; ++i) st = check_heads(rope, &h[i], batch, T);
+  if (st != SVDQ_OK) return st;
+  if (!w4a4(L) || (flags & ~SVDQ_FWD_CHECK)) return SVDQ_EUNSUPPORTED;
+  if (norm) {
+    st = svdq_norm_linear_forward(L, norm, X, M, Y, workspace, workspace_bytes, stream, 0);
+  } else {
+    if (overlap(Y, (size_t)M * N * 2, X, (size_t)M * L->host.K * 2)) return SVDQ_EINVAL;
+    st = svdq_linear_forward(L, X, M, Y, workspace, workspace_bytes, stream, 0);
+  }
+  if (st != SVDQ_OK) return st;
+  DeviceGuard g(L->device);
+  if (!g.ok) return SVDQ_ECUDA;
+  st = run_rope(rope, &h[0], k_heads ? &h[1] : nullptr, batch, T, positions, pos_batch, L->num_sms,
+                static_cast<cudaStream_t>(stream));
   if (st == SVDQ_OK && (flags & SVDQ_FWD_CHECK)) st = svdq_check(L, stream);
   return st;
 }

@@ -175,6 +175,28 @@ constexpr size_t kNormMaxSmem = 232448;
 bool norm_supported(int K);
 cudaError_t launch_norm_quant(const NormParams& p, int fmt, int num_sms, cudaStream_t stream);
 
+// Rotary positions with several axes (rope.cu).  Strides in elements.
+struct RopeTensor {
+  const __nv_bfloat16* in;
+  __nv_bfloat16* out;
+  long long in_batch, in_token, in_head, out_batch, out_token, out_head;
+  const __nv_bfloat16* weight;  // [D] or null
+  int heads;
+};
+struct RopeParams {
+  RopeTensor q, k;              // k.heads may be 0
+  int B, T, D;
+  int R;                        // rotated values of a head
+  int axes, dim[4];
+  int half, span, norm;
+  float eps;
+  double log2_theta;
+  const float* positions;       // [B or 1][T][axes]
+  long long pos_batch;
+  int splits;                   // warps that share a token (set by the launcher)
+};
+cudaError_t launch_rope(RopeParams p, int num_sms, cudaStream_t stream);
+
 // NVFP4 GEMM: operands from p.acodes / p.sfa (the first kernel's layouts) and
 // p.wmerged; tm_xl / tm_l2 the branch tiles, tm_y the output; with p.lora,
 // tm_xla / tm_l2a the LoRA tiles (XL_lora [M][32], (s B / alpha)^T [N][32]; the
