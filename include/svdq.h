@@ -476,7 +476,7 @@ typedef struct {
  * One kernel for every format (no per-token scale pass).  Errors: SVDQ_EINVAL
  * (NULL norm, X, codes, scales, or xl where the layer has a branch; alignment,
  * overlap, eps, mod_stride or rows_per_mod out of range; unknown flags),
- * SVDQ_EUNSUPPORTED (a SVDQ_W4A16_INT4 layer; K above 16384), SVDQ_ESTATE,
+ * SVDQ_EUNSUPPORTED (a SVDQ_W4A16_INT4 layer; K above 14336), SVDQ_ESTATE,
  * SVDQ_ECUDA. */
 svdq_status svdq_norm_quantize_act(const svdq_layer* layer, const svdq_norm* norm, const void* X, int M,
                                    void* codes, void* scales, void* xl, void* Y, void* stream);

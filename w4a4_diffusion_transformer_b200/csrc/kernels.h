@@ -168,12 +168,13 @@ struct NormParams {
   int nmt;                      // blocks of 16 branch columns to project (0..4)
   const __nv_bfloat16* amat[4]; // [16][K] each: rows of L1d^T, then of the adapter's A^T
   int xl_col[4];                // XL column of each block's first
+  int warps_per_row;            // set by the launcher
   int xl_zero;                  // > 0: 16 XL columns from here are zero (W8A8's padding)
 };
-constexpr int kNormMaxK = 16384;
+constexpr int kNormMaxK = 14336;              // a row's parameters and its tile fit in shared memory
 constexpr size_t kNormMaxSmem = 232448;
 bool norm_supported(int K);
-cudaError_t launch_norm_quant(const NormParams& p, int fmt, int num_sms, cudaStream_t stream);
+cudaError_t launch_norm_quant(NormParams p, int fmt, int num_sms, cudaStream_t stream);
 
 // Rotary positions with several axes (rope.cu).  Strides in elements.
 struct RopeTensor {

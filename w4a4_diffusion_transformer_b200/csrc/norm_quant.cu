@@ -23,11 +23,14 @@ namespace svdq {
 
 namespace {
 
-// A thread owns 16 columns of every row of its CTA's tile of R rows: the
-// parameters of its columns are read once per tile, a thread's 16 columns are
-// one NVFP4 group, a quarter of an INT4 group and one 16-byte chunk of INT8
-// codes, and a row's sums need two barriers whatever R.
-constexpr int kCols = 16;
+// A CTA of 8 warps handles tiles of 8 / W rows, W warps to a row; lane l of the
+// row's warp w owns the 8-value chunks (c W + w) 32 + l of the row and keeps
+// them, as BF16 pairs, in registers between the passes.  The columns'
+// parameters w (1 + scale), shift and 1/lam sit in shared memory as FP32, filled
+// once per CTA and modulation row; chunk q's eight values are two 16-byte words
+// at q and q + K/8, so that a warp's reads are free of bank conflicts.
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
 
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
@@ -36,36 +39,37 @@ __device__ __forceinline__ uint32_t pack2(float2 v) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-
-// 32 bytes (16 BF16 values) of global memory.
-__device__ __forceinline__ void load16(const __nv_bfloat16* p, uint32_t (&w)[8]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint4 b = *(reinterpret_cast<const uint4*>(p) + 1);
-  w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-  w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 h =
+      __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// The tile's R row totals of v, in every thread: warps reduce by shuffles, the
-// warps' partials meet in shared memory and are added in warp order.
-template <int R, bool kMax>
-__device__ __forceinline__ void reduce_rows(float (&v)[R], float* part, int nwarps) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// Eight FP32 parameters of chunk q.
+__device__ __forceinline__ void param8(const float4* t, int q, int nch, float2 (&v)[4]) {
+  const float4 a = t[q], b = t[q + nch];
+  v[0] = make_float2(a.x, a.y);
+  v[1] = make_float2(a.z, a.w);
+  v[2] = make_float2(b.x, b.y);
+  v[3] = make_float2(b.z, b.w);
+}
+
+// A row's total (or maximum) in every lane of its W warps: shuffles, then the
+// warps' partials through `slot` (W floats of this row), added in warp order.
+template <bool kMax>
+__device__ __forceinline__ float reduce_row(float v, float* slot, int W, int w, int bar) {
 #pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float u = __shfl_xor_sync(0xffffffffu, v[r], o);
-      v[r] = kMax ? fmaxf(v[r], u) : v[r] + u;
-    }
-  if (lane == 0)
-#pragma unroll
-    for (int r = 0; r < R; ++r) part[warp * R + r] = v[r];
-  __syncthreads();
-#pragma unroll
-  for (int r = 0; r < R; ++r) v[r] = part[r];
-  for (int w = 1; w < nwarps; ++w)
-#pragma unroll
-    for (int r = 0; r < R; ++r) v[r] = kMax ? fmaxf(v[r], part[w * R + r]) : v[r] + part[w * R + r];
+  for (int o = 16; o > 0; o >>= 1) {
+    const float u = __shfl_xor_sync(0xffffffffu, v, o);
+    v = kMax ? fmaxf(v, u) : v + u;
+  }
+  if (W > 1) {
+    if ((threadIdx.x & 31) == 0) slot[w] = v;
+    dev::named_barrier(bar, 32 * W);
+    v = slot[0];
+    for (int i = 1; i < W; ++i) v = kMax ? fmaxf(v, slot[i]) : v + slot[i];
+  }
+  return v;
 }
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -77,321 +81,309 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Shared memory in front of the y tile: three reduction buffers and the constants.
-__host__ __device__ constexpr int head_bytes(int R, int nwarps) { return (3 * R * nwarps * 4 + 64 + 15) / 16 * 16; }
-
-template <int R, int kFmt>
-__global__ void __launch_bounds__(R > 2 ? 512 : 1024) norm_quant_kernel(const NormParams p) {
+template <int kFmt, int C>
+__global__ void __launch_bounds__(kThreads, 2) norm_quant_kernel(const NormParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
-  const int K = p.K, M = p.M;
-  const int nwarps = blockDim.x >> 5;
-  const int ystride = 2 * K + 64;                       // bytes between rows of the y tile (bank shift by rows)
-  float* part0 = reinterpret_cast<float*>(smem);        // three reductions, a buffer each
-  float* part1 = part0 + R * nwarps;
-  float* part2 = part1 + R * nwarps;
-  float* rcp = part2 + R * nwarps;                      // the NVFP4 quantizer's constants
-  uint8_t* ytile = smem + head_bytes(R, nwarps);
-  const int tid = threadIdx.x;
-  const int c0 = tid * kCols;
-  const bool act = c0 < K;
-  const int row0 = blockIdx.x * R;
+  const int K = p.K, M = p.M, nch = K >> 3;             // chunks of 8 values in a row
+  const int W = p.warps_per_row, rows = kWarps / W;
+  float* slots = reinterpret_cast<float*>(smem);        // [2][3][8]: tile parity, reduction, warp
+  float* rcp = slots + 2 * 3 * kWarps;                  // the NVFP4 quantizer's constants
+  float4* gain = reinterpret_cast<float4*>(rcp + 16);   // w (1 + scale)
+  float4* shift = gain + 2 * nch;
+  float4* ilam = shift + 2 * nch;
+  uint8_t* ytile = reinterpret_cast<uint8_t*>(ilam + 2 * nch);
+  const int ystride = 2 * K + 64;                       // 64 bytes: rows shifted by half the banks
+  float* red = reinterpret_cast<float*>(ytile + rows * ystride);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rg = warp / W, w = warp % W;                // this warp's row of the tile, its place in the row
+  const int q0 = w * 32 + lane;                         // first chunk; the next are 32 W apart
 
   dev::griddep_launch_dependents();
-  if (kFmt == kFmtNvfp4 && tid < 16) rcp[tid] = p.rcp[tid];
+  if (kFmt == kFmtNvfp4 && threadIdx.x < 16) rcp[threadIdx.x] = p.rcp[threadIdx.x];
+  for (int i = threadIdx.x; i < 2 * nch; i += kThreads)
+    ilam[(i >> 1) + (i & 1) * nch] = reinterpret_cast<const float4*>(p.inv_lam)[i];
   // X may be the preceding kernel's output, and that kernel may still read the
   // buffers this one writes
   dev::griddep_wait();
 
-  uint32_t h[R][8];
-  float s[R];
+  const float invK = 1.0f / (float)K;
+  const int tiles = (p.mpad + rows - 1) / rows;
+  const int t0 = (int)((long long)tiles * blockIdx.x / gridDim.x);
+  const int t1 = (int)((long long)tiles * (blockIdx.x + 1) / gridDim.x);
+  int loaded = -1;                                      // modulation row in shared memory
+  for (int tile = t0; tile < t1; ++tile) {
+    const int row = tile * rows + rg;
+    const bool live = row < M;                          // rows M .. mpad - 1: zero codes and scales
+    float* slot = slots + ((tile & 1) * 3) * kWarps + rg * W;
+    uint32_t h[C][4];
+    // ---- h = bf16(x + r)
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
+    for (int c = 0; c < C; ++c) {
+      const int q = q0 + c * 32 * W;
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (live && q < nch) v = *reinterpret_cast<const uint4*>(p.x + (size_t)row * K + 8 * q);
+      h[c][0] = v.x; h[c][1] = v.y; h[c][2] = v.z; h[c][3] = v.w;
+    }
+    if (p.residual && live) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[r][i] = 0u;
-    if (act && row0 + r < M) load16(p.x + (size_t)(row0 + r) * K + c0, h[r]);
-  }
-  if (p.residual) {
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (act && row0 + r < M) {
-        uint32_t q[8];
-        load16(p.residual + (size_t)(row0 + r) * K + c0, q);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 a = unpack2(h[r][i]), b = unpack2(q[i]);
-          h[r][i] = pack2(make_float2(a.x + b.x, a.y + b.y));
+      for (int c = 0; c < C; ++c) {
+        const int q = q0 + c * 32 * W;
+        if (q < nch) {
+          const uint4 v = *reinterpret_cast<const uint4*>(p.residual + (size_t)row * K + 8 * q);
+          h[c][0] = add_bf16x2(h[c][0], v.x);
+          h[c][1] = add_bf16x2(h[c][1], v.y);
+          h[c][2] = add_bf16x2(h[c][2], v.z);
+          h[c][3] = add_bf16x2(h[c][3], v.w);
         }
       }
-  }
-  if (p.sum) {
+    }
+    if (p.sum && live) {
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-      if (act && row0 + r < M) {
-        uint4* o = reinterpret_cast<uint4*>(p.sum + (size_t)(row0 + r) * K + c0);
-        o[0] = make_uint4(h[r][0], h[r][1], h[r][2], h[r][3]);
-        o[1] = make_uint4(h[r][4], h[r][5], h[r][6], h[r][7]);
+      for (int c = 0; c < C; ++c) {
+        const int q = q0 + c * 32 * W;
+        if (q < nch)
+          *reinterpret_cast<uint4*>(p.sum + (size_t)row * K + 8 * q) = make_uint4(h[c][0], h[c][1], h[c][2], h[c][3]);
       }
-  }
-
-  // ---- statistics: the mean first (layer norm), then the mean square about it
-  const float invK = 1.0f / (float)K;
-  float mu[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) mu[r] = 0.f;
-  if (p.center) {
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
+    }
+    // ---- the tile's modulation rows: one, but where two sequences meet
+    const int first = min(tile * rows, M - 1), last = min(tile * rows + rows, M) - 1;
+    const int m0 = p.rows_per_mod > 0 ? first / p.rows_per_mod : 0;
+    const int m1 = p.rows_per_mod > 0 ? last / p.rows_per_mod : 0;
+    const int mine = m0 == m1 ? m0 : min(row, M - 1) / p.rows_per_mod;
+    // ---- statistics: the mean first (layer norm), then the mean square about it
+    float mu = 0.f;
+    if (p.center) {
       float2 a = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) a = __fadd2_rn(a, unpack2(h[r][i]));
-      mu[r] = a.x + a.y;
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a = __fadd2_rn(a, unpack2(h[c][i]));
+      mu = reduce_row<false>(a.x + a.y, slot, W, w, 1 + rg) * invK;
     }
-    reduce_rows<R, false>(mu, part0, nwarps);
+    float2 a2 = make_float2(0.f, 0.f);
+    const float2 nmu2 = make_float2(-mu, -mu);
 #pragma unroll
-    for (int r = 0; r < R; ++r) mu[r] *= invK;
-  }
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    float2 a = make_float2(0.f, 0.f);
-    const float2 m2 = make_float2(-mu[r], -mu[r]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 d = __fadd2_rn(unpack2(h[r][i]), m2);
-      a = __ffma2_rn(d, d, a);
-    }
-    s[r] = act ? a.x + a.y : 0.f;                       // a thread past K holds zeros, not values
-  }
-  reduce_rows<R, false>(s, part1, nwarps);
-#pragma unroll
-  for (int r = 0; r < R; ++r) s[r] = rsqrtf(s[r] * invK + p.eps);   // 1 / sqrt
-
-  // ---- y = bf16(n w (1 + scale) + shift), in h's place
-  float amax[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) amax[r] = 0.f;
-  if (act) {
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int col = c0 + 8 * half;
-      float2 g[4], sh[4], il[4];
-      int cur = -1;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float4 v = *reinterpret_cast<const float4*>(p.inv_lam + col + 4 * j);
-        il[2 * j] = make_float2(v.x, v.y);
-        il[2 * j + 1] = make_float2(v.z, v.w);
-      }
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int row = min(row0 + r, M - 1);
-        const int mr = p.rows_per_mod > 0 ? row / p.rows_per_mod : 0;
-        if (mr != cur) {                                // uniform over the CTA
-          cur = mr;
-          uint4 w = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);   // ones
-          if (p.weight) w = *reinterpret_cast<const uint4*>(p.weight + col);
-          const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            g[i] = unpack2(ws[i]);
-            sh[i] = make_float2(0.f, 0.f);
-          }
-          if (p.scale) {
-            const uint4 q = *reinterpret_cast<const uint4*>(p.scale + (size_t)mr * p.mod_stride + col);
-            const uint32_t qs[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) g[i] = __fmul2_rn(g[i], __fadd2_rn(make_float2(1.f, 1.f), unpack2(qs[i])));
-          }
-          if (p.shift) {
-            const uint4 q = *reinterpret_cast<const uint4*>(p.shift + (size_t)mr * p.mod_stride + col);
-            const uint32_t qs[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sh[i] = unpack2(qs[i]);
-          }
-        }
-        const float2 m2 = make_float2(-mu[r], -mu[r]), s2 = make_float2(s[r], s[r]);
+    for (int c = 0; c < C; ++c)
+      if (q0 + c * 32 * W < nch) {                       // a chunk past K holds zeros, not values
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 n = __fmul2_rn(__fadd2_rn(unpack2(h[r][4 * half + i]), m2), s2);
-          const uint32_t y = pack2(__ffma2_rn(n, g[i], sh[i]));
-          h[r][4 * half + i] = y;
-          if (kFmt == kFmtInt8) {
-            const float2 v = __fmul2_rn(unpack2(y), il[i]);
-            amax[r] = dev::fmax3(amax[r], fabsf(v.x), fabsf(v.y));
+          const float2 d = __fadd2_rn(unpack2(h[c][i]), nmu2);
+          a2 = __ffma2_rn(d, d, a2);
+        }
+      }
+    const float rstd = rsqrtf(reduce_row<false>(a2.x + a2.y, slot + kWarps, W, w, 1 + rg) * invK + p.eps);
+    const float2 rstd2 = make_float2(rstd, rstd), off2 = make_float2(-mu * rstd, -mu * rstd);
+
+    float amax = 0.f;
+    for (int m = m0; m <= m1; ++m) {
+      if (m != loaded) {                                // uniform over the CTA
+        __syncthreads();
+        for (int q = threadIdx.x; q < nch; q += kThreads) {
+          uint4 u = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);   // ones
+          if (p.weight) u = *reinterpret_cast<const uint4*>(p.weight + 8 * q);
+          float2 g[4] = {unpack2(u.x), unpack2(u.y), unpack2(u.z), unpack2(u.w)}, s[4] = {};
+          if (p.scale) {
+            u = *reinterpret_cast<const uint4*>(p.scale + m * p.mod_stride + 8 * q);
+            const float2 e[4] = {unpack2(u.x), unpack2(u.y), unpack2(u.z), unpack2(u.w)};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) g[i] = __fmul2_rn(g[i], __fadd2_rn(make_float2(1.f, 1.f), e[i]));
+          }
+          if (p.shift) {
+            u = *reinterpret_cast<const uint4*>(p.shift + m * p.mod_stride + 8 * q);
+            s[0] = unpack2(u.x); s[1] = unpack2(u.y); s[2] = unpack2(u.z); s[3] = unpack2(u.w);
+          }
+          gain[q] = make_float4(g[0].x, g[0].y, g[1].x, g[1].y);
+          gain[q + nch] = make_float4(g[2].x, g[2].y, g[3].x, g[3].y);
+          shift[q] = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
+          shift[q + nch] = make_float4(s[2].x, s[2].y, s[3].x, s[3].y);
+        }
+        loaded = m;
+        __syncthreads();
+      }
+      if (m != mine) continue;
+      // ---- y = bf16(n w (1 + scale) + shift), and the 4-bit quantizers
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int q = q0 + c * 32 * W;
+        const bool act = q < nch;
+        float2 g[4], sh[4], il[4], v[4];
+        if (act) {
+          param8(gain, q, nch, g);
+          param8(shift, q, nch, sh);
+          param8(ilam, q, nch, il);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 n = __ffma2_rn(unpack2(h[c][i]), rstd2, off2);
+            h[c][i] = pack2(__ffma2_rn(n, g[i], sh[i]));
+            v[i] = __fmul2_rn(unpack2(h[c][i]), il[i]);
+          }
+          if (p.nmt > 0 && live)
+            *reinterpret_cast<uint4*>(ytile + rg * ystride + q * 16) =
+                make_uint4(h[c][0], h[c][1], h[c][2], h[c][3]);
+          if (p.y && live)
+            *reinterpret_cast<uint4*>(p.y + (size_t)row * K + 8 * q) = make_uint4(h[c][0], h[c][1], h[c][2], h[c][3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = make_float2(0.f, 0.f);
+        }
+        float a = fmaxf(fabsf(v[0].x), fabsf(v[0].y));
+#pragma unroll
+        for (int i = 1; i < 4; ++i) a = dev::fmax3(a, fabsf(v[i].x), fabsf(v[i].y));
+        if (kFmt == kFmtInt8) {
+          amax = fmaxf(amax, a);
+        } else if (kFmt == kFmtNvfp4) {
+          // a group of 16 is two lanes' chunks
+          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+          uint32_t codes = 0u;
+          const uint32_t sb = live ? dev::nvfp4_quant8(v, a, p.c_x, p.g_x_exp, rcp, codes) : 0u;
+          // four groups' scale bytes are one word of the layout
+          uint32_t word = sb << (8 * ((lane >> 1) & 3));
+          word |= __shfl_xor_sync(0xffffffffu, word, 2);
+          word |= __shfl_xor_sync(0xffffffffu, word, 4);
+          if (act) {
+            if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(p.scales + sf_offset(row, q >> 1, K)) = word;
+            *reinterpret_cast<uint32_t*>(p.codes + act_tile_offset(row, q >> 5, (q & 31) >> 2, p.nst) + (q & 3) * 4) =
+                codes;
+          }
+        } else {
+          // a group of 64 is eight lanes' chunks
+          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 4));
+          const __nv_bfloat16 sb = __float2bfloat16_rn(live ? __fmul_rn(a, 1.0f / 7.0f) : 0.f);
+          const float sc = __bfloat162float(sb);
+          uint32_t codes = 0u;
+          if (sc != 0.f) {
+            const float inv = __frcp_rn(sc);
+            const float2 i2 = make_float2(inv, inv);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              // the sum with 1.5 * 2^23 holds the rounded integer in its low
+              // bits; the product is rounded before (no fused multiply-add)
+              const float2 k = __fmul2_rn(v[i], i2);
+              codes |= (__float_as_uint(__fadd_rn(k.x, 12582912.0f)) & 0xFu) << (8 * i);
+              codes |= (__float_as_uint(__fadd_rn(k.y, 12582912.0f)) & 0xFu) << (8 * i + 4);
+            }
+          }
+          if (act) {
+            if ((lane & 7) == 0)
+              reinterpret_cast<uint16_t*>(p.scales)[(size_t)(q >> 3) * p.mpad + row] = __bfloat16_as_ushort(sb);
+            if (live) *reinterpret_cast<uint32_t*>(p.codes + (size_t)row * (K / 2) + q * 4) = codes;
           }
         }
-        if (p.nmt > 0)
-          *reinterpret_cast<uint4*>(ytile + r * ystride + col * 2) =
-              make_uint4(h[r][4 * half], h[r][4 * half + 1], h[r][4 * half + 2], h[r][4 * half + 3]);
-        if (p.y && row0 + r < M)
-          *reinterpret_cast<uint4*>(p.y + (size_t)(row0 + r) * K + col) =
-              make_uint4(h[r][4 * half], h[r][4 * half + 1], h[r][4 * half + 2], h[r][4 * half + 3]);
       }
     }
-  }
-
-  // ---- the layer's quantizer (the arithmetic of k1_quant.cu)
-  if (kFmt == kFmtInt8) reduce_rows<R, true>(amax, part2, nwarps);
-  float2 il[8];
-  if (act) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float4 v = *reinterpret_cast<const float4*>(p.inv_lam + c0 + 4 * j);
-      il[2 * j] = make_float2(v.x, v.y);
-      il[2 * j + 1] = make_float2(v.z, v.w);
-    }
-  }
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int row = row0 + r;
-    const bool live = row < M;                          // rows M .. mpad - 1: zero codes and scales
-    float2 v[8];
-    if (act) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = __fmul2_rn(unpack2(h[r][i]), il[i]);
-    }
     if (kFmt == kFmtInt8) {
-      const float sc = live ? __fmul_rn(amax[r], 1.0f / 127.0f) : 0.f;
+      // one scale per token, from the whole row
+      amax = reduce_row<true>(amax, slot + 2 * kWarps, W, w, 1 + rg);
+      const float sc = live ? __fmul_rn(amax, 1.0f / 127.0f) : 0.f;
       const float inv = sc == 0.f ? 0.f : __frcp_rn(sc);
-      if (tid == 0) {
+      if (w == 0 && lane == 0) {
         float* sx = reinterpret_cast<float*>(p.scales);
         sx[row] = sc;
         sx[p.mpad + row] = inv;
       }
-      if (act) {
-        const float2 i2 = make_float2(inv, inv);
-        uint32_t w8[4];
+      const float2 i2 = make_float2(inv, inv);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 q0 = __fmul2_rn(v[2 * j], i2), q1 = __fmul2_rn(v[2 * j + 1], i2);
-          const int c[4] = {max(-127, min(127, __float2int_rn(q0.x))), max(-127, min(127, __float2int_rn(q0.y))),
-                            max(-127, min(127, __float2int_rn(q1.x))), max(-127, min(127, __float2int_rn(q1.y)))};
-          w8[j] = (uint32_t)(c[0] & 0xFF) | ((uint32_t)(c[1] & 0xFF) << 8) | ((uint32_t)(c[2] & 0xFF) << 16) |
-                  ((uint32_t)(c[3] & 0xFF) << 24);
-        }
-        *reinterpret_cast<uint4*>(p.codes + act_tile_offset(row, c0 >> 7, (c0 & 127) >> 4, p.nst)) =
-            make_uint4(w8[0], w8[1], w8[2], w8[3]);
-      }
-    } else if (kFmt == kFmtNvfp4) {
-      uint32_t packed[2] = {0u, 0u}, sb = 0u;
-      if (act && live) sb = dev::nvfp4_quant16(v, p.c_x, p.g_x_exp, rcp, packed);
-      // four neighbouring groups' scale bytes are one 32-bit word of the layout
-      uint32_t word = sb << (8 * (tid & 3));
-      word |= __shfl_xor_sync(0xffffffffu, word, 1);
-      word |= __shfl_xor_sync(0xffffffffu, word, 2);
-      if (act) {
-        if ((tid & 3) == 0) *reinterpret_cast<uint32_t*>(p.scales + sf_offset(row, tid, K)) = word;
-        *reinterpret_cast<uint2*>(p.codes + act_tile_offset(row, c0 >> 8, (c0 & 255) >> 5, p.nst) + (tid & 1) * 8) =
-            make_uint2(packed[0], packed[1]);
-      }
-    } else {
-      // INT4: a group of 64 is four neighbouring threads
-      float a = 0.f;
-      if (act) {
+      for (int c = 0; c < C; ++c) {
+        const int q = q0 + c * 32 * W;
+        if (q < nch) {
+          float2 il[4];
+          param8(ilam, q, nch, il);
+          uint32_t t[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) a = dev::fmax3(a, fabsf(v[i].x), fabsf(v[i].y));
-      }
-      a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-      a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-      const __nv_bfloat16 sb = __float2bfloat16_rn(live ? __fmul_rn(a, 1.0f / 7.0f) : 0.f);
-      const float sc = __bfloat162float(sb);
-      if (act) {
-        uint32_t packed[2] = {0u, 0u};
-        if (sc != 0.f) {
-          const float inv = __frcp_rn(sc);
-          const float2 i2 = make_float2(inv, inv);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t t = 0u;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              // the sum with 1.5 * 2^23 holds the rounded integer in its low
-              // bits; the product is rounded before (no fused multiply-add)
-              const float2 q = __fmul2_rn(v[4 * j + e], i2);
-              t |= (__float_as_uint(__fadd_rn(q.x, 12582912.0f)) & 0xFu) << (8 * e);
-              t |= (__float_as_uint(__fadd_rn(q.y, 12582912.0f)) & 0xFu) << (8 * e + 4);
-            }
-            packed[j] = t;
+          for (int i = 0; i < 4; ++i) {
+            // the sum with 1.5 * 2^23 holds the rounded integer, two's
+            // complement, in its low byte (|q| <= 127 (1 + 2^-22): no clamp)
+            const float2 k = __fmul2_rn(__fmul2_rn(unpack2(h[c][i]), il[i]), i2);
+            t[2 * i] = __float_as_uint(__fadd_rn(k.x, 12582912.0f));
+            t[2 * i + 1] = __float_as_uint(__fadd_rn(k.y, 12582912.0f));
           }
+          uint2 o;
+          o.x = __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
+          o.y = __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410);
+          if (sc == 0.f) o.x = o.y = 0u;
+          *reinterpret_cast<uint2*>(p.codes + act_tile_offset(row, q >> 4, (q & 15) >> 1, p.nst) + (q & 1) * 8) = o;
         }
-        if ((tid & 3) == 0)
-          reinterpret_cast<uint16_t*>(p.scales)[(size_t)(tid >> 2) * p.mpad + row] = __bfloat16_as_ushort(sb);
-        if (live)
-          *reinterpret_cast<uint2*>(p.codes + (size_t)row * (K / 2) + tid * 8) = make_uint2(packed[0], packed[1]);
       }
     }
-  }
-  if (p.nmt == 0) return;
+    if (p.nmt == 0 || tile * rows >= M) continue;       // uniform over the CTA
 
-  // ---- XL: 16 rank rows x 8 tokens per MMA, K split over the warps.  The order
-  // of k inside a block of 32 is free as long as both operands agree: lane
-  // (g, c) = (lane / 4, lane % 4) takes columns 8c .. 8c + 7 of the block, so
-  // each operand row is one 16-byte load and feeds two MMAs.
-  __syncthreads();                                      // the y tile is complete
-  const int warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-  float acc[4][4];
-#pragma unroll
-  for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[mt][i] = 0.f;
-  const uint8_t* yrow = ytile + g * ystride + c * 16;
-#pragma unroll 2
-  for (int kb = warp; kb < K / 32; kb += nwarps) {
-    uint4 b = make_uint4(0u, 0u, 0u, 0u);
-    if (g < R) b = *reinterpret_cast<const uint4*>(yrow + kb * 64);
+    // ---- XL: 16 rank rows x 8 tokens per MMA, K split over the warps.  The
+    // order of k inside a block of 32 is free as long as both operands agree:
+    // lane (g, c) = (lane / 4, lane % 4) takes columns 8c .. 8c + 7 of the
+    // block, so each operand row is one 16-byte load and feeds two MMAs.
+    __syncthreads();                                    // the y tile is complete
+    const int g = lane >> 2, c = lane & 3;
+    float acc[4][4];
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
-      if (mt < p.nmt) {
-        const __nv_bfloat16* a = p.amat[mt] + (size_t)g * K + kb * 32 + c * 8;
-        const uint4 lo = *reinterpret_cast<const uint4*>(a);
-        const uint4 hi = *reinterpret_cast<const uint4*>(a + 8 * (size_t)K);
-        mma_16816(acc[mt], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
-        mma_16816(acc[mt], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
-      }
-  }
-  __syncthreads();                                      // the y tile has been read: the partials take its place
-  float* red = reinterpret_cast<float*>(ytile);         // [warp][nmt * 16][8]
 #pragma unroll
-  for (int mt = 0; mt < 4; ++mt)
-    if (mt < p.nmt) {
-      float* o = red + ((size_t)(warp * p.nmt + mt) * 16 + g) * 8 + 2 * c;
-      *reinterpret_cast<float2*>(o) = make_float2(acc[mt][0], acc[mt][1]);
-      *reinterpret_cast<float2*>(o + 64) = make_float2(acc[mt][2], acc[mt][3]);
+      for (int i = 0; i < 4; ++i) acc[mt][i] = 0.f;
+    const uint8_t* yrow = ytile + g * ystride + c * 16;
+#pragma unroll 4
+    for (int kb = warp; kb < K / 32; kb += kWarps) {
+      uint4 b = make_uint4(0u, 0u, 0u, 0u);
+      if (g < rows) b = *reinterpret_cast<const uint4*>(yrow + kb * 64);
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+        if (mt < p.nmt) {
+          const __nv_bfloat16* a = p.amat[mt] + (size_t)g * K + kb * 32 + c * 8;
+          const uint4 lo = *reinterpret_cast<const uint4*>(a);
+          const uint4 hi = *reinterpret_cast<const uint4*>(a + 8 * (size_t)K);
+          mma_16816(acc[mt], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
+          mma_16816(acc[mt], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
+        }
     }
-  __syncthreads();
-  for (int i = tid; i < p.nmt * 16 * R; i += blockDim.x) {
-    const int j = i % (p.nmt * 16), r = i / (p.nmt * 16);   // rank row, token
-    if (row0 + r < M) {
-      float t = 0.f;
-      for (int w = 0; w < nwarps; ++w) t += red[((size_t)w * p.nmt * 16 + j) * 8 + r];
-      p.xl[(size_t)(row0 + r) * p.xl_stride + p.xl_col[j >> 4] + (j & 15)] = __float2bfloat16_rn(t);
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+      if (mt < p.nmt) {                                 // partials [warp][nmt 16][8]
+        float* o = red + ((size_t)(warp * p.nmt + mt) * 16 + g) * 8 + 2 * c;
+        *reinterpret_cast<float2*>(o) = make_float2(acc[mt][0], acc[mt][1]);
+        *reinterpret_cast<float2*>(o + 64) = make_float2(acc[mt][2], acc[mt][3]);
+      }
+    __syncthreads();                                    // ... and the y tile has been read
+    for (int i = threadIdx.x; i < p.nmt * 16 * rows; i += kThreads) {
+      const int j = i % (p.nmt * 16), r = tile * rows + i / (p.nmt * 16);   // rank row, token
+      if (r < M) {
+        float t = 0.f;
+#pragma unroll
+        for (int u = 0; u < kWarps; ++u) t += red[((size_t)u * p.nmt * 16 + j) * 8 + i / (p.nmt * 16)];
+        p.xl[(size_t)r * p.xl_stride + p.xl_col[j >> 4] + (j & 15)] = __float2bfloat16_rn(t);
+      }
+    }
+    if (p.xl_zero > 0 && threadIdx.x < 16 * rows) {
+      const int r = tile * rows + (threadIdx.x >> 4);
+      if (r < M) p.xl[(size_t)r * p.xl_stride + p.xl_zero + (threadIdx.x & 15)] = __float2bfloat16_rn(0.f);
     }
   }
-  if (p.xl_zero > 0)
-    for (int i = tid; i < 16 * R; i += blockDim.x)
-      if (row0 + (i >> 4) < M) p.xl[(size_t)(row0 + (i >> 4)) * p.xl_stride + p.xl_zero + (i & 15)] = __float2bfloat16_rn(0.f);
 }
 
-size_t smem_bytes(int R, const NormParams& p, int threads) {
-  const size_t nwarps = threads / 32, head = head_bytes(R, (int)nwarps);
-  const size_t tile = (size_t)R * (2 * (size_t)p.K + 64), red = nwarps * p.nmt * 16 * 8 * 4;
-  return head + (p.nmt > 0 ? (tile > red ? tile : red) : 0);
+size_t smem_bytes(int K, int nmt, int W) {
+  const size_t head = (2 * 3 * kWarps + 16) * 4, params = (size_t)K * 12;
+  const size_t tile = (size_t)(kWarps / W) * (2 * (size_t)K + 64), red = (size_t)kWarps * nmt * 16 * 8 * 4;
+  return head + params + (nmt > 0 ? tile + red : 0);
 }
 
-template <int R, int kFmt>
-cudaError_t launch(const NormParams& p, int threads, cudaStream_t stream) {
-  const size_t smem = smem_bytes(R, p, threads);
-  auto kern = norm_quant_kernel<R, kFmt>;
+template <int kFmt, int C>
+cudaError_t launch(const NormParams& p, int num_sms, cudaStream_t stream) {
+  const size_t smem = smem_bytes(p.K, p.nmt, p.warps_per_row);
+  if (smem > kNormMaxSmem) return cudaErrorInvalidValue;
+  auto kern = norm_quant_kernel<kFmt, C>;
   static thread_local int configured_device = -1;
   int dev = 0;
   cudaGetDevice(&dev);
   if (configured_device != dev) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormMaxSmem);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNormMaxSmem);
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
+  // persistent: as many CTAs as an SM holds, each a contiguous range of tiles
+  const int rows = kWarps / p.warps_per_row, tiles = (p.mpad + rows - 1) / rows;
+  const int per_sm = smem * 2 + 4096 <= kNormMaxSmem ? 2 : 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.mpad / R));
-  cfg.blockDim = dim3((unsigned)threads);
+  cfg.gridDim = dim3((unsigned)(tiles < per_sm * num_sms ? tiles : per_sm * num_sms));
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -402,22 +394,30 @@ cudaError_t launch(const NormParams& p, int threads, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-template <int R>
-cudaError_t launch_fmt(const NormParams& p, int fmt, int threads, cudaStream_t stream) {
-  if (fmt == kFmtNvfp4) return launch<R, kFmtNvfp4>(p, threads, stream);
-  if (fmt == kFmtInt4) return launch<R, kFmtInt4>(p, threads, stream);
-  return launch<R, kFmtInt8>(p, threads, stream);
+template <int kFmt>
+cudaError_t launch_fmt(const NormParams& p, int num_sms, cudaStream_t stream) {
+  const int chunks = (p.K / 8 + 32 * p.warps_per_row - 1) / (32 * p.warps_per_row);   // of a lane
+  if (chunks <= 1) return launch<kFmt, 1>(p, num_sms, stream);
+  if (chunks <= 2) return launch<kFmt, 2>(p, num_sms, stream);
+  if (chunks <= 4) return launch<kFmt, 4>(p, num_sms, stream);
+  if (chunks <= 6) return launch<kFmt, 6>(p, num_sms, stream);
+  if (chunks <= 8) return launch<kFmt, 8>(p, num_sms, stream);
+  return launch<kFmt, 12>(p, num_sms, stream);
 }
 
 }  // namespace
 
 bool norm_supported(int K) { return K <= kNormMaxK; }
 
-cudaError_t launch_norm_quant(const NormParams& p, int fmt, int num_sms, cudaStream_t stream) {
-  const int threads = (p.K / kCols + 31) / 32 * 32;
-  const bool wide = threads <= 512 && smem_bytes(4, p, threads) <= kNormMaxSmem;
-  if (wide && p.M >= 4 * num_sms) return launch_fmt<4>(p, fmt, threads, stream);
-  return launch_fmt<2>(p, fmt, threads, stream);
+cudaError_t launch_norm_quant(NormParams p, int fmt, int num_sms, cudaStream_t stream) {
+  // a lane holds at most 12 chunks of a row; with few rows, more warps to a row
+  int W = 1;
+  while (W < kWarps && p.K > 12 * 256 * W) W *= 2;
+  while (W < kWarps && (p.M + kWarps / W - 1) / (kWarps / W) < num_sms) W *= 2;
+  p.warps_per_row = W;
+  if (fmt == kFmtNvfp4) return launch_fmt<kFmtNvfp4>(p, num_sms, stream);
+  if (fmt == kFmtInt4) return launch_fmt<kFmtInt4>(p, num_sms, stream);
+  return launch_fmt<kFmtInt8>(p, num_sms, stream);
 }
 
 }  // namespace svdq
