@@ -561,6 +561,41 @@ svdq_status svdq_qkv_forward(const svdq_layer* layer, const svdq_norm* norm, con
                              const void* k_weight, const float* positions, int64_t pos_batch, void* Y,
                              void* workspace, size_t workspace_bytes, void* stream, unsigned flags);
 
+/* The residual of a layer's output: Y = bf16(residual + gate * y), where y is
+ * the layer's FP32 output with bias and activation (rounded only here).  Device
+ * memory of the layer's device, BF16, 16-byte aligned.
+ *   residual   [M][N]; may be Y itself (in place), but not overlap it otherwise.
+ *   gate       rows of N values, gate_stride elements apart (a multiple of 8),
+ *              or NULL (1); token m uses row m / rows_per_gate, or row 0 when
+ *              rows_per_gate is 0. */
+typedef struct {
+  const void* residual;
+  const void* gate;
+  int64_t gate_stride;
+  int rows_per_gate;
+} svdq_residual;
+
+/* svdq_gemm, svdq_linear_forward with a residual in the GEMM's epilogue (same
+ * kernels otherwise; SVDQ_NVFP4, SVDQ_INT4, SVDQ_W8A8_INT8).  res is read during
+ * the call only.  flags: SVDQ_FWD_GELU, SVDQ_FWD_CHECK, and SVDQ_FWD_NO_BRANCH
+ * for svdq_gemm_residual (others: SVDQ_EUNSUPPORTED).  Y must not overlap X.
+ * Always the single-CTA GEMM, whatever SVDQ_K2_KERNEL says. */
+svdq_status svdq_gemm_residual(const svdq_layer* layer, const void* codes, const void* scales, const void* xl, int M,
+                               const svdq_residual* res, void* Y, void* stream, unsigned flags);
+svdq_status svdq_linear_forward_residual(const svdq_layer* layer, const void* X, int M, const svdq_residual* res,
+                                         void* Y, void* workspace, size_t workspace_bytes, void* stream,
+                                         unsigned flags);
+
+/* svdq_mlp_block_forward -- the MLP of a transformer block through the chain:
+ * [svdq_norm] -> fc1 -> [GELU] -> fc2 -> [residual].  svdq_mlp_forward with a
+ * normalisation in front (norm, or NULL) and a residual behind (res, or NULL).
+ * X, the norm's sum and Y may be the residual stream itself: res->residual may
+ * be X, the sum and Y.  Layers and workspace as for svdq_mlp_forward; flags:
+ * SVDQ_FWD_GELU, SVDQ_FWD_CHECK. */
+svdq_status svdq_mlp_block_forward(const svdq_layer* fc1, const svdq_layer* fc2, const svdq_norm* norm, const void* X,
+                                   int M, const svdq_residual* res, void* Y, void* workspace, size_t workspace_bytes,
+                                   void* stream, unsigned flags);
+
 #ifdef __cplusplus
 }
 #endif

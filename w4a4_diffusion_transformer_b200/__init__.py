@@ -53,6 +53,7 @@ EXPORTED = [
     "svdq_selftest_wait_timeout", "svdq_mlp_workspace_bytes", "svdq_mlp_fc1", "svdq_mlp_forward",
     "svdq_set_lora", "svdq_serialized_bytes", "svdq_serialize", "svdq_deserialize",
     "svdq_norm_quantize_act", "svdq_norm_linear_forward", "svdq_rope_heads", "svdq_qkv_forward",
+    "svdq_gemm_residual", "svdq_linear_forward_residual", "svdq_mlp_block_forward",
 ]
 STATIC_WORKSPACE_BYTES = 16 << 20   # SVDQ_STATIC_WORKSPACE_BYTES
 
@@ -78,6 +79,11 @@ class NormStruct(ctypes.Structure):
     _fields_ = [("residual", ctypes.c_void_p), ("sum", ctypes.c_void_p), ("weight", ctypes.c_void_p),
                 ("scale", ctypes.c_void_p), ("shift", ctypes.c_void_p), ("mod_stride", ctypes.c_int64),
                 ("rows_per_mod", ctypes.c_int), ("eps", ctypes.c_float), ("flags", ctypes.c_uint)]
+
+
+class ResidualStruct(ctypes.Structure):
+    _fields_ = [("residual", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("gate_stride", ctypes.c_int64),
+                ("rows_per_gate", ctypes.c_int)]
 
 
 class RopeStruct(ctypes.Structure):
@@ -132,6 +138,9 @@ def load() -> ctypes.CDLL:
         "svdq_deserialize": (I, [P, SZ, I, ctypes.POINTER(P)]),
         "svdq_norm_quantize_act": (I, [P, P, P, I, P, P, P, P, P]),
         "svdq_norm_linear_forward": (I, [P, P, P, I, P, P, SZ, P, U]),
+        "svdq_gemm_residual": (I, [P, P, P, P, I, P, P, P, U]),
+        "svdq_linear_forward_residual": (I, [P, P, I, P, P, P, SZ, P, U]),
+        "svdq_mlp_block_forward": (I, [P, P, P, P, I, P, P, P, SZ, P, U]),
         "svdq_rope_heads": (I, [P, P, P, I, I, P, ctypes.c_int64, P]),
         "svdq_qkv_forward": (I, [P, P, P, I, I, P, I, I, P, P, P, ctypes.c_int64, P, P, SZ, P, U]),
     }
@@ -273,6 +282,27 @@ class Norm:
             _need(weight, K * 2, "weight")
         for r in self._rows:
             r.need(M, K, self._per)
+
+
+class Residual:
+    """A residual in a GEMM's epilogue (svdq_residual): Y = residual + gate * y,
+    token m gated by row m // rows_per_gate (0: row 0; no gate: 1).  Holds
+    references to its tensors; one object can be used for any number of calls."""
+
+    def __init__(self, residual, gate=None, rows_per_gate: int = 0, gate_stride: Optional[int] = None):
+        if _is_tensor(residual):
+            _bf16_tensor(residual, "residual")
+        self._keep = (residual, gate)
+        self._rows = None if gate is None else _Rows(gate, "gate", gate_stride)
+        self._per = int(rows_per_gate)
+        stride = 0 if self._rows is None or self._rows.rows == 1 else self._rows.stride or 0
+        self._c = ResidualStruct(_ptr(residual), _ptr(gate), int(stride), self._per)
+        self._ref = ctypes.addressof(self._c)
+
+    def _need(self, M: int, N: int):
+        _need(self._keep[0], M * N * 2, "residual")
+        if self._rows is not None:
+            self._rows.need(M, N, self._per)
 
 
 class Rope:
@@ -557,6 +587,25 @@ class Layer:
                                        _ptr(Y), _ptr(workspace), workspace_bytes, _stream(stream), flags),
                "svdq_qkv_forward")
 
+    def gemm_residual(self, codes, scales, xl, M: int, residual: Residual, Y, stream=None, flags: int = 0):
+        """The second kernel with a residual in its epilogue (svdq_gemm_residual)."""
+        self._need_act(M, Y=Y, codes=codes, scales=scales, xl=xl)
+        if M > 0:
+            residual._need(M, self._N)
+        _check(load().svdq_gemm_residual(self._h, _ptr(codes), _ptr(scales), _ptr(xl), M, residual._ref, _ptr(Y),
+                                         _stream(stream), flags), "svdq_gemm_residual")
+
+    def forward_residual(self, X, M: int, residual: Residual, Y, workspace, workspace_bytes: int, stream=None,
+                         flags: int = 0):
+        """Forward with a residual in the GEMM's epilogue (svdq_linear_forward_residual)."""
+        self._need_act(M, X=X, Y=Y)
+        if M > 0:
+            residual._need(M, self._N)
+        _need(workspace, workspace_bytes, "workspace")
+        _check(load().svdq_linear_forward_residual(self._h, _ptr(X), M, residual._ref, _ptr(Y), _ptr(workspace),
+                                                   workspace_bytes, _stream(stream), flags),
+               "svdq_linear_forward_residual")
+
     def act_scales_to_logical(self, device_layout: np.ndarray, M: int) -> np.ndarray:
         """NVFP4: uint8 [M][K/16] E4M3 bytes; INT4: uint16 [M][K/64] BF16 bits;
         W8A8: float32 [M] (one scale per token)."""
@@ -608,3 +657,19 @@ def mlp_forward(fc1: Layer, fc2: Layer, X, M: int, Y, workspace, workspace_bytes
     _need(workspace, workspace_bytes, "workspace")
     _check(load().svdq_mlp_forward(fc1._h, fc2._h, _ptr(X), M, _ptr(Y), _ptr(workspace), workspace_bytes,
                                    _stream(stream), flags), "svdq_mlp_forward")
+
+
+def mlp_block_forward(fc1: Layer, fc2: Layer, norm: Optional[Norm], X, M: int, residual: Optional[Residual], Y,
+                      workspace, workspace_bytes: int, stream=None, flags: int = 0):
+    """[norm ->] fc1 -> [GELU] -> fc2 [-> residual] (svdq_mlp_block_forward)."""
+    fc1._need_act(M, X=X)
+    fc2._need_act(M, Y=Y)
+    if M > 0:
+        if norm is not None:
+            norm._need(M, fc1._K)
+        if residual is not None:
+            residual._need(M, fc2._N)
+    _need(workspace, workspace_bytes, "workspace")
+    _check(load().svdq_mlp_block_forward(fc1._h, fc2._h, None if norm is None else norm._ref, _ptr(X), M,
+                                         None if residual is None else residual._ref, _ptr(Y), _ptr(workspace),
+                                         workspace_bytes, _stream(stream), flags), "svdq_mlp_block_forward")

@@ -129,6 +129,12 @@ struct DeviceGuard {
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 
+// The residual epilogue of a GEMM call: none when residual is null.
+struct Epilogue {
+  const void* residual = nullptr;
+  ResidualParams gate = {};
+};
+
 // Formats with quantized activations (the two-kernel forward): NVFP4, INT4, W8A8.
 bool w4a4(const svdq_layer* L) {
   return L->host.format == SVDQ_NVFP4 || L->host.format == SVDQ_INT4 || L->host.format == SVDQ_W8A8_INT8;
@@ -391,10 +397,16 @@ svdq_status run_k1(const svdq_layer* L, const void* X, int M, void* codes, void*
   return launch_k1(tm_x, L->tm_l1t, tm_c, p, fmt, mode, stream) == cudaSuccess ? SVDQ_OK : SVDQ_ECUDA;
 }
 
+// The output map of a GEMM, and of the residual it adds.
+bool make_out_map(CUtensorMap* m, const void* base, int M, int N) {
+  return make_map(m, base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, N, M, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
 svdq_status run_k2_int8(const svdq_layer* L, const void* codes, const void* scales, const void* xl, int M, void* Y,
-                        cudaStream_t stream, bool branch, bool gelu) {
+                        cudaStream_t stream, bool branch, bool gelu, const Epilogue& epi) {
   const HostPrep& h = L->host;
-  CUtensorMap tm_xl, tm_y;
+  CUtensorMap tm_xl, tm_y, tm_r;
+  if (epi.residual && !make_out_map(&tm_r, epi.residual, M, h.N)) return SVDQ_ECUDA;
   if (!make_map(&tm_y, Y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, h.N, M, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
     return SVDQ_ECUDA;
   if (branch) {
@@ -418,7 +430,10 @@ svdq_status run_k2_int8(const svdq_layer* L, const void* codes, const void* scal
   p.budget_ns = L->budget_ns;
   p.branch = branch ? 1 : 0;
   p.gelu = gelu ? 1 : 0;
-  return launch_k2_int8(tm_xl, L->tm_l2s, tm_y, p, L->num_sms, stream) == cudaSuccess ? SVDQ_OK : SVDQ_ECUDA;
+  p.res = epi.gate;
+  return launch_k2_int8(tm_xl, L->tm_l2s, tm_y, epi.residual ? &tm_r : nullptr, p, L->num_sms, stream) == cudaSuccess
+             ? SVDQ_OK
+             : SVDQ_ECUDA;
 }
 
 // The LoRA adapter's down pass: XL columns 32..63 = bf16(X A), the first
@@ -453,10 +468,11 @@ svdq_status run_upproj(const svdq_layer* L, const void* xl, int xlw, int width, 
 }
 
 svdq_status run_k2_int4(const svdq_layer* L, const void* codes, const void* scales, const void* xl, int M,
-                        void* Y, cudaStream_t stream, bool branch, bool gelu, bool lora_on) {
+                        void* Y, cudaStream_t stream, bool branch, bool gelu, bool lora_on, const Epilogue& epi) {
   const HostPrep& h = L->host;
   const bool lora = h.lora_r > 0 && lora_on;
-  CUtensorMap tm_a, tm_xl, tm_y, tm_xla;
+  CUtensorMap tm_a, tm_xl, tm_y, tm_xla, tm_r;
+  if (epi.residual && !make_out_map(&tm_r, epi.residual, M, h.N)) return SVDQ_ECUDA;
   if (!make_map(&tm_a, codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, h.K / 2, M, 32, 128, CU_TENSOR_MAP_SWIZZLE_NONE))
     return SVDQ_ECUDA;
   if (!make_map(&tm_y, Y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, h.N, M, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
@@ -493,11 +509,13 @@ svdq_status run_k2_int4(const svdq_layer* L, const void* codes, const void* scal
   p.branch = branch ? 1 : 0;
   p.gelu = gelu ? 1 : 0;
   p.lora = lora ? 1 : 0;
+  p.res = epi.gate;
+  // the residual epilogue is the single-CTA kernel's
   const cudaError_t e =
-      L->k2_kernel == 2 && !lora
+      L->k2_kernel == 2 && !lora && !epi.residual
           ? launch_k2_int4_pair(tm_a, L->tm_wq_pair, tm_xl, L->tm_l2s_pair, tm_y, p, L->num_sms, stream)
-          : launch_k2_int4(tm_a, L->tm_wq, tm_xl, L->tm_l2s, tm_y, tm_xla, lora ? L->tm_lora_l2s : L->tm_l2s, p,
-                           L->num_sms, stream);
+          : launch_k2_int4(tm_a, L->tm_wq, tm_xl, L->tm_l2s, tm_y, tm_xla, lora ? L->tm_lora_l2s : L->tm_l2s,
+                           epi.residual ? &tm_r : nullptr, p, L->num_sms, stream);
   return e == cudaSuccess ? SVDQ_OK : SVDQ_ECUDA;
 }
 
@@ -505,12 +523,13 @@ svdq_status run_k2_int4(const svdq_layer* L, const void* codes, const void* scal
 // XL_lora (s B) in its own ring stage, the INT4 GEMM by reloading its branch
 // buffer within the tile; either way into the same accumulator.
 svdq_status run_k2(const svdq_layer* L, const void* codes, const void* scales, const void* xl, int M, void* Y,
-                   cudaStream_t stream, bool branch, bool gelu, bool lora_on = true) {
-  if (L->host.format == SVDQ_INT4) return run_k2_int4(L, codes, scales, xl, M, Y, stream, branch, gelu, lora_on);
-  if (w8a8(L->host)) return run_k2_int8(L, codes, scales, xl, M, Y, stream, branch, gelu);
+                   cudaStream_t stream, bool branch, bool gelu, bool lora_on = true, const Epilogue& epi = {}) {
+  if (L->host.format == SVDQ_INT4) return run_k2_int4(L, codes, scales, xl, M, Y, stream, branch, gelu, lora_on, epi);
+  if (w8a8(L->host)) return run_k2_int8(L, codes, scales, xl, M, Y, stream, branch, gelu, epi);
   const HostPrep& h = L->host;
   const bool lora = h.lora_r > 0 && lora_on;
-  CUtensorMap tm_xl, tm_y, tm_xla;
+  CUtensorMap tm_xl, tm_y, tm_xla, tm_r;
+  if (epi.residual && !make_out_map(&tm_r, epi.residual, M, h.N)) return SVDQ_ECUDA;
   if (!make_map(&tm_y, Y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, h.N, M, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
     return SVDQ_ECUDA;
   const uint64_t xl_row = (uint64_t)xl_width(h) * 2;
@@ -548,10 +567,12 @@ svdq_status run_k2(const svdq_layer* L, const void* codes, const void* scales, c
   p.lora = lora ? 1 : 0;
   // The CTA-pair kernel (256 x 256 tiles) is exact but measured slower than the
   // single-CTA kernel on this part; it runs only when SVDQ_K2_KERNEL=pair, and
-  // only for layers without a LoRA adapter.
-  const bool pair = L->k2_kernel == 2 && !lora;
+  // only for layers without a LoRA adapter and calls without a residual.
+  p.res = epi.gate;
+  const bool pair = L->k2_kernel == 2 && !lora && !epi.residual;
   const cudaError_t e = pair ? launch_k2_pair(tm_xl, L->tm_l2s_pair, tm_y, p, L->num_sms, stream)
-                             : launch_k2(tm_xl, L->tm_l2s, tm_y, tm_xla, L->tm_lora_l2s, p, L->num_sms, stream);
+                             : launch_k2(tm_xl, L->tm_l2s, tm_y, tm_xla, L->tm_lora_l2s,
+                                         epi.residual ? &tm_r : nullptr, p, L->num_sms, stream);
   return e == cudaSuccess ? SVDQ_OK : SVDQ_ECUDA;
 }
 
@@ -679,10 +700,14 @@ ChainLayout chain_layout(const svdq_layer* L1, const svdq_layer* L2, int M, bool
   return c;
 }
 
-// fc1's first kernel, then its GEMM in chain mode (fc2's codes, scales and
+svdq_status run_norm(const svdq_layer* L, const svdq_norm* n, const void* X, int M, void* codes, void* scales,
+                     void* xl, void* y, cudaStream_t stream);
+
+// fc1's first kernel (or its normalising form), then its GEMM in chain mode (fc2's codes, scales and
 // down-projection partials), then the fixed-order sum of the partials into XL2.
 svdq_status run_chain_fc1(const svdq_layer* L1, const svdq_layer* L2, const void* X, int M, void* codes2,
-                          void* scales2, void* xl2, void* partials, int S, uint8_t* ws1, cudaStream_t s, bool gelu) {
+                          void* scales2, void* xl2, void* partials, int S, uint8_t* ws1, cudaStream_t s, bool gelu,
+                          const svdq_norm* norm = nullptr) {
   const HostPrep& h1 = L1->host;
   const HostPrep& h2 = L2->host;
   const WsLayout w = ws_layout(h1, M);
@@ -690,7 +715,8 @@ svdq_status run_chain_fc1(const svdq_layer* L1, const svdq_layer* L2, const void
   void* scales1 = ws1 + w.scales;
   void* xl1 = ws1 + w.xl;
   const bool branch1 = h1.rank > 0, branch2 = h2.rank > 0;
-  svdq_status st = run_k1(L1, X, M, codes1, scales1, xl1, s, branch1 ? 0 : 1);
+  svdq_status st = norm ? run_norm(L1, norm, X, M, codes1, scales1, xl1, nullptr, s)
+                        : run_k1(L1, X, M, codes1, scales1, xl1, s, branch1 ? 0 : 1);
   if (st != SVDQ_OK) return st;
   CUtensorMap tm_xl;
   if (branch1) {
@@ -894,8 +920,39 @@ svdq_status run_rope(const svdq_rope* r, const svdq_heads* q, const svdq_heads* 
 
 // The second kernel (the adapter, if any, is added inside it).
 svdq_status run_gemm_stage(const svdq_layer* L, const void* codes, const void* scales, const void* xl, int M,
-                           void* Y, cudaStream_t s, bool branch, bool gelu, bool lora_on) {
-  return run_k2(L, codes, scales, xl, M, Y, s, branch, gelu, lora_on);
+                           void* Y, cudaStream_t s, bool branch, bool gelu, bool lora_on, const Epilogue& epi = {}) {
+  return run_k2(L, codes, scales, xl, M, Y, s, branch, gelu, lora_on, epi);
+}
+
+svdq_status check_residual(const svdq_layer* L, const svdq_residual* r, int M, const void* Y, Epilogue* epi) {
+  if (!r || !r->residual || misaligned(r->residual) || misaligned(r->gate)) return SVDQ_EINVAL;
+  if (r->gate && (r->rows_per_gate < 0 || r->gate_stride < 0 || r->gate_stride % 8)) return SVDQ_EINVAL;
+  const size_t out = (size_t)M * L->host.N * 2;
+  if (r->residual != Y && overlap(r->residual, out, Y, out)) return SVDQ_EINVAL;
+  epi->residual = r->residual;
+  epi->gate.gate = static_cast<const __nv_bfloat16*>(r->gate);
+  epi->gate.gate_stride = r->gate_stride;
+  epi->gate.rows_per_gate = r->rows_per_gate;
+  return SVDQ_OK;
+}
+
+svdq_status gemm_call(const svdq_layer* L, const void* codes, const void* scales, const void* xl, int M, void* Y,
+                      void* stream, unsigned flags, const Epilogue& epi) {
+  if ((reinterpret_cast<uintptr_t>(scales) & 15) || (reinterpret_cast<uintptr_t>(xl) & 15)) return SVDQ_EINVAL;
+  svdq_status st = check_forward_args(L, codes, M, Y);
+  if (st != SVDQ_OK) return st;
+  if (!w4a4(L)) return SVDQ_EUNSUPPORTED;
+  if (!scales) return SVDQ_EINVAL;
+  const bool bare = (flags & SVDQ_FWD_NO_BRANCH) != 0;
+  const bool branch = L->host.rank > 0 && !bare;
+  const bool lora = L->host.lora_r > 0 && !bare;
+  if ((branch || lora) && !xl) return SVDQ_EINVAL;
+  DeviceGuard g(L->device);
+  if (!g.ok) return SVDQ_ECUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  st = run_gemm_stage(L, codes, scales, xl, M, Y, s, branch, (flags & SVDQ_FWD_GELU) != 0, lora, epi);
+  if (st == SVDQ_OK && (flags & SVDQ_FWD_CHECK)) st = svdq_check(L, stream);
+  return st;
 }
 
 }  // namespace
@@ -1123,21 +1180,7 @@ svdq_status svdq_quantize_act(const svdq_layer* L, const void* X, int M, void* c
 
 svdq_status svdq_gemm(const svdq_layer* L, const void* codes, const void* scales, const void* xl, int M, void* Y,
                       void* stream, unsigned flags) {
-  if ((reinterpret_cast<uintptr_t>(scales) & 15) || (reinterpret_cast<uintptr_t>(xl) & 15)) return SVDQ_EINVAL;
-  svdq_status st = check_forward_args(L, codes, M, Y);
-  if (st != SVDQ_OK) return st;
-  if (!w4a4(L)) return SVDQ_EUNSUPPORTED;
-  if (!scales) return SVDQ_EINVAL;
-  const bool bare = (flags & SVDQ_FWD_NO_BRANCH) != 0;
-  const bool branch = L->host.rank > 0 && !bare;
-  const bool lora = L->host.lora_r > 0 && !bare;
-  if ((branch || lora) && !xl) return SVDQ_EINVAL;
-  DeviceGuard g(L->device);
-  if (!g.ok) return SVDQ_ECUDA;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  st = run_gemm_stage(L, codes, scales, xl, M, Y, s, branch, (flags & SVDQ_FWD_GELU) != 0, lora);
-  if (st == SVDQ_OK && (flags & SVDQ_FWD_CHECK)) st = svdq_check(L, stream);
-  return st;
+  return gemm_call(L, codes, scales, xl, M, Y, stream, flags, {});
 }
 
 svdq_status svdq_linear_forward(const svdq_layer* L, const void* X, int M, void* Y, void* workspace,
@@ -1554,6 +1597,72 @@ svdq_status svdq_qkv_forward(const svdq_layer* L, const svdq_norm* norm, const v
   st = run_rope(rope, &h[0], k_heads ? &h[1] : nullptr, batch, T, positions, pos_batch, L->num_sms,
                 static_cast<cudaStream_t>(stream));
   if (st == SVDQ_OK && (flags & SVDQ_FWD_CHECK)) st = svdq_check(L, stream);
+  return st;
+}
+
+svdq_status svdq_gemm_residual(const svdq_layer* L, const void* codes, const void* scales, const void* xl, int M,
+                               const svdq_residual* res, void* Y, void* stream, unsigned flags) {
+  if (!L || !Y || M < 1) return SVDQ_EINVAL;
+  Epilogue epi;
+  const svdq_status st = check_residual(L, res, M, Y, &epi);
+  if (st != SVDQ_OK) return st;
+  if (flags & ~(SVDQ_FWD_GELU | SVDQ_FWD_CHECK | SVDQ_FWD_NO_BRANCH)) return SVDQ_EUNSUPPORTED;
+  return gemm_call(L, codes, scales, xl, M, Y, stream, flags, epi);
+}
+
+svdq_status svdq_linear_forward_residual(const svdq_layer* L, const void* X, int M, const svdq_residual* res, void* Y,
+                                         void* workspace, size_t workspace_bytes, void* stream, unsigned flags) {
+  if (!L || !X || !Y || M < 1) return SVDQ_EINVAL;
+  Epilogue epi;
+  svdq_status st = check_residual(L, res, M, Y, &epi);
+  if (st != SVDQ_OK) return st;
+  if (overlap(X, (size_t)M * L->host.K * 2, Y, (size_t)M * L->host.N * 2)) return SVDQ_EINVAL;
+  if (!w4a4(L) || (flags & ~(SVDQ_FWD_GELU | SVDQ_FWD_CHECK))) return SVDQ_EUNSUPPORTED;
+  st = check_forward_args(L, X, M, Y);
+  if (st != SVDQ_OK) return st;
+  const WsLayout w = ws_layout(L->host, M);
+  if (!workspace || workspace_bytes < w.total || (reinterpret_cast<uintptr_t>(workspace) & 255)) return SVDQ_EINVAL;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  st = svdq_quantize_act(L, X, M, ws + w.codes, ws + w.scales, ws + w.xl, stream, 0);
+  return st == SVDQ_OK ? gemm_call(L, ws + w.codes, ws + w.scales, ws + w.xl, M, Y, stream, flags, epi) : st;
+}
+
+svdq_status svdq_mlp_block_forward(const svdq_layer* fc1, const svdq_layer* fc2, const svdq_norm* norm, const void* X,
+                                   int M, const svdq_residual* res, void* Y, void* workspace, size_t workspace_bytes,
+                                   void* stream, unsigned flags) {
+  svdq_status st = check_forward_args(fc1, X, M, Y);
+  if (st == SVDQ_EINVAL) return st;
+  if (!fc2) return SVDQ_EINVAL;
+  Epilogue epi;
+  if (norm) {
+    const svdq_status sn = check_norm(fc1, norm, X, M);
+    if (sn != SVDQ_OK) return sn;
+  }
+  if (res) {
+    const svdq_status sr = check_residual(fc2, res, M, Y, &epi);
+    if (sr != SVDQ_OK) return sr;
+  }
+  // Y may be X, the norm's residual or its sum: only the first kernel touches
+  // those, and the last one writes Y after every kernel before it has ended
+  if (st != SVDQ_OK) return st;
+  if (fc2->device < 0) return SVDQ_ESTATE;
+  if (!chainable(fc1, fc2)) return SVDQ_EUNSUPPORTED;
+  if (flags & ~(SVDQ_FWD_GELU | SVDQ_FWD_CHECK)) return SVDQ_EUNSUPPORTED;
+  const ChainLayout c = chain_layout(fc1, fc2, M, false);
+  if (!workspace || workspace_bytes < c.total || (reinterpret_cast<uintptr_t>(workspace) & 255)) return SVDQ_EINVAL;
+  DeviceGuard g(fc1->device);
+  if (!g.ok) return SVDQ_ECUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  st = run_chain_fc1(fc1, fc2, X, M, ws + c.codes2, ws + c.scales2, ws + c.xl2, ws + c.partials, c.S, ws, s,
+                     (flags & SVDQ_FWD_GELU) != 0, norm);
+  if (st == SVDQ_OK)
+    st = run_k2(fc2, ws + c.codes2, ws + c.scales2, ws + c.xl2, M, Y, s, fc2->host.rank > 0, false, true, epi);
+  if (st == SVDQ_OK && (flags & SVDQ_FWD_CHECK)) {
+    st = svdq_check(fc1, stream);
+    const svdq_status st2 = svdq_check(fc2, stream);
+    if (st == SVDQ_OK) st = st2;
+  }
   return st;
 }
 

@@ -44,6 +44,7 @@
 
 #include "kernels.h"
 #include "nvfp4_quant.cuh"
+#include "residual.cuh"
 #include "sm100.cuh"
 
 namespace svdq {
@@ -102,13 +103,18 @@ constexpr int kTmemCols = 512;
 constexpr int kSFCol0 = 256;
 constexpr int kSFStageCols = 12 * kKB;       // 4 columns of A + 8 of B per K block
 
-template <bool kChain>
+// Kernel modes: the layer, the chain's fc1, the layer with a residual epilogue.
+constexpr int kModeLayer = 0, kModeChain = 1, kModeResidual = 2;
+constexpr int kResBarBytes = kEpiWarps * 16;       // two load barriers per epilogue warp
+
+template <int kMode>
 struct K2Layout {
-  static constexpr bool deep = !kChain && SVDQ_K2_DEEP;
+  static constexpr bool deep = kMode == kModeLayer && SVDQ_K2_DEEP;
   static constexpr int stages = deep ? 4 : 3;
   static constexpr int br_bytes = deep ? 0 : kBrBytes;
   static constexpr int epi_warp_bytes = deep ? 512 : kEpiWarpBytes;   // deep: 128 bias floats only
-  static constexpr int smem = stages * kStageBytes + br_bytes + kEpiWarps * epi_warp_bytes + 1024 + 256;
+  static constexpr int smem = stages * kStageBytes + br_bytes + kEpiWarps * epi_warp_bytes + 1024 + 256 +
+                              (kMode == kModeResidual ? kResBarBytes : 0);
   static_assert(smem <= 232448, "shared memory per block");
   static_assert(kSFCol0 + stages * kSFStageCols <= kTmemCols, "TMEM budget");
 };
@@ -147,12 +153,13 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <bool kChain>
+template <int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
     k2_kernel(const __grid_constant__ CUtensorMap tm_xl, const __grid_constant__ CUtensorMap tm_l2,
               const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_xla,
-              const __grid_constant__ CUtensorMap tm_l2a, K2Params p) {
-  using Lay = K2Layout<kChain>;
+              const __grid_constant__ CUtensorMap tm_l2a, const __grid_constant__ CUtensorMap tm_r, K2Params p) {
+  using Lay = K2Layout<kMode>;
+  constexpr bool kChain = kMode == kModeChain, kRes = kMode == kModeResidual;
   constexpr int kStages = Lay::stages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -170,6 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* rcp_s = reinterpret_cast<float*>(tmem_slot + 4);   // chain mode: the quantizer's constants
+  uint64_t* res_bar = reinterpret_cast<uint64_t*>(epi_buf + kEpiWarps * Lay::epi_warp_bytes + 256);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -204,6 +212,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     dev::mbar_init(acc_full, 1);
     dev::mbar_init(acc_empty, kEpiWarps);
     dev::mbar_init(drain, 1);
+    if (kRes)
+      for (int i = 0; i < 2 * kEpiWarps; ++i) dev::mbar_init(&res_bar[i], 1);
     *abort_flag = 0;
     if (kChain) {
 #pragma unroll
@@ -451,6 +461,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!Lay::deep && lane == 0) dev::tma_prefetch_desc(&tm_y);
       int tcount = 0, chunk = 0;
       bool ok = true;
+      dev::ResidualLoads loads{&tm_r, res_bar + 2 * (warp - kEpiWarp0), wbuf, 0};
+      if (kRes) {
+        // the residual and the gate may come from the preceding kernel
+        dev::griddep_wait();
+        if (lane == 0 && blockIdx.x < ts.units()) {
+          for (int c = 0; c < 2; ++c)
+            loads.issue(ts.n0(blockIdx.x, 0) + half * 128 + c * 32, ts.m0(blockIdx.x) + q * 32);
+        }
+      }
       for (int u = blockIdx.x; u < ts.units() && ok; u += gridDim.x) {
         for (int t = ts.first(u); t < ts.last(u) && ok; ++t, ++tcount) {
           const int m0 = ts.m0(u);
@@ -514,16 +533,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();                                 // bias_s is restaged for the next tile
           } else {
+          const __nv_bfloat16* gate = kRes ? dev::gate_row(p.res, m0 + q * 32 + lane, M) : nullptr;
 #pragma unroll
           for (int c = 0; c < 4; ++c, ++chunk) {
             uint32_t (&cur)[32] = c == 0 ? va : c == 1 ? vb : c == 2 ? vc : vd;
-            // the buffer of this chunk was last read by the store issued two chunks ago
-            if (lane == 0) dev::bulk_wait_group_read<1>();
+            if (kRes) {
+              // the residual's chunk is in the buffer
+              const bool here = loads.wait(chunk, abort_flag, p.budget_ns);
+              if (!__all_sync(0xffffffffu, here)) {
+                if (lane == 0) record_error(p.err, abort_flag, 0x20B);
+                ok = false;
+                break;
+              }
+            } else if (lane == 0) {
+              // the buffer of this chunk was last read by the store issued two chunks ago
+              dev::bulk_wait_group_read<1>();
+            }
             __syncwarp();
             uint8_t* buf = wbuf + (chunk & 1) * kEpiBufBytes;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              uint32_t packed[4];
+              uint32_t packed[4], rs[4] = {}, gt[4] = {};
+              if (kRes) {
+                const uint4 r4 = *reinterpret_cast<const uint4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4));
+                const uint4 g4 = dev::gate8(gate, n0 + c * 32 + j * 8, N);
+                rs[0] = r4.x; rs[1] = r4.y; rs[2] = r4.z; rs[3] = r4.w;
+                gt[0] = g4.x; gt[1] = g4.y; gt[2] = g4.z; gt[3] = g4.w;
+              }
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const float2 b2 = reinterpret_cast<const float2*>(bias_s)[c * 16 + j * 4 + e];
@@ -533,8 +569,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                   y0 = dev::gelu_tanh(y0);
                   y1 = dev::gelu_tanh(y1);
                 }
-                const __nv_bfloat162 h2 = __floats2bfloat162_rn(y0, y1);
-                packed[e] = *reinterpret_cast<const uint32_t*>(&h2);
+                if (kRes) {
+                  packed[e] = dev::add_gated(rs[e], gt[e], y0, y1);
+                } else {
+                  const __nv_bfloat162 h2 = __floats2bfloat162_rn(y0, y1);
+                  packed[e] = *reinterpret_cast<const uint32_t*>(&h2);
+                }
               }
               // 64-byte swizzle: 16-byte chunk j of row `lane` sits at j ^ ((lane >> 1) & 3)
               *reinterpret_cast<uint4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
@@ -545,12 +585,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) {
               dev::tma_store_2d(&tm_y, buf, n0 + c * 32, m0 + q * 32);
               dev::bulk_commit_group();
+              if (kRes) {
+                // the chunk after next takes this buffer, once the store has read it
+                const int un = c < 2 ? u : u + (int)gridDim.x;
+                if (un < ts.units()) {
+                  dev::bulk_wait_group_read<0>();
+                  loads.issue(ts.n0(un, 0) + half * 128 + ((c + 2) & 3) * 32, ts.m0(un) + q * 32);
+                }
+              }
             }
           }
           __syncwarp();
           }
         }
       }
+      if (kRes && lane == 0) loads.drain(abort_flag, p.budget_ns);
       if (!Lay::deep && lane == 0) dev::bulk_wait_group_all();
     } else {
       // ---------------------------------------------- chain: fc2's input
@@ -776,29 +825,29 @@ void k2_pack_weights(const uint8_t* tiled_codes, const uint8_t* sf, int N, int K
 
 namespace {
 
-template <bool kChain>
+template <int kMode>
 cudaError_t configure_k2() {
   static thread_local int configured_device = -1;
   int dev = 0;
   cudaGetDevice(&dev);
   if (configured_device == dev) return cudaSuccess;
   cudaError_t e =
-      cudaFuncSetAttribute(k2_kernel<kChain>, cudaFuncAttributeMaxDynamicSharedMemorySize, K2Layout<kChain>::smem);
+      cudaFuncSetAttribute(k2_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, K2Layout<kMode>::smem);
   if (e != cudaSuccess) return e;
   // the warpgroups' register budgets add up to exactly 128 per thread
   cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, k2_kernel<kChain>);
+  e = cudaFuncGetAttributes(&fa, k2_kernel<kMode>);
   if (e != cudaSuccess) return e;
   if (fa.numRegs != 128) return cudaErrorInvalidConfiguration;
   configured_device = dev;
   return cudaSuccess;
 }
 
-template <bool kChain>
+template <int kMode>
 cudaError_t launch_k2_impl(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, const CUtensorMap& tm_y,
-                           const CUtensorMap& tm_xla, const CUtensorMap& tm_l2a, const K2Params& p, int grid,
-                           cudaStream_t stream) {
-  cudaError_t e = configure_k2<kChain>();
+                           const CUtensorMap& tm_xla, const CUtensorMap& tm_l2a, const CUtensorMap& tm_r,
+                           const K2Params& p, int grid, cudaStream_t stream) {
+  cudaError_t e = configure_k2<kMode>();
   if (e != cudaSuccess) return e;
   // Programmatic dependent launch: the prologue (barriers, TMEM, descriptor
   // prefetch, weight stream) overlaps the tail of the kernel that produces the
@@ -806,23 +855,25 @@ cudaError_t launch_k2_impl(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, c
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = K2Layout<kChain>::smem;
+  cfg.dynamicSmemBytes = K2Layout<kMode>::smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k2_kernel<kChain>, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, p);
+  return cudaLaunchKernelEx(&cfg, k2_kernel<kMode>, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, tm_r, p);
 }
 
 }  // namespace
 
 cudaError_t launch_k2(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, const CUtensorMap& tm_y,
-                      const CUtensorMap& tm_xla, const CUtensorMap& tm_l2a, const K2Params& p, int num_sms,
-                      cudaStream_t stream) {
+                      const CUtensorMap& tm_xla, const CUtensorMap& tm_l2a, const CUtensorMap* tm_r,
+                      const K2Params& p, int num_sms, cudaStream_t stream) {
   const int tiles = ((p.M + kBM - 1) / kBM) * ((p.N + kBN - 1) / kBN);
-  return launch_k2_impl<false>(tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, p, tiles < num_sms ? tiles : num_sms, stream);
+  const int grid = tiles < num_sms ? tiles : num_sms;
+  if (tm_r) return launch_k2_impl<kModeResidual>(tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, *tm_r, p, grid, stream);
+  return launch_k2_impl<kModeLayer>(tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, tm_y, p, grid, stream);
 }
 
 int k2_chain_splits(int M, int N, int num_sms) {
@@ -836,8 +887,8 @@ int k2_chain_splits(int M, int N, int num_sms) {
 cudaError_t launch_k2_chain(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, const K2Params& p, int num_sms,
                             cudaStream_t stream) {
   const int units = ((p.M + kBM - 1) / kBM) * p.chain.S;
-  // tm_y and the LoRA maps are not used in chain mode: any valid map fills the slots
-  return launch_k2_impl<true>(tm_xl, tm_l2, tm_l2, tm_l2, tm_l2, p, units < num_sms ? units : num_sms, stream);
+  // tm_y, tm_r and the LoRA maps are not used in chain mode: any valid map fills the slots
+  return launch_k2_impl<kModeChain>(tm_xl, tm_l2, tm_l2, tm_l2, tm_l2, tm_l2, p, units < num_sms ? units : num_sms, stream);
 }
 
 }  // namespace svdq

@@ -49,6 +49,7 @@
 #include <cuda_runtime.h>
 
 #include "kernels.h"
+#include "residual.cuh"
 #include "sm100.cuh"
 
 namespace svdq {
@@ -99,6 +100,10 @@ constexpr int kSmemBytes =
     kOStages * kOStageBytes + kBrBytes + kPStages * kPStageBytes + kEpiWarps * kEpiWarpBytes + 256 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory per block");
 constexpr int kTmemCols = 512;
+// the barriers' 256 bytes hold the residual's two load barriers per epilogue warp too
+constexpr int kResBar = 160;
+static_assert((2 * kPStages + 2 * kOStages + 2 + 4 + 1) * 8 + 8 <= kResBar && kResBar + kEpiWarps * 16 <= 256,
+              "barrier space");
 
 __device__ __forceinline__ void record_error(int* err, volatile int* abort_flag, int code) {
   atomicCAS(err, 0, code);
@@ -132,11 +137,15 @@ __device__ __forceinline__ void dequant_word(uint32_t w, __half2 s2, uint32_t (&
 // buffer's barriers then complete twice per tile; both sides count the phases.
 constexpr int kLoraLoadG = 2, kLoraMmaG = 5;
 
+//
+// kRes: the epilogue adds the gated output to the residual of tm_r.
+template <bool kRes>
 __global__ void __launch_bounds__(kThreads, 1)
     k2_int4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                    const __grid_constant__ CUtensorMap tm_xl, const __grid_constant__ CUtensorMap tm_l2,
                    const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_xla,
-                   const __grid_constant__ CUtensorMap tm_l2a, K2Int4Params p) {
+                   const __grid_constant__ CUtensorMap tm_l2a, const __grid_constant__ CUtensorMap tm_r,
+                   K2Int4Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* oring = smem;                                          // operand ring (1 KiB aligned)
@@ -154,6 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint64_t* res_bar = reinterpret_cast<uint64_t*>(epi_buf + kEpiWarps * kEpiWarpBytes + kResBar);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -182,6 +192,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       dev::mbar_init(&acc_empty[b], kEpiWarps);
     }
     dev::mbar_init(drain, 1);
+    if (kRes)
+      for (int i = 0; i < 2 * kEpiWarps; ++i) dev::mbar_init(&res_bar[i], 1);
     *abort_flag = 0;
     dev::fence_mbar_init();
   }
@@ -416,7 +428,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* wbuf = epi_buf + (warp - kEpiWarp0) * kEpiWarpBytes;
     if (lane == 0) dev::tma_prefetch_desc(&tm_y);
     int tcount = 0, chunk = 0;
-    for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++tcount) {
+    dev::ResidualLoads loads{&tm_r, res_bar + 2 * (warp - kEpiWarp0), wbuf, 0};
+    if (kRes) {
+      // the residual and the gate may come from the preceding kernel
+      dev::griddep_wait();
+      if (lane == 0 && blockIdx.x < num_tiles)
+        for (int c = 0; c < 2; ++c)
+          loads.issue((int)blockIdx.x / tiles_m * kBN + c * 32, (int)blockIdx.x % tiles_m * kBM + q * 32);
+    }
+    bool ok = true;
+    for (int tile = blockIdx.x; tile < num_tiles && ok; tile += gridDim.x, ++tcount) {
       const int m0 = (tile % tiles_m) * kBM;
       const int n0 = (tile / tiles_m) * kBN;
       const int ab = tcount & 1;
@@ -428,6 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       dev::tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(ab * 256);
+      const __nv_bfloat16* gate = kRes ? dev::gate_row(p.res, m0 + q * 32 + lane, M) : nullptr;
       uint32_t va[32], vb[32];
       dev::tmem_load_32cols(taddr, va);
       dev::tmem_load_wait(va);
@@ -448,13 +470,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           bias[4 * f + 2] = b4.z;
           bias[4 * f + 3] = b4.w;
         }
-        // the buffer of this chunk was last read by the store issued two chunks ago
-        if (lane == 0) dev::bulk_wait_group_read<1>();
+        if (kRes) {
+          // the residual's chunk is in the buffer (after a wait that ran out the
+          // chunk is still finished, so that the accumulator is handed back)
+          const bool here = loads.wait(chunk, abort_flag, p.budget_ns);
+          if (!__all_sync(0xffffffffu, here)) {
+            if (lane == 0 && ok) record_error(p.err, abort_flag, 0x308);
+            ok = false;
+          }
+        } else if (lane == 0) {
+          // the buffer of this chunk was last read by the store issued two chunks ago
+          dev::bulk_wait_group_read<1>();
+        }
         __syncwarp();
         uint8_t* buf = wbuf + (chunk & 1) * kEpiBufBytes;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          uint32_t packed[4];
+          uint32_t packed[4], rs[4] = {}, gt[4] = {};
+          if (kRes) {
+            const uint4 r4 = *reinterpret_cast<const uint4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4));
+            const uint4 g4 = dev::gate8(gate, n0 + c * 32 + j * 8, N);
+            rs[0] = r4.x; rs[1] = r4.y; rs[2] = r4.z; rs[3] = r4.w;
+            gt[0] = g4.x; gt[1] = g4.y; gt[2] = g4.z; gt[3] = g4.w;
+          }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int i0 = j * 8 + 2 * e;
@@ -464,8 +502,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               y0 = dev::gelu_tanh(y0);
               y1 = dev::gelu_tanh(y1);
             }
-            const __nv_bfloat162 h2 = __floats2bfloat162_rn(y0, y1);
-            packed[e] = *reinterpret_cast<const uint32_t*>(&h2);
+            if (kRes) {
+              packed[e] = dev::add_gated(rs[e], gt[e], y0, y1);
+            } else {
+              const __nv_bfloat162 h2 = __floats2bfloat162_rn(y0, y1);
+              packed[e] = *reinterpret_cast<const uint32_t*>(&h2);
+            }
           }
           // 64-byte swizzle: 16-byte chunk j of row `lane` sits at j ^ ((lane >> 1) & 3)
           *reinterpret_cast<uint4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
@@ -476,6 +518,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           dev::tma_store_2d(&tm_y, buf, n0 + c * 32, m0 + q * 32);
           dev::bulk_commit_group();
+          if (kRes && ok) {
+            // the chunk after next takes this buffer, once the store has read it
+            const int tn = c < 6 ? tile : tile + (int)gridDim.x;
+            if (tn < num_tiles) {
+              dev::bulk_wait_group_read<0>();
+              loads.issue(tn / tiles_m * kBN + ((c + 2) & 7) * 32, tn % tiles_m * kBM + q * 32);
+            }
+          }
         }
         if (c + 1 < 8) dev::tmem_load_wait(nxt);
         if (c == 6) {
@@ -487,6 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     }
+    if (kRes && lane == 0) loads.drain(abort_flag, p.budget_ns);
     if (lane == 0) dev::bulk_wait_group_all();
   }
 
@@ -502,18 +553,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-cudaError_t launch_k2_int4(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const CUtensorMap& tm_xl,
-                           const CUtensorMap& tm_l2, const CUtensorMap& tm_y, const CUtensorMap& tm_xla,
-                           const CUtensorMap& tm_l2a, const K2Int4Params& p, int num_sms, cudaStream_t stream) {
+namespace {
+
+template <bool kRes>
+cudaError_t launch_k2_int4_impl(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const CUtensorMap& tm_xl,
+                                const CUtensorMap& tm_l2, const CUtensorMap& tm_y, const CUtensorMap& tm_xla,
+                                const CUtensorMap& tm_l2a, const CUtensorMap& tm_r, const K2Int4Params& p,
+                                int num_sms, cudaStream_t stream) {
   static thread_local int configured_device = -1;
   int dev = 0;
   cudaGetDevice(&dev);
   if (configured_device != dev) {
-    cudaError_t e = cudaFuncSetAttribute(k2_int4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    cudaError_t e = cudaFuncSetAttribute(k2_int4_kernel<kRes>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     // the warpgroups' register budgets fit the launch allocation
     cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, k2_int4_kernel);
+    e = cudaFuncGetAttributes(&fa, k2_int4_kernel<kRes>);
     if (e != cudaSuccess) return e;
     if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
     configured_device = dev;
@@ -530,7 +585,17 @@ cudaError_t launch_k2_int4(const CUtensorMap& tm_a, const CUtensorMap& tm_b, con
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k2_int4_kernel, tm_a, tm_b, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, p);
+  return cudaLaunchKernelEx(&cfg, k2_int4_kernel<kRes>, tm_a, tm_b, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, tm_r, p);
+}
+
+}  // namespace
+
+cudaError_t launch_k2_int4(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const CUtensorMap& tm_xl,
+                           const CUtensorMap& tm_l2, const CUtensorMap& tm_y, const CUtensorMap& tm_xla,
+                           const CUtensorMap& tm_l2a, const CUtensorMap* tm_r, const K2Int4Params& p, int num_sms,
+                           cudaStream_t stream) {
+  return tm_r ? launch_k2_int4_impl<true>(tm_a, tm_b, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, *tm_r, p, num_sms, stream)
+              : launch_k2_int4_impl<false>(tm_a, tm_b, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, tm_y, p, num_sms, stream);
 }
 
 }  // namespace svdq

@@ -29,6 +29,7 @@
 #include <cuda_runtime.h>
 
 #include "kernels.h"
+#include "residual.cuh"
 #include "sm100.cuh"
 
 namespace svdq {
@@ -53,7 +54,8 @@ constexpr int kBrXL = kBM * 64;              // XL rows (32 BF16, the rank in th
 constexpr int kBrBytes = kBrXL + kBN * 64;
 constexpr int kEpiBufBytes = 32 * 64;
 constexpr int kEpiWarpBytes = 2 * kEpiBufBytes + 1024;   // two chunk buffers + 128 bias + 128 s_w floats
-constexpr int kSmemBytes = kStages * kStageBytes + kBrBytes + kEpiWarps * kEpiWarpBytes + 1024 + 256;
+constexpr int kResBarBytes = kEpiWarps * 16;             // two load barriers per epilogue warp
+constexpr int kSmemBytes = kStages * kStageBytes + kBrBytes + kEpiWarps * kEpiWarpBytes + 1024 + 256 + kResBarBytes;
 static_assert(kSmemBytes <= 232448, "shared memory per block");
 constexpr int kTmemCols = 512;
 constexpr int kBranchCol = 256;
@@ -77,9 +79,12 @@ __device__ __forceinline__ void record_error(int* err, volatile int* abort_flag,
   *abort_flag = 1;
 }
 
+// kRes: the epilogue adds the gated output to the residual of tm_r.
+template <bool kRes>
 __global__ void __launch_bounds__(kThreads, 1)
     k2_int8_kernel(const __grid_constant__ CUtensorMap tm_xl, const __grid_constant__ CUtensorMap tm_l2,
-                   const __grid_constant__ CUtensorMap tm_y, K2Int8Params p) {
+                   const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_r,
+                   K2Int8Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* brbuf = smem + kStages * kStageBytes;
@@ -93,6 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* drain = acc_empty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint64_t* res_bar = reinterpret_cast<uint64_t*>(epi_buf + kEpiWarps * kEpiWarpBytes + 256);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -113,6 +119,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     dev::mbar_init(acc_full, 1);
     dev::mbar_init(acc_empty, kEpiWarps);
     dev::mbar_init(drain, 1);
+    if (kRes)
+      for (int i = 0; i < 2 * kEpiWarps; ++i) dev::mbar_init(&res_bar[i], 1);
     *abort_flag = 0;
     dev::fence_mbar_init();
   }
@@ -242,7 +250,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* sw_s = bias_s + 128;
     if (lane == 0) dev::tma_prefetch_desc(&tm_y);
     int tcount = 0, chunk = 0;
-    for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++tcount) {
+    dev::ResidualLoads loads{&tm_r, res_bar + 2 * (warp - kEpiWarp0), wbuf, 0};
+    if (kRes) {
+      // the residual and the gate may come from the preceding kernel
+      dev::griddep_wait();
+      if (lane == 0 && blockIdx.x < num_tiles)
+        for (int c = 0; c < 2; ++c)
+          loads.issue((int)blockIdx.x / tiles_m * kBN + half * 128 + c * 32,
+                      (int)blockIdx.x % tiles_m * kBM + q * 32);
+    }
+    bool ok = true;
+    for (int tile = blockIdx.x; tile < num_tiles && ok; tile += gridDim.x, ++tcount) {
       const int m0 = (tile % tiles_m) * kBM;
       const int n0 = (tile / tiles_m) * kBN + half * 128;
       {
@@ -293,15 +311,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       dev::tc_fence_before();
       __syncwarp();
       if (lane == 0) dev::mbar_arrive(acc_empty);
+      const __nv_bfloat16* gate = kRes ? dev::gate_row(p.res, m0 + q * 32 + lane, M) : nullptr;
 #pragma unroll
       for (int c = 0; c < 4; ++c, ++chunk) {
         uint32_t (&cur)[32] = c == 0 ? va : c == 1 ? vb : c == 2 ? vc : vd;
-        if (lane == 0) dev::bulk_wait_group_read<1>();
+        if (kRes) {
+          // the residual's chunk is in the buffer
+          const bool here = loads.wait(chunk, abort_flag, p.budget_ns);
+          if (!__all_sync(0xffffffffu, here)) {
+            if (lane == 0) record_error(p.err, abort_flag, 0x507);
+            ok = false;
+            break;
+          }
+        } else if (lane == 0) {
+          dev::bulk_wait_group_read<1>();
+        }
         __syncwarp();
         uint8_t* buf = wbuf + (chunk & 1) * kEpiBufBytes;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          uint32_t packed[4];
+          uint32_t packed[4], rs[4] = {}, gt[4] = {};
+          if (kRes) {
+            const uint4 r4 = *reinterpret_cast<const uint4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4));
+            const uint4 g4 = dev::gate8(gate, n0 + c * 32 + j * 8, N);
+            rs[0] = r4.x; rs[1] = r4.y; rs[2] = r4.z; rs[3] = r4.w;
+            gt[0] = g4.x; gt[1] = g4.y; gt[2] = g4.z; gt[3] = g4.w;
+          }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 b2 = reinterpret_cast<const float2*>(bias_s)[c * 16 + j * 4 + e];
@@ -311,8 +346,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               y0 = dev::gelu_tanh(y0);
               y1 = dev::gelu_tanh(y1);
             }
-            const __nv_bfloat162 h2 = __floats2bfloat162_rn(y0, y1);
-            packed[e] = *reinterpret_cast<const uint32_t*>(&h2);
+            if (kRes) {
+              packed[e] = dev::add_gated(rs[e], gt[e], y0, y1);
+            } else {
+              const __nv_bfloat162 h2 = __floats2bfloat162_rn(y0, y1);
+              packed[e] = *reinterpret_cast<const uint32_t*>(&h2);
+            }
           }
           *reinterpret_cast<uint4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
               make_uint4(packed[0], packed[1], packed[2], packed[3]);
@@ -322,10 +361,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           dev::tma_store_2d(&tm_y, buf, n0 + c * 32, m0 + q * 32);
           dev::bulk_commit_group();
+          if (kRes) {
+            // the chunk after next takes this buffer, once the store has read it
+            const int tn = c < 2 ? tile : tile + (int)gridDim.x;
+            if (tn < num_tiles) {
+              dev::bulk_wait_group_read<0>();
+              loads.issue(tn / tiles_m * kBN + half * 128 + ((c + 2) & 3) * 32, tn % tiles_m * kBM + q * 32);
+            }
+          }
         }
       }
       __syncwarp();
     }
+    if (kRes && lane == 0) loads.drain(abort_flag, p.budget_ns);
     if (lane == 0) dev::bulk_wait_group_all();
   }
 
@@ -345,16 +393,19 @@ size_t k2_int8_weight_bytes(int N, int K) {
   return (size_t)((N + 255) / 256) * (size_t)((K + 127) / 128) * (size_t)kBBytes;
 }
 
-cudaError_t launch_k2_int8(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, const CUtensorMap& tm_y,
-                           const K2Int8Params& p, int num_sms, cudaStream_t stream) {
+namespace {
+
+template <bool kRes>
+cudaError_t launch_k2_int8_impl(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, const CUtensorMap& tm_y,
+                                const CUtensorMap& tm_r, const K2Int8Params& p, int num_sms, cudaStream_t stream) {
   static thread_local int configured_device = -1;
   int dev = 0;
   cudaGetDevice(&dev);
   if (configured_device != dev) {
-    cudaError_t e = cudaFuncSetAttribute(k2_int8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    cudaError_t e = cudaFuncSetAttribute(k2_int8_kernel<kRes>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, k2_int8_kernel);
+    e = cudaFuncGetAttributes(&fa, k2_int8_kernel<kRes>);
     if (e != cudaSuccess) return e;
     if (fa.numRegs != 128) return cudaErrorInvalidConfiguration;
     configured_device = dev;
@@ -370,7 +421,15 @@ cudaError_t launch_k2_int8(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, c
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k2_int8_kernel, tm_xl, tm_l2, tm_y, p);
+  return cudaLaunchKernelEx(&cfg, k2_int8_kernel<kRes>, tm_xl, tm_l2, tm_y, tm_r, p);
+}
+
+}  // namespace
+
+cudaError_t launch_k2_int8(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, const CUtensorMap& tm_y,
+                           const CUtensorMap* tm_r, const K2Int8Params& p, int num_sms, cudaStream_t stream) {
+  return tm_r ? launch_k2_int8_impl<true>(tm_xl, tm_l2, tm_y, *tm_r, p, num_sms, stream)
+              : launch_k2_int8_impl<false>(tm_xl, tm_l2, tm_y, tm_y, p, num_sms, stream);
 }
 
 }  // namespace svdq
