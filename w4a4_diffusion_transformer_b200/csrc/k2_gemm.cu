@@ -103,9 +103,10 @@ constexpr int kTmemCols = 512;
 constexpr int kSFCol0 = 256;
 constexpr int kSFStageCols = 12 * kKB;       // 4 columns of A + 8 of B per K block
 
-// Kernel modes: the layer, the chain's fc1, the layer with a residual epilogue.
-constexpr int kModeLayer = 0, kModeChain = 1, kModeResidual = 2;
-constexpr int kResBarBytes = kEpiWarps * 16;       // two load barriers per epilogue warp
+// Kernel modes: the layer, the chain's fc1, the layer with a residual epilogue
+// (without and with GELU in front of it).
+constexpr int kModeLayer = 0, kModeChain = 1, kModeResidual = 2, kModeResidualGelu = 3;
+constexpr int kResBytes = kEpiWarps * (16 + 256);   // per epilogue warp two load barriers and 128 gate values
 
 template <int kMode>
 struct K2Layout {
@@ -114,7 +115,7 @@ struct K2Layout {
   static constexpr int br_bytes = deep ? 0 : kBrBytes;
   static constexpr int epi_warp_bytes = deep ? 512 : kEpiWarpBytes;   // deep: 128 bias floats only
   static constexpr int smem = stages * kStageBytes + br_bytes + kEpiWarps * epi_warp_bytes + 1024 + 256 +
-                              (kMode == kModeResidual ? kResBarBytes : 0);
+                              (kMode >= kModeResidual ? kResBytes : 0);
   static_assert(smem <= 232448, "shared memory per block");
   static_assert(kSFCol0 + stages * kSFStageCols <= kTmemCols, "TMEM budget");
 };
@@ -159,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_xla,
               const __grid_constant__ CUtensorMap tm_l2a, const __grid_constant__ CUtensorMap tm_r, K2Params p) {
   using Lay = K2Layout<kMode>;
-  constexpr bool kChain = kMode == kModeChain, kRes = kMode == kModeResidual;
+  constexpr bool kChain = kMode == kModeChain, kRes = kMode >= kModeResidual;
   constexpr int kStages = Lay::stages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -462,7 +463,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       int tcount = 0, chunk = 0;
       bool ok = true;
       dev::ResidualLoads loads{&tm_r, res_bar + 2 * (warp - kEpiWarp0), wbuf, 0};
+      dev::Gate<128> gate;
       if (kRes) {
+        gate.staged = reinterpret_cast<uint4*>(res_bar + 2 * kEpiWarps) + 16 * (warp - kEpiWarp0);
         // the residual and the gate may come from the preceding kernel
         dev::griddep_wait();
         if (lane == 0 && blockIdx.x < ts.units()) {
@@ -481,6 +484,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             float4 b4 = make_float4(0.f, 0.f, 0.f, 0.f);
             if (col < N) b4 = __ldg(reinterpret_cast<const float4*>(p.bias + col));
             reinterpret_cast<float4*>(bias_s)[lane] = b4;
+          }
+          if (kRes) {
+            gate.tile(p.res, m0 + q * 32, M, n0, N);
+            if (lane == 0)
+              for (int c = 2; c < 4; ++c)
+                if (n0 + c * 32 < N) dev::tma_prefetch_2d(&tm_r, n0 + c * 32, m0 + q * 32);
           }
           const bool got = dev::mbar_wait(acc_full, (uint32_t)tcount & 1u, abort_flag, p.budget_ns);
           if (!__all_sync(0xffffffffu, got)) {          // warp-uniform exit (tcgen05.ld is warp-collective)
@@ -533,7 +542,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();                                 // bias_s is restaged for the next tile
           } else {
-          const __nv_bfloat16* gate = kRes ? dev::gate_row(p.res, m0 + q * 32 + lane, M) : nullptr;
 #pragma unroll
           for (int c = 0; c < 4; ++c, ++chunk) {
             uint32_t (&cur)[32] = c == 0 ? va : c == 1 ? vb : c == 2 ? vc : vd;
@@ -551,15 +559,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             uint8_t* buf = wbuf + (chunk & 1) * kEpiBufBytes;
+            if (kRes) {
+              dev::residual_chunk<kMode == kModeResidualGelu>(buf, gate, c, n0, N, [&](int i, float (&v)[8]) {
+                const float4 b0 = reinterpret_cast<const float4*>(bias_s + c * 32 + i)[0];
+                const float4 b1 = reinterpret_cast<const float4*>(bias_s + c * 32 + i)[1];
+                const float b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = p.alpha * __uint_as_float(cur[i + e]) + b[e];
+              });
+            } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              uint32_t packed[4], rs[4] = {}, gt[4] = {};
-              if (kRes) {
-                const uint4 r4 = *reinterpret_cast<const uint4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4));
-                const uint4 g4 = dev::gate8(gate, n0 + c * 32 + j * 8, N);
-                rs[0] = r4.x; rs[1] = r4.y; rs[2] = r4.z; rs[3] = r4.w;
-                gt[0] = g4.x; gt[1] = g4.y; gt[2] = g4.z; gt[3] = g4.w;
-              }
+              uint32_t packed[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 const float2 b2 = reinterpret_cast<const float2*>(bias_s)[c * 16 + j * 4 + e];
@@ -569,16 +580,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                   y0 = dev::gelu_tanh(y0);
                   y1 = dev::gelu_tanh(y1);
                 }
-                if (kRes) {
-                  packed[e] = dev::add_gated(rs[e], gt[e], y0, y1);
-                } else {
-                  const __nv_bfloat162 h2 = __floats2bfloat162_rn(y0, y1);
-                  packed[e] = *reinterpret_cast<const uint32_t*>(&h2);
-                }
+                const __nv_bfloat162 h2 = __floats2bfloat162_rn(y0, y1);
+                packed[e] = *reinterpret_cast<const uint32_t*>(&h2);
               }
               // 64-byte swizzle: 16-byte chunk j of row `lane` sits at j ^ ((lane >> 1) & 3)
               *reinterpret_cast<uint4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
                   make_uint4(packed[0], packed[1], packed[2], packed[3]);
+            }
             }
             dev::fence_async_shared();                    // make the writes visible to the TMA engine
             __syncwarp();
@@ -872,6 +880,8 @@ cudaError_t launch_k2(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, const 
                       const K2Params& p, int num_sms, cudaStream_t stream) {
   const int tiles = ((p.M + kBM - 1) / kBM) * ((p.N + kBN - 1) / kBN);
   const int grid = tiles < num_sms ? tiles : num_sms;
+  if (tm_r && p.gelu)
+    return launch_k2_impl<kModeResidualGelu>(tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, *tm_r, p, grid, stream);
   if (tm_r) return launch_k2_impl<kModeResidual>(tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, *tm_r, p, grid, stream);
   return launch_k2_impl<kModeLayer>(tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, tm_y, p, grid, stream);
 }

@@ -96,8 +96,9 @@ constexpr int kBrABytes = kBM * 64;
 constexpr int kBrBytes = kBrABytes + kBN * 64;       // 24 KiB
 constexpr int kEpiBufBytes = 32 * 64;                // one 32 x 32 BF16 output chunk
 constexpr int kEpiWarpBytes = 2 * kEpiBufBytes;
+constexpr int kGateBytes = kEpiWarps * 512;          // 256 gate values per epilogue warp
 constexpr int kSmemBytes =
-    kOStages * kOStageBytes + kBrBytes + kPStages * kPStageBytes + kEpiWarps * kEpiWarpBytes + 256 + 1024;
+    kOStages * kOStageBytes + kBrBytes + kPStages * kPStageBytes + kEpiWarps * kEpiWarpBytes + 256 + kGateBytes + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory per block");
 constexpr int kTmemCols = 512;
 // the barriers' 256 bytes hold the residual's two load barriers per epilogue warp too
@@ -138,8 +139,9 @@ __device__ __forceinline__ void dequant_word(uint32_t w, __half2 s2, uint32_t (&
 constexpr int kLoraLoadG = 2, kLoraMmaG = 5;
 
 //
-// kRes: the epilogue adds the gated output to the residual of tm_r.
-template <bool kRes>
+// kRes: the epilogue adds the gated output to the residual of tm_r (kResGelu:
+// GELU in front of it; without a residual p.gelu says).
+template <bool kRes, bool kResGelu>
 __global__ void __launch_bounds__(kThreads, 1)
     k2_int4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                    const __grid_constant__ CUtensorMap tm_xl, const __grid_constant__ CUtensorMap tm_l2,
@@ -429,7 +431,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) dev::tma_prefetch_desc(&tm_y);
     int tcount = 0, chunk = 0;
     dev::ResidualLoads loads{&tm_r, res_bar + 2 * (warp - kEpiWarp0), wbuf, 0};
+    dev::Gate<256> gate;
     if (kRes) {
+      gate.staged = reinterpret_cast<uint4*>(epi_buf + kEpiWarps * kEpiWarpBytes + 256) + 32 * (warp - kEpiWarp0);
       // the residual and the gate may come from the preceding kernel
       dev::griddep_wait();
       if (lane == 0 && blockIdx.x < num_tiles)
@@ -441,6 +445,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int m0 = (tile % tiles_m) * kBM;
       const int n0 = (tile / tiles_m) * kBN;
       const int ab = tcount & 1;
+      if (kRes) {
+        gate.tile(p.res, m0 + q * 32, M, n0, N);
+        if (lane == 0)
+          for (int c = 2; c < 8; ++c)
+            if (n0 + c * 32 < N) dev::tma_prefetch_2d(&tm_r, n0 + c * 32, m0 + q * 32);
+      }
       const bool got = dev::mbar_wait(&acc_full[ab], (uint32_t)(tcount >> 1) & 1u, abort_flag, p.budget_ns);
       if (!__all_sync(0xffffffffu, got)) {          // warp-uniform exit (tcgen05.ld is warp-collective)
         if (lane == 0) record_error(p.err, abort_flag, 0x307);
@@ -449,7 +459,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       dev::tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(ab * 256);
-      const __nv_bfloat16* gate = kRes ? dev::gate_row(p.res, m0 + q * 32 + lane, M) : nullptr;
       uint32_t va[32], vb[32];
       dev::tmem_load_32cols(taddr, va);
       dev::tmem_load_wait(va);
@@ -484,15 +493,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         uint8_t* buf = wbuf + (chunk & 1) * kEpiBufBytes;
+        if (kRes) {
+          dev::residual_chunk<kResGelu>(buf, gate, c, n0, N, [&](int i, float (&v)[8]) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = p.alpha * __uint_as_float(cur[i + e]) + bias[i + e];
+          });
+        } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          uint32_t packed[4], rs[4] = {}, gt[4] = {};
-          if (kRes) {
-            const uint4 r4 = *reinterpret_cast<const uint4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4));
-            const uint4 g4 = dev::gate8(gate, n0 + c * 32 + j * 8, N);
-            rs[0] = r4.x; rs[1] = r4.y; rs[2] = r4.z; rs[3] = r4.w;
-            gt[0] = g4.x; gt[1] = g4.y; gt[2] = g4.z; gt[3] = g4.w;
-          }
+          uint32_t packed[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int i0 = j * 8 + 2 * e;
@@ -502,16 +511,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               y0 = dev::gelu_tanh(y0);
               y1 = dev::gelu_tanh(y1);
             }
-            if (kRes) {
-              packed[e] = dev::add_gated(rs[e], gt[e], y0, y1);
-            } else {
-              const __nv_bfloat162 h2 = __floats2bfloat162_rn(y0, y1);
-              packed[e] = *reinterpret_cast<const uint32_t*>(&h2);
-            }
+            const __nv_bfloat162 h2 = __floats2bfloat162_rn(y0, y1);
+            packed[e] = *reinterpret_cast<const uint32_t*>(&h2);
           }
           // 64-byte swizzle: 16-byte chunk j of row `lane` sits at j ^ ((lane >> 1) & 3)
           *reinterpret_cast<uint4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
               make_uint4(packed[0], packed[1], packed[2], packed[3]);
+        }
         }
         dev::fence_async_shared();                    // make the writes visible to the TMA engine
         __syncwarp();
@@ -555,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 namespace {
 
-template <bool kRes>
+template <bool kRes, bool kResGelu>
 cudaError_t launch_k2_int4_impl(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const CUtensorMap& tm_xl,
                                 const CUtensorMap& tm_l2, const CUtensorMap& tm_y, const CUtensorMap& tm_xla,
                                 const CUtensorMap& tm_l2a, const CUtensorMap& tm_r, const K2Int4Params& p,
@@ -564,11 +570,11 @@ cudaError_t launch_k2_int4_impl(const CUtensorMap& tm_a, const CUtensorMap& tm_b
   int dev = 0;
   cudaGetDevice(&dev);
   if (configured_device != dev) {
-    cudaError_t e = cudaFuncSetAttribute(k2_int4_kernel<kRes>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    cudaError_t e = cudaFuncSetAttribute(k2_int4_kernel<kRes, kResGelu>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     // the warpgroups' register budgets fit the launch allocation
     cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, k2_int4_kernel<kRes>);
+    e = cudaFuncGetAttributes(&fa, k2_int4_kernel<kRes, kResGelu>);
     if (e != cudaSuccess) return e;
     if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
     configured_device = dev;
@@ -585,7 +591,7 @@ cudaError_t launch_k2_int4_impl(const CUtensorMap& tm_a, const CUtensorMap& tm_b
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k2_int4_kernel<kRes>, tm_a, tm_b, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, tm_r, p);
+  return cudaLaunchKernelEx(&cfg, k2_int4_kernel<kRes, kResGelu>, tm_a, tm_b, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, tm_r, p);
 }
 
 }  // namespace
@@ -594,8 +600,11 @@ cudaError_t launch_k2_int4(const CUtensorMap& tm_a, const CUtensorMap& tm_b, con
                            const CUtensorMap& tm_l2, const CUtensorMap& tm_y, const CUtensorMap& tm_xla,
                            const CUtensorMap& tm_l2a, const CUtensorMap* tm_r, const K2Int4Params& p, int num_sms,
                            cudaStream_t stream) {
-  return tm_r ? launch_k2_int4_impl<true>(tm_a, tm_b, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, *tm_r, p, num_sms, stream)
-              : launch_k2_int4_impl<false>(tm_a, tm_b, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, tm_y, p, num_sms, stream);
+  if (!tm_r)
+    return launch_k2_int4_impl<false, false>(tm_a, tm_b, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, tm_y, p, num_sms, stream);
+  return p.gelu
+             ? launch_k2_int4_impl<true, true>(tm_a, tm_b, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, *tm_r, p, num_sms, stream)
+             : launch_k2_int4_impl<true, false>(tm_a, tm_b, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, *tm_r, p, num_sms, stream);
 }
 
 }  // namespace svdq

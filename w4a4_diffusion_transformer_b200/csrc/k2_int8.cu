@@ -54,8 +54,8 @@ constexpr int kBrXL = kBM * 64;              // XL rows (32 BF16, the rank in th
 constexpr int kBrBytes = kBrXL + kBN * 64;
 constexpr int kEpiBufBytes = 32 * 64;
 constexpr int kEpiWarpBytes = 2 * kEpiBufBytes + 1024;   // two chunk buffers + 128 bias + 128 s_w floats
-constexpr int kResBarBytes = kEpiWarps * 16;             // two load barriers per epilogue warp
-constexpr int kSmemBytes = kStages * kStageBytes + kBrBytes + kEpiWarps * kEpiWarpBytes + 1024 + 256 + kResBarBytes;
+constexpr int kResBytes = kEpiWarps * (16 + 256);        // per epilogue warp two load barriers and 128 gate values
+constexpr int kSmemBytes = kStages * kStageBytes + kBrBytes + kEpiWarps * kEpiWarpBytes + 1024 + 256 + kResBytes;
 static_assert(kSmemBytes <= 232448, "shared memory per block");
 constexpr int kTmemCols = 512;
 constexpr int kBranchCol = 256;
@@ -79,8 +79,9 @@ __device__ __forceinline__ void record_error(int* err, volatile int* abort_flag,
   *abort_flag = 1;
 }
 
-// kRes: the epilogue adds the gated output to the residual of tm_r.
-template <bool kRes>
+// kRes: the epilogue adds the gated output to the residual of tm_r (kResGelu:
+// GELU in front of it; without a residual p.gelu says).
+template <bool kRes, bool kResGelu>
 __global__ void __launch_bounds__(kThreads, 1)
     k2_int8_kernel(const __grid_constant__ CUtensorMap tm_xl, const __grid_constant__ CUtensorMap tm_l2,
                    const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_r,
@@ -251,7 +252,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) dev::tma_prefetch_desc(&tm_y);
     int tcount = 0, chunk = 0;
     dev::ResidualLoads loads{&tm_r, res_bar + 2 * (warp - kEpiWarp0), wbuf, 0};
+    dev::Gate<128> gate;
     if (kRes) {
+      gate.staged = reinterpret_cast<uint4*>(res_bar + 2 * kEpiWarps) + 16 * (warp - kEpiWarp0);
       // the residual and the gate may come from the preceding kernel
       dev::griddep_wait();
       if (lane == 0 && blockIdx.x < num_tiles)
@@ -272,6 +275,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         reinterpret_cast<float4*>(bias_s)[lane] = b4;
         reinterpret_cast<float4*>(sw_s)[lane] = w4;
+      }
+      if (kRes) {
+        gate.tile(p.res, m0 + q * 32, M, n0, N);
+        if (lane == 0)
+          for (int c = 2; c < 4; ++c)
+            if (n0 + c * 32 < N) dev::tma_prefetch_2d(&tm_r, n0 + c * 32, m0 + q * 32);
       }
       const bool got = dev::mbar_wait(acc_full, (uint32_t)tcount & 1u, abort_flag, p.budget_ns);
       if (!__all_sync(0xffffffffu, got)) {
@@ -311,7 +320,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       dev::tc_fence_before();
       __syncwarp();
       if (lane == 0) dev::mbar_arrive(acc_empty);
-      const __nv_bfloat16* gate = kRes ? dev::gate_row(p.res, m0 + q * 32 + lane, M) : nullptr;
 #pragma unroll
       for (int c = 0; c < 4; ++c, ++chunk) {
         uint32_t (&cur)[32] = c == 0 ? va : c == 1 ? vb : c == 2 ? vc : vd;
@@ -328,15 +336,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         uint8_t* buf = wbuf + (chunk & 1) * kEpiBufBytes;
+        if (kRes) {
+          dev::residual_chunk<kResGelu>(buf, gate, c, n0, N, [&](int i, float (&v)[8]) {
+            const float4 b0 = reinterpret_cast<const float4*>(bias_s + c * 32 + i)[0];
+            const float4 b1 = reinterpret_cast<const float4*>(bias_s + c * 32 + i)[1];
+            const float b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(cur[i + e]) + b[e];
+          });
+        } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          uint32_t packed[4], rs[4] = {}, gt[4] = {};
-          if (kRes) {
-            const uint4 r4 = *reinterpret_cast<const uint4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4));
-            const uint4 g4 = dev::gate8(gate, n0 + c * 32 + j * 8, N);
-            rs[0] = r4.x; rs[1] = r4.y; rs[2] = r4.z; rs[3] = r4.w;
-            gt[0] = g4.x; gt[1] = g4.y; gt[2] = g4.z; gt[3] = g4.w;
-          }
+          uint32_t packed[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 b2 = reinterpret_cast<const float2*>(bias_s)[c * 16 + j * 4 + e];
@@ -346,15 +357,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               y0 = dev::gelu_tanh(y0);
               y1 = dev::gelu_tanh(y1);
             }
-            if (kRes) {
-              packed[e] = dev::add_gated(rs[e], gt[e], y0, y1);
-            } else {
-              const __nv_bfloat162 h2 = __floats2bfloat162_rn(y0, y1);
-              packed[e] = *reinterpret_cast<const uint32_t*>(&h2);
-            }
+            const __nv_bfloat162 h2 = __floats2bfloat162_rn(y0, y1);
+            packed[e] = *reinterpret_cast<const uint32_t*>(&h2);
           }
           *reinterpret_cast<uint4*>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
               make_uint4(packed[0], packed[1], packed[2], packed[3]);
+        }
         }
         dev::fence_async_shared();
         __syncwarp();
@@ -395,17 +403,17 @@ size_t k2_int8_weight_bytes(int N, int K) {
 
 namespace {
 
-template <bool kRes>
+template <bool kRes, bool kResGelu>
 cudaError_t launch_k2_int8_impl(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, const CUtensorMap& tm_y,
                                 const CUtensorMap& tm_r, const K2Int8Params& p, int num_sms, cudaStream_t stream) {
   static thread_local int configured_device = -1;
   int dev = 0;
   cudaGetDevice(&dev);
   if (configured_device != dev) {
-    cudaError_t e = cudaFuncSetAttribute(k2_int8_kernel<kRes>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    cudaError_t e = cudaFuncSetAttribute(k2_int8_kernel<kRes, kResGelu>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, k2_int8_kernel<kRes>);
+    e = cudaFuncGetAttributes(&fa, k2_int8_kernel<kRes, kResGelu>);
     if (e != cudaSuccess) return e;
     if (fa.numRegs != 128) return cudaErrorInvalidConfiguration;
     configured_device = dev;
@@ -421,15 +429,16 @@ cudaError_t launch_k2_int8_impl(const CUtensorMap& tm_xl, const CUtensorMap& tm_
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k2_int8_kernel<kRes>, tm_xl, tm_l2, tm_y, tm_r, p);
+  return cudaLaunchKernelEx(&cfg, k2_int8_kernel<kRes, kResGelu>, tm_xl, tm_l2, tm_y, tm_r, p);
 }
 
 }  // namespace
 
 cudaError_t launch_k2_int8(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, const CUtensorMap& tm_y,
                            const CUtensorMap* tm_r, const K2Int8Params& p, int num_sms, cudaStream_t stream) {
-  return tm_r ? launch_k2_int8_impl<true>(tm_xl, tm_l2, tm_y, *tm_r, p, num_sms, stream)
-              : launch_k2_int8_impl<false>(tm_xl, tm_l2, tm_y, tm_y, p, num_sms, stream);
+  if (!tm_r) return launch_k2_int8_impl<false, false>(tm_xl, tm_l2, tm_y, tm_y, p, num_sms, stream);
+  return p.gelu ? launch_k2_int8_impl<true, true>(tm_xl, tm_l2, tm_y, *tm_r, p, num_sms, stream)
+                : launch_k2_int8_impl<true, false>(tm_xl, tm_l2, tm_y, *tm_r, p, num_sms, stream);
 }
 
 }  // namespace svdq
