@@ -129,12 +129,6 @@ struct DeviceGuard {
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 
-// The residual epilogue of a GEMM call: none when residual is null.
-struct Epilogue {
-  const void* residual = nullptr;
-  ResidualParams gate = {};
-};
-
 // Formats with quantized activations (the two-kernel forward): NVFP4, INT4, W8A8.
 bool w4a4(const svdq_layer* L) {
   return L->host.format == SVDQ_NVFP4 || L->host.format == SVDQ_INT4 || L->host.format == SVDQ_W8A8_INT8;
@@ -397,16 +391,10 @@ svdq_status run_k1(const svdq_layer* L, const void* X, int M, void* codes, void*
   return launch_k1(tm_x, L->tm_l1t, tm_c, p, fmt, mode, stream) == cudaSuccess ? SVDQ_OK : SVDQ_ECUDA;
 }
 
-// The output map of a GEMM, and of the residual it adds.
-bool make_out_map(CUtensorMap* m, const void* base, int M, int N) {
-  return make_map(m, base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, N, M, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
-}
-
 svdq_status run_k2_int8(const svdq_layer* L, const void* codes, const void* scales, const void* xl, int M, void* Y,
-                        cudaStream_t stream, bool branch, bool gelu, const Epilogue& epi) {
+                        cudaStream_t stream, bool branch, bool gelu, const ResidualParams& res) {
   const HostPrep& h = L->host;
-  CUtensorMap tm_xl, tm_y, tm_r;
-  if (epi.residual && !make_out_map(&tm_r, epi.residual, M, h.N)) return SVDQ_ECUDA;
+  CUtensorMap tm_xl, tm_y;
   if (!make_map(&tm_y, Y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, h.N, M, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
     return SVDQ_ECUDA;
   if (branch) {
@@ -430,10 +418,8 @@ svdq_status run_k2_int8(const svdq_layer* L, const void* codes, const void* scal
   p.budget_ns = L->budget_ns;
   p.branch = branch ? 1 : 0;
   p.gelu = gelu ? 1 : 0;
-  p.res = epi.gate;
-  return launch_k2_int8(tm_xl, L->tm_l2s, tm_y, epi.residual ? &tm_r : nullptr, p, L->num_sms, stream) == cudaSuccess
-             ? SVDQ_OK
-             : SVDQ_ECUDA;
+  p.res = res;
+  return launch_k2_int8(tm_xl, L->tm_l2s, tm_y, p, L->num_sms, stream) == cudaSuccess ? SVDQ_OK : SVDQ_ECUDA;
 }
 
 // The LoRA adapter's down pass: XL columns 32..63 = bf16(X A), the first
@@ -468,11 +454,10 @@ svdq_status run_upproj(const svdq_layer* L, const void* xl, int xlw, int width, 
 }
 
 svdq_status run_k2_int4(const svdq_layer* L, const void* codes, const void* scales, const void* xl, int M,
-                        void* Y, cudaStream_t stream, bool branch, bool gelu, bool lora_on, const Epilogue& epi) {
+                        void* Y, cudaStream_t stream, bool branch, bool gelu, bool lora_on, const ResidualParams& res) {
   const HostPrep& h = L->host;
   const bool lora = h.lora_r > 0 && lora_on;
-  CUtensorMap tm_a, tm_xl, tm_y, tm_xla, tm_r;
-  if (epi.residual && !make_out_map(&tm_r, epi.residual, M, h.N)) return SVDQ_ECUDA;
+  CUtensorMap tm_a, tm_xl, tm_y, tm_xla;
   if (!make_map(&tm_a, codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, h.K / 2, M, 32, 128, CU_TENSOR_MAP_SWIZZLE_NONE))
     return SVDQ_ECUDA;
   if (!make_map(&tm_y, Y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, h.N, M, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
@@ -509,13 +494,13 @@ svdq_status run_k2_int4(const svdq_layer* L, const void* codes, const void* scal
   p.branch = branch ? 1 : 0;
   p.gelu = gelu ? 1 : 0;
   p.lora = lora ? 1 : 0;
-  p.res = epi.gate;
+  p.res = res;
   // the residual epilogue is the single-CTA kernel's
   const cudaError_t e =
-      L->k2_kernel == 2 && !lora && !epi.residual
+      L->k2_kernel == 2 && !lora && !res.residual
           ? launch_k2_int4_pair(tm_a, L->tm_wq_pair, tm_xl, L->tm_l2s_pair, tm_y, p, L->num_sms, stream)
-          : launch_k2_int4(tm_a, L->tm_wq, tm_xl, L->tm_l2s, tm_y, tm_xla, lora ? L->tm_lora_l2s : L->tm_l2s,
-                           epi.residual ? &tm_r : nullptr, p, L->num_sms, stream);
+          : launch_k2_int4(tm_a, L->tm_wq, tm_xl, L->tm_l2s, tm_y, tm_xla, lora ? L->tm_lora_l2s : L->tm_l2s, p,
+                           L->num_sms, stream);
   return e == cudaSuccess ? SVDQ_OK : SVDQ_ECUDA;
 }
 
@@ -523,13 +508,12 @@ svdq_status run_k2_int4(const svdq_layer* L, const void* codes, const void* scal
 // XL_lora (s B) in its own ring stage, the INT4 GEMM by reloading its branch
 // buffer within the tile; either way into the same accumulator.
 svdq_status run_k2(const svdq_layer* L, const void* codes, const void* scales, const void* xl, int M, void* Y,
-                   cudaStream_t stream, bool branch, bool gelu, bool lora_on = true, const Epilogue& epi = {}) {
-  if (L->host.format == SVDQ_INT4) return run_k2_int4(L, codes, scales, xl, M, Y, stream, branch, gelu, lora_on, epi);
-  if (w8a8(L->host)) return run_k2_int8(L, codes, scales, xl, M, Y, stream, branch, gelu, epi);
+                   cudaStream_t stream, bool branch, bool gelu, bool lora_on = true, const ResidualParams& res = {}) {
+  if (L->host.format == SVDQ_INT4) return run_k2_int4(L, codes, scales, xl, M, Y, stream, branch, gelu, lora_on, res);
+  if (w8a8(L->host)) return run_k2_int8(L, codes, scales, xl, M, Y, stream, branch, gelu, res);
   const HostPrep& h = L->host;
   const bool lora = h.lora_r > 0 && lora_on;
-  CUtensorMap tm_xl, tm_y, tm_xla, tm_r;
-  if (epi.residual && !make_out_map(&tm_r, epi.residual, M, h.N)) return SVDQ_ECUDA;
+  CUtensorMap tm_xl, tm_y, tm_xla;
   if (!make_map(&tm_y, Y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, h.N, M, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
     return SVDQ_ECUDA;
   const uint64_t xl_row = (uint64_t)xl_width(h) * 2;
@@ -568,11 +552,10 @@ svdq_status run_k2(const svdq_layer* L, const void* codes, const void* scales, c
   // The CTA-pair kernel (256 x 256 tiles) is exact but measured slower than the
   // single-CTA kernel on this part; it runs only when SVDQ_K2_KERNEL=pair, and
   // only for layers without a LoRA adapter and calls without a residual.
-  p.res = epi.gate;
-  const bool pair = L->k2_kernel == 2 && !lora && !epi.residual;
+  p.res = res;
+  const bool pair = L->k2_kernel == 2 && !lora && !res.residual;
   const cudaError_t e = pair ? launch_k2_pair(tm_xl, L->tm_l2s_pair, tm_y, p, L->num_sms, stream)
-                             : launch_k2(tm_xl, L->tm_l2s, tm_y, tm_xla, L->tm_lora_l2s,
-                                         epi.residual ? &tm_r : nullptr, p, L->num_sms, stream);
+                             : launch_k2(tm_xl, L->tm_l2s, tm_y, tm_xla, L->tm_lora_l2s, p, L->num_sms, stream);
   return e == cudaSuccess ? SVDQ_OK : SVDQ_ECUDA;
 }
 
@@ -920,24 +903,24 @@ svdq_status run_rope(const svdq_rope* r, const svdq_heads* q, const svdq_heads* 
 
 // The second kernel (the adapter, if any, is added inside it).
 svdq_status run_gemm_stage(const svdq_layer* L, const void* codes, const void* scales, const void* xl, int M,
-                           void* Y, cudaStream_t s, bool branch, bool gelu, bool lora_on, const Epilogue& epi = {}) {
-  return run_k2(L, codes, scales, xl, M, Y, s, branch, gelu, lora_on, epi);
+                           void* Y, cudaStream_t s, bool branch, bool gelu, bool lora_on, const ResidualParams& res = {}) {
+  return run_k2(L, codes, scales, xl, M, Y, s, branch, gelu, lora_on, res);
 }
 
-svdq_status check_residual(const svdq_layer* L, const svdq_residual* r, int M, const void* Y, Epilogue* epi) {
+svdq_status check_residual(const svdq_layer* L, const svdq_residual* r, int M, const void* Y, ResidualParams* out) {
   if (!r || !r->residual || misaligned(r->residual) || misaligned(r->gate)) return SVDQ_EINVAL;
   if (r->gate && (r->rows_per_gate < 0 || r->gate_stride < 0 || r->gate_stride % 8)) return SVDQ_EINVAL;
-  const size_t out = (size_t)M * L->host.N * 2;
-  if (r->residual != Y && overlap(r->residual, out, Y, out)) return SVDQ_EINVAL;
-  epi->residual = r->residual;
-  epi->gate.gate = static_cast<const __nv_bfloat16*>(r->gate);
-  epi->gate.gate_stride = r->gate_stride;
-  epi->gate.rows_per_gate = r->rows_per_gate;
+  const size_t bytes = (size_t)M * L->host.N * 2;
+  if (r->residual != Y && overlap(r->residual, bytes, Y, bytes)) return SVDQ_EINVAL;
+  out->residual = static_cast<const __nv_bfloat16*>(r->residual);
+  out->gate = static_cast<const __nv_bfloat16*>(r->gate);
+  out->gate_stride = r->gate_stride;
+  out->rows_per_gate = r->rows_per_gate;
   return SVDQ_OK;
 }
 
 svdq_status gemm_call(const svdq_layer* L, const void* codes, const void* scales, const void* xl, int M, void* Y,
-                      void* stream, unsigned flags, const Epilogue& epi) {
+                      void* stream, unsigned flags, const ResidualParams& res) {
   if ((reinterpret_cast<uintptr_t>(scales) & 15) || (reinterpret_cast<uintptr_t>(xl) & 15)) return SVDQ_EINVAL;
   svdq_status st = check_forward_args(L, codes, M, Y);
   if (st != SVDQ_OK) return st;
@@ -950,7 +933,7 @@ svdq_status gemm_call(const svdq_layer* L, const void* codes, const void* scales
   DeviceGuard g(L->device);
   if (!g.ok) return SVDQ_ECUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  st = run_gemm_stage(L, codes, scales, xl, M, Y, s, branch, (flags & SVDQ_FWD_GELU) != 0, lora, epi);
+  st = run_gemm_stage(L, codes, scales, xl, M, Y, s, branch, (flags & SVDQ_FWD_GELU) != 0, lora, res);
   if (st == SVDQ_OK && (flags & SVDQ_FWD_CHECK)) st = svdq_check(L, stream);
   return st;
 }
@@ -1603,7 +1586,7 @@ svdq_status svdq_qkv_forward(const svdq_layer* L, const svdq_norm* norm, const v
 svdq_status svdq_gemm_residual(const svdq_layer* L, const void* codes, const void* scales, const void* xl, int M,
                                const svdq_residual* res, void* Y, void* stream, unsigned flags) {
   if (!L || !Y || M < 1) return SVDQ_EINVAL;
-  Epilogue epi;
+  ResidualParams epi = {};
   const svdq_status st = check_residual(L, res, M, Y, &epi);
   if (st != SVDQ_OK) return st;
   if (flags & ~(SVDQ_FWD_GELU | SVDQ_FWD_CHECK | SVDQ_FWD_NO_BRANCH)) return SVDQ_EUNSUPPORTED;
@@ -1613,7 +1596,7 @@ svdq_status svdq_gemm_residual(const svdq_layer* L, const void* codes, const voi
 svdq_status svdq_linear_forward_residual(const svdq_layer* L, const void* X, int M, const svdq_residual* res, void* Y,
                                          void* workspace, size_t workspace_bytes, void* stream, unsigned flags) {
   if (!L || !X || !Y || M < 1) return SVDQ_EINVAL;
-  Epilogue epi;
+  ResidualParams epi = {};
   svdq_status st = check_residual(L, res, M, Y, &epi);
   if (st != SVDQ_OK) return st;
   if (overlap(X, (size_t)M * L->host.K * 2, Y, (size_t)M * L->host.N * 2)) return SVDQ_EINVAL;
@@ -1633,7 +1616,7 @@ svdq_status svdq_mlp_block_forward(const svdq_layer* fc1, const svdq_layer* fc2,
   svdq_status st = check_forward_args(fc1, X, M, Y);
   if (st == SVDQ_EINVAL) return st;
   if (!fc2) return SVDQ_EINVAL;
-  Epilogue epi;
+  ResidualParams epi = {};
   if (norm) {
     const svdq_status sn = check_norm(fc1, norm, X, M);
     if (sn != SVDQ_OK) return sn;

@@ -106,7 +106,7 @@ constexpr int kSFStageCols = 12 * kKB;       // 4 columns of A + 8 of B per K bl
 // Kernel modes: the layer, the chain's fc1, the layer with a residual epilogue
 // (without and with GELU in front of it).
 constexpr int kModeLayer = 0, kModeChain = 1, kModeResidual = 2, kModeResidualGelu = 3;
-constexpr int kResBytes = kEpiWarps * (16 + 256);   // per epilogue warp two load barriers and 128 gate values
+constexpr int kResBytes = kEpiWarps * 256;          // 128 gate values per epilogue warp
 
 template <int kMode>
 struct K2Layout {
@@ -158,7 +158,7 @@ template <int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
     k2_kernel(const __grid_constant__ CUtensorMap tm_xl, const __grid_constant__ CUtensorMap tm_l2,
               const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_xla,
-              const __grid_constant__ CUtensorMap tm_l2a, const __grid_constant__ CUtensorMap tm_r, K2Params p) {
+              const __grid_constant__ CUtensorMap tm_l2a, K2Params p) {
   using Lay = K2Layout<kMode>;
   constexpr bool kChain = kMode == kModeChain, kRes = kMode >= kModeResidual;
   constexpr int kStages = Lay::stages;
@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* rcp_s = reinterpret_cast<float*>(tmem_slot + 4);   // chain mode: the quantizer's constants
-  uint64_t* res_bar = reinterpret_cast<uint64_t*>(epi_buf + kEpiWarps * Lay::epi_warp_bytes + 256);
+  uint4* gates = reinterpret_cast<uint4*>(epi_buf + kEpiWarps * Lay::epi_warp_bytes + 256);   // residual modes
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -213,8 +213,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     dev::mbar_init(acc_full, 1);
     dev::mbar_init(acc_empty, kEpiWarps);
     dev::mbar_init(drain, 1);
-    if (kRes)
-      for (int i = 0; i < 2 * kEpiWarps; ++i) dev::mbar_init(&res_bar[i], 1);
     *abort_flag = 0;
     if (kChain) {
 #pragma unroll
@@ -462,16 +460,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!Lay::deep && lane == 0) dev::tma_prefetch_desc(&tm_y);
       int tcount = 0, chunk = 0;
       bool ok = true;
-      dev::ResidualLoads loads{&tm_r, res_bar + 2 * (warp - kEpiWarp0), wbuf, 0};
+      const dev::ResidualLoads loads{p.res.residual, wbuf, M, N};
       dev::Gate<128> gate;
       if (kRes) {
-        gate.staged = reinterpret_cast<uint4*>(res_bar + 2 * kEpiWarps) + 16 * (warp - kEpiWarp0);
+        gate.staged = gates + 16 * (warp - kEpiWarp0);
         // the residual and the gate may come from the preceding kernel
         dev::griddep_wait();
-        if (lane == 0 && blockIdx.x < ts.units()) {
+        if (blockIdx.x < ts.units())
           for (int c = 0; c < 2; ++c)
-            loads.issue(ts.n0(blockIdx.x, 0) + half * 128 + c * 32, ts.m0(blockIdx.x) + q * 32);
-        }
+            loads.issue(c, ts.n0(blockIdx.x, 0) + half * 128 + c * 32, ts.m0(blockIdx.x) + q * 32);
       }
       for (int u = blockIdx.x; u < ts.units() && ok; u += gridDim.x) {
         for (int t = ts.first(u); t < ts.last(u) && ok; ++t, ++tcount) {
@@ -487,9 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (kRes) {
             gate.tile(p.res, m0 + q * 32, M, n0, N);
-            if (lane == 0)
-              for (int c = 2; c < 4; ++c)
-                if (n0 + c * 32 < N) dev::tma_prefetch_2d(&tm_r, n0 + c * 32, m0 + q * 32);
+            loads.prefetch<64>(n0 + 64, m0 + q * 32);
           }
           const bool got = dev::mbar_wait(acc_full, (uint32_t)tcount & 1u, abort_flag, p.budget_ns);
           if (!__all_sync(0xffffffffu, got)) {          // warp-uniform exit (tcgen05.ld is warp-collective)
@@ -546,13 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 4; ++c, ++chunk) {
             uint32_t (&cur)[32] = c == 0 ? va : c == 1 ? vb : c == 2 ? vc : vd;
             if (kRes) {
-              // the residual's chunk is in the buffer
-              const bool here = loads.wait(chunk, abort_flag, p.budget_ns);
-              if (!__all_sync(0xffffffffu, here)) {
-                if (lane == 0) record_error(p.err, abort_flag, 0x20B);
-                ok = false;
-                break;
-              }
+              loads.wait();                               // the residual's chunk is in the buffer
             } else if (lane == 0) {
               // the buffer of this chunk was last read by the store issued two chunks ago
               dev::bulk_wait_group_read<1>();
@@ -593,13 +582,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) {
               dev::tma_store_2d(&tm_y, buf, n0 + c * 32, m0 + q * 32);
               dev::bulk_commit_group();
-              if (kRes) {
-                // the chunk after next takes this buffer, once the store has read it
-                const int un = c < 2 ? u : u + (int)gridDim.x;
-                if (un < ts.units()) {
-                  dev::bulk_wait_group_read<0>();
-                  loads.issue(ts.n0(un, 0) + half * 128 + ((c + 2) & 3) * 32, ts.m0(un) + q * 32);
-                }
+            }
+            if (kRes) {
+              // the chunk after next takes this buffer, once the store has read it
+              const int un = c < 2 ? u : u + (int)gridDim.x;
+              if (un < ts.units()) {
+                if (lane == 0) dev::bulk_wait_group_read<0>();
+                __syncwarp();
+                loads.issue(chunk & 1, ts.n0(un, 0) + half * 128 + ((c + 2) & 3) * 32, ts.m0(un) + q * 32);
+              } else {
+                loads.skip();
               }
             }
           }
@@ -607,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (kRes && lane == 0) loads.drain(abort_flag, p.budget_ns);
+      if (kRes) dev::cp_async_wait_all();
       if (!Lay::deep && lane == 0) dev::bulk_wait_group_all();
     } else {
       // ---------------------------------------------- chain: fc2's input
@@ -853,8 +845,8 @@ cudaError_t configure_k2() {
 
 template <int kMode>
 cudaError_t launch_k2_impl(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, const CUtensorMap& tm_y,
-                           const CUtensorMap& tm_xla, const CUtensorMap& tm_l2a, const CUtensorMap& tm_r,
-                           const K2Params& p, int grid, cudaStream_t stream) {
+                           const CUtensorMap& tm_xla, const CUtensorMap& tm_l2a, const K2Params& p, int grid,
+                           cudaStream_t stream) {
   cudaError_t e = configure_k2<kMode>();
   if (e != cudaSuccess) return e;
   // Programmatic dependent launch: the prologue (barriers, TMEM, descriptor
@@ -870,20 +862,20 @@ cudaError_t launch_k2_impl(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, c
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k2_kernel<kMode>, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, tm_r, p);
+  return cudaLaunchKernelEx(&cfg, k2_kernel<kMode>, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, p);
 }
 
 }  // namespace
 
 cudaError_t launch_k2(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, const CUtensorMap& tm_y,
-                      const CUtensorMap& tm_xla, const CUtensorMap& tm_l2a, const CUtensorMap* tm_r,
-                      const K2Params& p, int num_sms, cudaStream_t stream) {
+                      const CUtensorMap& tm_xla, const CUtensorMap& tm_l2a, const K2Params& p, int num_sms,
+                      cudaStream_t stream) {
   const int tiles = ((p.M + kBM - 1) / kBM) * ((p.N + kBN - 1) / kBN);
   const int grid = tiles < num_sms ? tiles : num_sms;
-  if (tm_r && p.gelu)
-    return launch_k2_impl<kModeResidualGelu>(tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, *tm_r, p, grid, stream);
-  if (tm_r) return launch_k2_impl<kModeResidual>(tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, *tm_r, p, grid, stream);
-  return launch_k2_impl<kModeLayer>(tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, tm_y, p, grid, stream);
+  if (p.res.residual)
+    return p.gelu ? launch_k2_impl<kModeResidualGelu>(tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, p, grid, stream)
+                  : launch_k2_impl<kModeResidual>(tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, p, grid, stream);
+  return launch_k2_impl<kModeLayer>(tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, p, grid, stream);
 }
 
 int k2_chain_splits(int M, int N, int num_sms) {
@@ -897,8 +889,8 @@ int k2_chain_splits(int M, int N, int num_sms) {
 cudaError_t launch_k2_chain(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, const K2Params& p, int num_sms,
                             cudaStream_t stream) {
   const int units = ((p.M + kBM - 1) / kBM) * p.chain.S;
-  // tm_y, tm_r and the LoRA maps are not used in chain mode: any valid map fills the slots
-  return launch_k2_impl<kModeChain>(tm_xl, tm_l2, tm_l2, tm_l2, tm_l2, tm_l2, p, units < num_sms ? units : num_sms, stream);
+  // tm_y and the LoRA maps are not used in chain mode: any valid map fills the slots
+  return launch_k2_impl<kModeChain>(tm_xl, tm_l2, tm_l2, tm_l2, tm_l2, p, units < num_sms ? units : num_sms, stream);
 }
 
 }  // namespace svdq

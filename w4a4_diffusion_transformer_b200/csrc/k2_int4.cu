@@ -101,10 +101,6 @@ constexpr int kSmemBytes =
     kOStages * kOStageBytes + kBrBytes + kPStages * kPStageBytes + kEpiWarps * kEpiWarpBytes + 256 + kGateBytes + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory per block");
 constexpr int kTmemCols = 512;
-// the barriers' 256 bytes hold the residual's two load barriers per epilogue warp too
-constexpr int kResBar = 160;
-static_assert((2 * kPStages + 2 * kOStages + 2 + 4 + 1) * 8 + 8 <= kResBar && kResBar + kEpiWarps * 16 <= 256,
-              "barrier space");
 
 __device__ __forceinline__ void record_error(int* err, volatile int* abort_flag, int code) {
   atomicCAS(err, 0, code);
@@ -146,8 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     k2_int4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                    const __grid_constant__ CUtensorMap tm_xl, const __grid_constant__ CUtensorMap tm_l2,
                    const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_xla,
-                   const __grid_constant__ CUtensorMap tm_l2a, const __grid_constant__ CUtensorMap tm_r,
-                   K2Int4Params p) {
+                   const __grid_constant__ CUtensorMap tm_l2a, K2Int4Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* oring = smem;                                          // operand ring (1 KiB aligned)
@@ -165,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint64_t* res_bar = reinterpret_cast<uint64_t*>(epi_buf + kEpiWarps * kEpiWarpBytes + kResBar);
+  uint4* gates = reinterpret_cast<uint4*>(epi_buf + kEpiWarps * kEpiWarpBytes + 256);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -194,8 +189,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       dev::mbar_init(&acc_empty[b], kEpiWarps);
     }
     dev::mbar_init(drain, 1);
-    if (kRes)
-      for (int i = 0; i < 2 * kEpiWarps; ++i) dev::mbar_init(&res_bar[i], 1);
     *abort_flag = 0;
     dev::fence_mbar_init();
   }
@@ -430,26 +423,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* wbuf = epi_buf + (warp - kEpiWarp0) * kEpiWarpBytes;
     if (lane == 0) dev::tma_prefetch_desc(&tm_y);
     int tcount = 0, chunk = 0;
-    dev::ResidualLoads loads{&tm_r, res_bar + 2 * (warp - kEpiWarp0), wbuf, 0};
+    const dev::ResidualLoads loads{p.res.residual, wbuf, M, N};
     dev::Gate<256> gate;
     if (kRes) {
-      gate.staged = reinterpret_cast<uint4*>(epi_buf + kEpiWarps * kEpiWarpBytes + 256) + 32 * (warp - kEpiWarp0);
+      gate.staged = gates + 32 * (warp - kEpiWarp0);
       // the residual and the gate may come from the preceding kernel
       dev::griddep_wait();
-      if (lane == 0 && blockIdx.x < num_tiles)
+      if (blockIdx.x < num_tiles)
         for (int c = 0; c < 2; ++c)
-          loads.issue((int)blockIdx.x / tiles_m * kBN + c * 32, (int)blockIdx.x % tiles_m * kBM + q * 32);
+          loads.issue(c, (int)blockIdx.x / tiles_m * kBN + c * 32, (int)blockIdx.x % tiles_m * kBM + q * 32);
     }
-    bool ok = true;
-    for (int tile = blockIdx.x; tile < num_tiles && ok; tile += gridDim.x, ++tcount) {
+    for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++tcount) {
       const int m0 = (tile % tiles_m) * kBM;
       const int n0 = (tile / tiles_m) * kBN;
       const int ab = tcount & 1;
       if (kRes) {
         gate.tile(p.res, m0 + q * 32, M, n0, N);
-        if (lane == 0)
-          for (int c = 2; c < 8; ++c)
-            if (n0 + c * 32 < N) dev::tma_prefetch_2d(&tm_r, n0 + c * 32, m0 + q * 32);
+        loads.prefetch<192>(n0 + 64, m0 + q * 32);
       }
       const bool got = dev::mbar_wait(&acc_full[ab], (uint32_t)(tcount >> 1) & 1u, abort_flag, p.budget_ns);
       if (!__all_sync(0xffffffffu, got)) {          // warp-uniform exit (tcgen05.ld is warp-collective)
@@ -480,13 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           bias[4 * f + 3] = b4.w;
         }
         if (kRes) {
-          // the residual's chunk is in the buffer (after a wait that ran out the
-          // chunk is still finished, so that the accumulator is handed back)
-          const bool here = loads.wait(chunk, abort_flag, p.budget_ns);
-          if (!__all_sync(0xffffffffu, here)) {
-            if (lane == 0 && ok) record_error(p.err, abort_flag, 0x308);
-            ok = false;
-          }
+          loads.wait();                                 // the residual's chunk is in the buffer
         } else if (lane == 0) {
           // the buffer of this chunk was last read by the store issued two chunks ago
           dev::bulk_wait_group_read<1>();
@@ -524,13 +508,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           dev::tma_store_2d(&tm_y, buf, n0 + c * 32, m0 + q * 32);
           dev::bulk_commit_group();
-          if (kRes && ok) {
-            // the chunk after next takes this buffer, once the store has read it
-            const int tn = c < 6 ? tile : tile + (int)gridDim.x;
-            if (tn < num_tiles) {
-              dev::bulk_wait_group_read<0>();
-              loads.issue(tn / tiles_m * kBN + ((c + 2) & 7) * 32, tn % tiles_m * kBM + q * 32);
-            }
+        }
+        if (kRes) {
+          // the chunk after next takes this buffer, once the store has read it
+          const int tn = c < 6 ? tile : tile + (int)gridDim.x;
+          if (tn < num_tiles) {
+            if (lane == 0) dev::bulk_wait_group_read<0>();
+            __syncwarp();
+            loads.issue(chunk & 1, tn / tiles_m * kBN + ((c + 2) & 7) * 32, tn % tiles_m * kBM + q * 32);
+          } else {
+            loads.skip();
           }
         }
         if (c + 1 < 8) dev::tmem_load_wait(nxt);
@@ -543,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     }
-    if (kRes && lane == 0) loads.drain(abort_flag, p.budget_ns);
+    if (kRes) dev::cp_async_wait_all();
     if (lane == 0) dev::bulk_wait_group_all();
   }
 
@@ -564,8 +551,7 @@ namespace {
 template <bool kRes, bool kResGelu>
 cudaError_t launch_k2_int4_impl(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const CUtensorMap& tm_xl,
                                 const CUtensorMap& tm_l2, const CUtensorMap& tm_y, const CUtensorMap& tm_xla,
-                                const CUtensorMap& tm_l2a, const CUtensorMap& tm_r, const K2Int4Params& p,
-                                int num_sms, cudaStream_t stream) {
+                                const CUtensorMap& tm_l2a, const K2Int4Params& p, int num_sms, cudaStream_t stream) {
   static thread_local int configured_device = -1;
   int dev = 0;
   cudaGetDevice(&dev);
@@ -591,20 +577,18 @@ cudaError_t launch_k2_int4_impl(const CUtensorMap& tm_a, const CUtensorMap& tm_b
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k2_int4_kernel<kRes, kResGelu>, tm_a, tm_b, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, tm_r, p);
+  return cudaLaunchKernelEx(&cfg, k2_int4_kernel<kRes, kResGelu>, tm_a, tm_b, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, p);
 }
 
 }  // namespace
 
 cudaError_t launch_k2_int4(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const CUtensorMap& tm_xl,
                            const CUtensorMap& tm_l2, const CUtensorMap& tm_y, const CUtensorMap& tm_xla,
-                           const CUtensorMap& tm_l2a, const CUtensorMap* tm_r, const K2Int4Params& p, int num_sms,
-                           cudaStream_t stream) {
-  if (!tm_r)
-    return launch_k2_int4_impl<false, false>(tm_a, tm_b, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, tm_y, p, num_sms, stream);
-  return p.gelu
-             ? launch_k2_int4_impl<true, true>(tm_a, tm_b, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, *tm_r, p, num_sms, stream)
-             : launch_k2_int4_impl<true, false>(tm_a, tm_b, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, *tm_r, p, num_sms, stream);
+                           const CUtensorMap& tm_l2a, const K2Int4Params& p, int num_sms, cudaStream_t stream) {
+  if (!p.res.residual)
+    return launch_k2_int4_impl<false, false>(tm_a, tm_b, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, p, num_sms, stream);
+  return p.gelu ? launch_k2_int4_impl<true, true>(tm_a, tm_b, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, p, num_sms, stream)
+                : launch_k2_int4_impl<true, false>(tm_a, tm_b, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, p, num_sms, stream);
 }
 
 }  // namespace svdq

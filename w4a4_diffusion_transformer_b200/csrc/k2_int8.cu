@@ -54,8 +54,8 @@ constexpr int kBrXL = kBM * 64;              // XL rows (32 BF16, the rank in th
 constexpr int kBrBytes = kBrXL + kBN * 64;
 constexpr int kEpiBufBytes = 32 * 64;
 constexpr int kEpiWarpBytes = 2 * kEpiBufBytes + 1024;   // two chunk buffers + 128 bias + 128 s_w floats
-constexpr int kResBytes = kEpiWarps * (16 + 256);        // per epilogue warp two load barriers and 128 gate values
-constexpr int kSmemBytes = kStages * kStageBytes + kBrBytes + kEpiWarps * kEpiWarpBytes + 1024 + 256 + kResBytes;
+constexpr int kGateBytes = kEpiWarps * 256;              // 128 gate values per epilogue warp
+constexpr int kSmemBytes = kStages * kStageBytes + kBrBytes + kEpiWarps * kEpiWarpBytes + 1024 + 256 + kGateBytes;
 static_assert(kSmemBytes <= 232448, "shared memory per block");
 constexpr int kTmemCols = 512;
 constexpr int kBranchCol = 256;
@@ -84,8 +84,7 @@ __device__ __forceinline__ void record_error(int* err, volatile int* abort_flag,
 template <bool kRes, bool kResGelu>
 __global__ void __launch_bounds__(kThreads, 1)
     k2_int8_kernel(const __grid_constant__ CUtensorMap tm_xl, const __grid_constant__ CUtensorMap tm_l2,
-                   const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_r,
-                   K2Int8Params p) {
+                   const __grid_constant__ CUtensorMap tm_y, K2Int8Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* brbuf = smem + kStages * kStageBytes;
@@ -99,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* drain = acc_empty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  uint64_t* res_bar = reinterpret_cast<uint64_t*>(epi_buf + kEpiWarps * kEpiWarpBytes + 256);
+  uint4* gates = reinterpret_cast<uint4*>(epi_buf + kEpiWarps * kEpiWarpBytes + 256);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -120,8 +119,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     dev::mbar_init(acc_full, 1);
     dev::mbar_init(acc_empty, kEpiWarps);
     dev::mbar_init(drain, 1);
-    if (kRes)
-      for (int i = 0; i < 2 * kEpiWarps; ++i) dev::mbar_init(&res_bar[i], 1);
     *abort_flag = 0;
     dev::fence_mbar_init();
   }
@@ -251,19 +248,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* sw_s = bias_s + 128;
     if (lane == 0) dev::tma_prefetch_desc(&tm_y);
     int tcount = 0, chunk = 0;
-    dev::ResidualLoads loads{&tm_r, res_bar + 2 * (warp - kEpiWarp0), wbuf, 0};
+    const dev::ResidualLoads loads{p.res.residual, wbuf, M, N};
     dev::Gate<128> gate;
     if (kRes) {
-      gate.staged = reinterpret_cast<uint4*>(res_bar + 2 * kEpiWarps) + 16 * (warp - kEpiWarp0);
+      gate.staged = gates + 16 * (warp - kEpiWarp0);
       // the residual and the gate may come from the preceding kernel
       dev::griddep_wait();
-      if (lane == 0 && blockIdx.x < num_tiles)
+      if (blockIdx.x < num_tiles)
         for (int c = 0; c < 2; ++c)
-          loads.issue((int)blockIdx.x / tiles_m * kBN + half * 128 + c * 32,
-                      (int)blockIdx.x % tiles_m * kBM + q * 32);
+          loads.issue(c, (int)blockIdx.x / tiles_m * kBN + half * 128 + c * 32, (int)blockIdx.x % tiles_m * kBM + q * 32);
     }
-    bool ok = true;
-    for (int tile = blockIdx.x; tile < num_tiles && ok; tile += gridDim.x, ++tcount) {
+    for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++tcount) {
       const int m0 = (tile % tiles_m) * kBM;
       const int n0 = (tile / tiles_m) * kBN + half * 128;
       {
@@ -278,9 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (kRes) {
         gate.tile(p.res, m0 + q * 32, M, n0, N);
-        if (lane == 0)
-          for (int c = 2; c < 4; ++c)
-            if (n0 + c * 32 < N) dev::tma_prefetch_2d(&tm_r, n0 + c * 32, m0 + q * 32);
+        loads.prefetch<64>(n0 + 64, m0 + q * 32);
       }
       const bool got = dev::mbar_wait(acc_full, (uint32_t)tcount & 1u, abort_flag, p.budget_ns);
       if (!__all_sync(0xffffffffu, got)) {
@@ -324,13 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < 4; ++c, ++chunk) {
         uint32_t (&cur)[32] = c == 0 ? va : c == 1 ? vb : c == 2 ? vc : vd;
         if (kRes) {
-          // the residual's chunk is in the buffer
-          const bool here = loads.wait(chunk, abort_flag, p.budget_ns);
-          if (!__all_sync(0xffffffffu, here)) {
-            if (lane == 0) record_error(p.err, abort_flag, 0x507);
-            ok = false;
-            break;
-          }
+          loads.wait();                                 // the residual's chunk is in the buffer
         } else if (lane == 0) {
           dev::bulk_wait_group_read<1>();
         }
@@ -369,19 +356,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           dev::tma_store_2d(&tm_y, buf, n0 + c * 32, m0 + q * 32);
           dev::bulk_commit_group();
-          if (kRes) {
-            // the chunk after next takes this buffer, once the store has read it
-            const int tn = c < 2 ? tile : tile + (int)gridDim.x;
-            if (tn < num_tiles) {
-              dev::bulk_wait_group_read<0>();
-              loads.issue(tn / tiles_m * kBN + half * 128 + ((c + 2) & 3) * 32, tn % tiles_m * kBM + q * 32);
-            }
+        }
+        if (kRes) {
+          // the chunk after next takes this buffer, once the store has read it
+          const int tn = c < 2 ? tile : tile + (int)gridDim.x;
+          if (tn < num_tiles) {
+            if (lane == 0) dev::bulk_wait_group_read<0>();
+            __syncwarp();
+            loads.issue(chunk & 1, tn / tiles_m * kBN + half * 128 + ((c + 2) & 3) * 32, tn % tiles_m * kBM + q * 32);
+          } else {
+            loads.skip();
           }
         }
       }
       __syncwarp();
     }
-    if (kRes && lane == 0) loads.drain(abort_flag, p.budget_ns);
+    if (kRes) dev::cp_async_wait_all();
     if (lane == 0) dev::bulk_wait_group_all();
   }
 
@@ -405,7 +395,7 @@ namespace {
 
 template <bool kRes, bool kResGelu>
 cudaError_t launch_k2_int8_impl(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, const CUtensorMap& tm_y,
-                                const CUtensorMap& tm_r, const K2Int8Params& p, int num_sms, cudaStream_t stream) {
+                                const K2Int8Params& p, int num_sms, cudaStream_t stream) {
   static thread_local int configured_device = -1;
   int dev = 0;
   cudaGetDevice(&dev);
@@ -429,16 +419,16 @@ cudaError_t launch_k2_int8_impl(const CUtensorMap& tm_xl, const CUtensorMap& tm_
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k2_int8_kernel<kRes, kResGelu>, tm_xl, tm_l2, tm_y, tm_r, p);
+  return cudaLaunchKernelEx(&cfg, k2_int8_kernel<kRes, kResGelu>, tm_xl, tm_l2, tm_y, p);
 }
 
 }  // namespace
 
 cudaError_t launch_k2_int8(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, const CUtensorMap& tm_y,
-                           const CUtensorMap* tm_r, const K2Int8Params& p, int num_sms, cudaStream_t stream) {
-  if (!tm_r) return launch_k2_int8_impl<false, false>(tm_xl, tm_l2, tm_y, tm_y, p, num_sms, stream);
-  return p.gelu ? launch_k2_int8_impl<true, true>(tm_xl, tm_l2, tm_y, *tm_r, p, num_sms, stream)
-                : launch_k2_int8_impl<true, false>(tm_xl, tm_l2, tm_y, *tm_r, p, num_sms, stream);
+                           const K2Int8Params& p, int num_sms, cudaStream_t stream) {
+  if (!p.res.residual) return launch_k2_int8_impl<false, false>(tm_xl, tm_l2, tm_y, p, num_sms, stream);
+  return p.gelu ? launch_k2_int8_impl<true, true>(tm_xl, tm_l2, tm_y, p, num_sms, stream)
+                : launch_k2_int8_impl<true, false>(tm_xl, tm_l2, tm_y, p, num_sms, stream);
 }
 
 }  // namespace svdq

@@ -54,9 +54,9 @@ struct K2Chain {
   float rcp[16];                // the quantizer's reciprocal constants (K1Params::rcp)
 };
 
-// Residual epilogue of the GEMMs: Y = bf16(residual + gate * y); the residual
-// itself comes through a tensor map.
+// Residual epilogue of the GEMMs: Y = bf16(residual + gate * y).
 struct ResidualParams {
+  const __nv_bfloat16* residual;  // [M][N], or null: no residual
   const __nv_bfloat16* gate;    // rows of N, gate_stride elements apart, or null
   long long gate_stride;
   int rows_per_gate;            // 0: one row for all tokens
@@ -78,7 +78,7 @@ struct K2Params {
   int gelu;                     // 1: tanh-GELU epilogue
   int lora;                     // 1: one more ring stage per tile adds XL_lora (s B / alpha) (tm_xla, tm_l2a)
   K2Chain chain;                // launch_k2_chain only
-  ResidualParams res;           // with a residual map
+  ResidualParams res;
 };
 
 struct K2Int4Params {
@@ -95,7 +95,7 @@ struct K2Int4Params {
   int branch;                   // 1: add XL (L2b / alpha) into the accumulator
   int gelu;                     // 1: tanh-GELU epilogue
   int lora;                     // 1: add XL_lora (s B / alpha) too (tm_xla, tm_l2a), same accumulator
-  ResidualParams res;           // with a residual map
+  ResidualParams res;
 };
 
 struct K2Int8Params {
@@ -110,7 +110,7 @@ struct K2Int8Params {
   unsigned long long budget_ns;
   int branch;                   // 1: add XL L2b (rank 16) from its own accumulator
   int gelu;
-  ResidualParams res;           // with a residual map
+  ResidualParams res;
 };
 
 struct UpParams {
@@ -212,11 +212,10 @@ cudaError_t launch_rope(RopeParams p, int num_sms, cudaStream_t stream);
 // NVFP4 GEMM: operands from p.acodes / p.sfa (the first kernel's layouts) and
 // p.wmerged; tm_xl / tm_l2 the branch tiles, tm_y the output; with p.lora,
 // tm_xla / tm_l2a the LoRA tiles (XL_lora [M][32], (s B / alpha)^T [N][32]; the
-// same boxes and swizzle as tm_xl / tm_l2).  tm_r, here and in the GEMMs below:
-// the residual of the epilogue, a map like tm_y's, or null.
+// same boxes and swizzle as tm_xl / tm_l2).
 cudaError_t launch_k2(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, const CUtensorMap& tm_y,
-                      const CUtensorMap& tm_xla, const CUtensorMap& tm_l2a, const CUtensorMap* tm_r,
-                      const K2Params& p, int num_sms, cudaStream_t stream);
+                      const CUtensorMap& tm_xla, const CUtensorMap& tm_l2a, const K2Params& p, int num_sms,
+                      cudaStream_t stream);
 int k2_block_n();
 // The same GEMM in chain mode (p.chain; Y is not written): CTA c owns 128-row
 // block c / S and the c % S-th of S contiguous ranges of N tiles.
@@ -249,8 +248,7 @@ void k2_pair_pack_weights(const uint8_t* tiled_codes, const uint8_t* sf, int N, 
 // codes [N][K/2] (box 32 B x 256 rows), both unswizzled.
 cudaError_t launch_k2_int4(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const CUtensorMap& tm_xl,
                            const CUtensorMap& tm_l2, const CUtensorMap& tm_y, const CUtensorMap& tm_xla,
-                           const CUtensorMap& tm_l2a, const CUtensorMap* tm_r, const K2Int4Params& p, int num_sms,
-                           cudaStream_t stream);
+                           const CUtensorMap& tm_l2a, const K2Int4Params& p, int num_sms, cudaStream_t stream);
 // The INT4 GEMM on CTA pairs (256 x 256 tiles, clusters of two): tm_b and tm_l2
 // with boxes of k2_int4_pair_rows_b() rows.
 int k2_int4_pair_rows_b();
@@ -261,7 +259,7 @@ cudaError_t launch_k2_int4_pair(const CUtensorMap& tm_a, const CUtensorMap& tm_b
 // W8A8 GEMM (tcgen05 kind::i8): tm_xl / tm_l2 the branch tiles (as for the
 // NVFP4 GEMM, L2b unscaled), tm_y the output.
 cudaError_t launch_k2_int8(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, const CUtensorMap& tm_y,
-                           const CUtensorMap* tm_r, const K2Int8Params& p, int num_sms, cudaStream_t stream);
+                           const K2Int8Params& p, int num_sms, cudaStream_t stream);
 size_t k2_int8_weight_bytes(int N, int K);
 
 // Y is read and rewritten through tm_y: a BF16 [M][N] map with boxes of 64
