@@ -539,8 +539,8 @@ typedef struct {
  *              elements between sequences (0: shared).  A non-finite position
  *              gives NaN in the pairs that use it.
  * Runs on the device that holds q->in, whichever is current.  Errors:
- * SVDQ_EINVAL (NULL rope, q, positions or a tensor's pointers, sizes below 1,
- * strides, alignment, overlap, flags, theta or eps out of range, memory that is
+ * SVDQ_EINVAL (NULL rope, q, positions or a tensor's pointers, sizes below 1, a
+ * batch above 65535, strides, alignment, overlap, flags, theta or eps out of range, memory that is
  * not device memory), SVDQ_EUNSUPPORTED (head_dim, dims as above), SVDQ_ECUDA. */
 svdq_status svdq_rope_heads(const svdq_rope* rope, const svdq_heads* q, const svdq_heads* k, int batch, int T,
                             const float* positions, int64_t pos_batch, void* stream);

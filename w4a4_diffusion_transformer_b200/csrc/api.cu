@@ -892,10 +892,19 @@ svdq_status run_rope(const svdq_rope* r, const svdq_heads* q, const svdq_heads* 
     p.R += r->dim[a];
   }
   p.half = (r->flags & SVDQ_ROPE_HALF) ? 1 : 0;
-  p.span = (r->flags & SVDQ_ROPE_SPAN) ? 1 : 0;
   p.norm = (r->flags & SVDQ_ROPE_NORM) ? 1 : 0;
   p.eps = r->eps;
-  p.log2_theta = std::log2(r->theta);
+  // Frequencies in turns per position.  Each is the one before times a constant:
+  // after 127 products the relative error is below 2^-45, which a position of
+  // 2^24 turns into 2^-23 of a turn.
+  const double log2_theta = std::log2(r->theta), turn = 0.15915494309189533577;   // 1 / (2 pi)
+  const bool span = (r->flags & SVDQ_ROPE_SPAN) != 0;
+  double f = turn;
+  for (int a = 0, i = 0; a < r->axes; ++a) {
+    const double ratio = std::exp2(-2.0 * log2_theta / (span ? p.R : r->dim[a]));
+    if (!span) f = turn;
+    for (int k = 0; k < r->dim[a] / 2; ++k, f *= ratio) p.turns[i++] = f;
+  }
   p.positions = positions;
   p.pos_batch = pos_batch;
   return launch_rope(p, num_sms, stream) == cudaSuccess ? SVDQ_OK : SVDQ_ECUDA;
@@ -1527,7 +1536,7 @@ svdq_status svdq_norm_linear_forward(const svdq_layer* L, const svdq_norm* norm,
 
 svdq_status svdq_rope_heads(const svdq_rope* rope, const svdq_heads* q, const svdq_heads* k, int batch, int T,
                             const float* positions, int64_t pos_batch, void* stream) {
-  if (!q || !positions || batch < 1 || T < 1 || (int64_t)batch * T > INT_MAX || pos_batch < 0 ||
+  if (!q || !positions || batch < 1 || batch > 65535 || T < 1 || (int64_t)batch * T > INT_MAX || pos_batch < 0 ||
       (reinterpret_cast<uintptr_t>(positions) & 3))
     return SVDQ_EINVAL;
   svdq_status st = check_rope(rope);
@@ -1548,7 +1557,7 @@ svdq_status svdq_qkv_forward(const svdq_layer* L, const svdq_norm* norm, const v
                              const svdq_rope* rope, int q_heads, int k_heads, const void* q_weight,
                              const void* k_weight, const float* positions, int64_t pos_batch, void* Y,
                              void* workspace, size_t workspace_bytes, void* stream, unsigned flags) {
-  if (!L || !X || !Y || !positions || batch < 1 || T < 1 || (int64_t)batch * T > INT_MAX || pos_batch < 0 ||
+  if (!L || !X || !Y || !positions || batch < 1 || batch > 65535 || T < 1 || (int64_t)batch * T > INT_MAX || pos_batch < 0 ||
       (reinterpret_cast<uintptr_t>(positions) & 3) || q_heads < 1 || k_heads < 0)
     return SVDQ_EINVAL;
   svdq_status st = check_rope(rope);

@@ -200,14 +200,14 @@ struct RopeParams {
   int B, T, D;
   int R;                        // rotated values of a head
   int axes, dim[4];
-  int half, span, norm;
+  int half, norm;
   float eps;
-  double log2_theta;
+  double turns[128];            // turns per position of each pair: theta^(-2i/d) / (2 pi)
   const float* positions;       // [B or 1][T][axes]
   long long pos_batch;
-  int splits;                   // warps that share a token (set by the launcher)
+  int log2_splits, log2_pairs;  // warps that share a token, angles kept per token (set by the launcher)
 };
-cudaError_t launch_rope(RopeParams p, int num_sms, cudaStream_t stream);
+cudaError_t launch_rope(RopeParams& p, int num_sms, cudaStream_t stream);
 
 // NVFP4 GEMM: operands from p.acodes / p.sfa (the first kernel's layouts) and
 // p.wmerged; tm_xl / tm_l2 the branch tiles, tm_y the output; with p.lora,

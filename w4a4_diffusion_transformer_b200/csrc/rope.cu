@@ -14,11 +14,20 @@
 // becomes FP32: positions of many thousands keep their angle to FP32 accuracy.
 // Everything else is FP32 with one rounding to BF16.
 //
-// Memory bound: every value of q and k is read and written once.  A warp takes
-// one token (S warps share one when there are few): its lanes own 8 consecutive
-// values of a head, so the cosines and sines of a lane are computed once per
-// token and stay in registers for all heads, and its frequencies once per
-// kernel.
+// Memory bound: every value of q and k is read and written once.  A CTA takes
+// 4 / S tokens of a sequence, S warps to a token.  Its threads first form the
+// tokens' angles together (as every warp's own work, with the frequencies, they
+// cost more than the rotation itself) while each warp's first heads are already
+// on their way.  A lane then
+// owns 8 consecutive values of a head: the products of its weights with its
+// cosines and sines stay in registers for all heads, so that a head costs its
+// norm and two multiply-adds a value.
+//
+// 4608 tokens, 24 + 24 heads of 128: 21.6 us, 5.25 TB/s of a copy's 6.56 (a warp
+// per token with its own angles: 40.3); 2 x 14040 tokens, 12 + 12 heads: 70.0 us,
+// 4.93 TB/s.  What counts is warps in flight: 32 per SM at 64 registers (24 at
+// 80: 27.0 us), and few instructions in front of a token's heads (8 head steps
+// a warp instead of 24: 27.0 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -29,7 +38,8 @@ namespace svdq {
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
+constexpr int kSteps = 32;                              // head steps of a warp when there are tokens enough
 constexpr int kUnroll = 4;                              // heads in flight per lane
 
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
@@ -40,138 +50,172 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// kLanes lanes hold a head (the power of two that holds D / 8).
-template <int kLanes, bool kHalf>
-__device__ __forceinline__ void rotate_heads(const RopeParams& p, const RopeTensor& t, int b, int tok, int split,
-                                             const float (&cs)[kHalf ? 8 : 4], const float (&sn)[kHalf ? 8 : 4],
-                                             int partner, int turned) {
-  constexpr int kPerWarp = 32 / kLanes;                 // heads a warp handles at once
-  const int lane = threadIdx.x & 31;
-  const int c = lane % kLanes, sub = lane / kLanes;
-  const bool act = 8 * c < p.D;
-  const __nv_bfloat16* in = t.in + b * t.in_batch + tok * t.in_token + 8 * c;
-  __nv_bfloat16* out = t.out + b * t.out_batch + tok * t.out_token + 8 * c;
-  // the weight of this lane's values, and (halves) of its partner's
-  uint4 wq = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u), wp = wq;
-  if (t.weight && act) {
-    wq = *reinterpret_cast<const uint4*>(t.weight + 8 * c);
-    if (kHalf) wp = *reinterpret_cast<const uint4*>(t.weight + 8 * (partner % kLanes));
-  }
-  const uint32_t wa[4] = {wq.x, wq.y, wq.z, wq.w}, wb[4] = {wp.x, wp.y, wp.z, wp.w};
-  const float invD = 1.0f / (float)p.D;
-  const int step = kPerWarp * p.splits;
-  for (int h0 = split * kPerWarp; h0 < t.heads; h0 += step * kUnroll) {
-    uint4 raw[kUnroll];
+// The heads of one tensor that a warp takes of its token: h0, h0 + step, ...
+struct Walk {
+  const __nv_bfloat16* in;                              // this lane's values of the next head to load
+  __nv_bfloat16* out;                                   // ... to store
+  long long in_step, out_step;
+  int loads, stores;                                    // heads left
+
+  __device__ __forceinline__ void load(uint4 (&raw)[kUnroll]) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int h = h0 + u * step + sub;
       raw[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (act && h < t.heads) raw[u] = *reinterpret_cast<const uint4*>(in + h * t.in_head);
+      if (loads > 0) raw[u] = *reinterpret_cast<const uint4*>(in);
+      in += in_step;
+      --loads;
     }
+  }
+  __device__ __forceinline__ void store(const uint4& v) {
+    if (stores > 0) *reinterpret_cast<uint4*>(out) = v;
+    out += out_step;
+    --stores;
+  }
+};
+
+template <int kLanes>
+__device__ __forceinline__ Walk walk(const RopeParams& p, const RopeTensor& t, int b, int tok, int split) {
+  const int lane = threadIdx.x & 31, c = lane % kLanes;
+  const int h0 = split * (32 / kLanes) + lane / kLanes, step = (32 / kLanes) << p.log2_splits;
+  Walk w;
+  w.in = t.in + b * t.in_batch + tok * t.in_token + h0 * t.in_head + 8 * c;
+  w.out = t.out + b * t.out_batch + tok * t.out_token + h0 * t.out_head + 8 * c;
+  w.in_step = step * t.in_head;
+  w.out_step = step * t.out_head;
+  w.loads = 8 * c < p.D && tok < p.T ? (t.heads - h0 + step - 1) / step : 0;
+  w.stores = w.loads;
+  return w;
+}
+
+// One tensor's heads.  kLanes lanes hold a head (the power of two that holds
+// D / 8); raw: the first heads, already loaded; angle: cosine and sine of this
+// lane's first pair.
+template <int kLanes, bool kHalf>
+__device__ __forceinline__ void rotate_heads(const RopeParams& p, const RopeTensor& t, Walk& w,
+                                             uint4 (&raw)[kUnroll], const float2* angle, int partner, int turned,
+                                             float sign) {
+  const int c = (threadIdx.x & 31) % kLanes;
+  // out = x a + (the pair's other value) b, both with the weight that x and the
+  // other carry; the head's 1 / sqrt follows
+  float2 a[4], b[4];
+  {
+    uint4 q = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u), o = q;   // ones
+    if (p.norm && t.weight && 8 * c < p.D) {
+      q = *reinterpret_cast<const uint4*>(t.weight + 8 * c);
+      o = *reinterpret_cast<const uint4*>(t.weight + 8 * (partner % kLanes));
+    }
+    const uint32_t qs[4] = {q.x, q.y, q.z, q.w}, os[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = unpack2(qs[i]);
+      if (kHalf) {
+        float2 u = make_float2(1.f, 0.f), v = u;
+        if (turned > 0) {
+          u = angle[2 * i];
+          v = angle[2 * i + 1];
+        }
+        const float2 y = unpack2(os[i]);
+        a[i] = make_float2(x.x * u.x, x.y * v.x);
+        b[i] = make_float2(sign * y.x * u.y, sign * y.y * v.y);
+      } else {
+        const float2 u = i < turned ? angle[i] : make_float2(1.f, 0.f);
+        a[i] = make_float2(x.x * u.x, x.y * u.x);
+        b[i] = make_float2(-x.y * u.y, x.x * u.y);
+      }
+    }
+  }
+  const float invD = 1.0f / (float)p.D;
+  const bool whole = p.R == p.D;                        // every value of a head turns
+  const int step = (32 / kLanes) << p.log2_splits;
+  for (int h = 0; h < t.heads; h += kUnroll * step) {   // uniform over the warp: the shuffles need every lane
+    if (h > 0) w.load(raw);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int h = h0 + u * step + sub;
-      const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+      if (u > 0 && h + u * step >= t.heads) break;      // uniform too
+      const uint32_t x[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
       float2 v[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = unpack2(w[i]);
-      float r = 1.0f;
+      for (int k = 0; k < 4; ++k) v[k] = unpack2(x[k]);
+      float2 r2 = make_float2(1.f, 1.f);
       if (p.norm) {
-        float2 a = make_float2(0.f, 0.f);
+        float2 q = __fmul2_rn(v[0], v[0]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a = __ffma2_rn(v[i], v[i], a);
-        float s = a.x + a.y;
+        for (int k = 1; k < 4; ++k) q = __ffma2_rn(v[k], v[k], q);
+        float s = q.x + q.y;
 #pragma unroll
         for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        r = rsqrtf(s * invD + p.eps);
-      }
-      const float2 r2 = make_float2(r, r);
-      float2 q[4];                                      // halves: the partner's values
-      if (kHalf) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          q[i] = unpack2(__shfl_sync(0xffffffffu, w[i], partner));
-          if (p.norm) q[i] = __fmul2_rn(__fmul2_rn(q[i], r2), unpack2(wb[i]));
-        }
-      }
-      if (p.norm) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = __fmul2_rn(__fmul2_rn(v[i], r2), unpack2(wa[i]));
+        r2.x = r2.y = rsqrtf(s * invD + p.eps);
       }
       uint32_t o[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (kHalf)                                      // sn carries the sign of this lane's half
-          o[i] = pack2(v[i].x * cs[(2 * i) & 7] + q[i].x * sn[(2 * i) & 7],
-                       v[i].y * cs[(2 * i + 1) & 7] + q[i].y * sn[(2 * i + 1) & 7]);
-        else
-          o[i] = pack2(v[i].x * cs[i & 3] - v[i].y * sn[i & 3], v[i].y * cs[i & 3] + v[i].x * sn[i & 3]);
-        // values past the span are not multiplied at all: an infinity or NaN
-        // beside one stays where it is
-        if (i >= turned) o[i] = pack2(v[i].x, v[i].y);
+      for (int k = 0; k < 4; ++k) {
+        const float2 other = kHalf ? unpack2(__shfl_sync(0xffffffffu, x[k], partner)) : make_float2(v[k].y, v[k].x);
+        const float2 y = __fmul2_rn(__ffma2_rn(v[k], a[k], __fmul2_rn(other, b[k])), r2);
+        o[k] = pack2(y.x, y.y);
       }
-      if (act && h < t.heads) *reinterpret_cast<uint4*>(out + h * t.out_head) = make_uint4(o[0], o[1], o[2], o[3]);
+      if (!whole) {
+        // values past the span are not multiplied by a sine at all: an infinity
+        // or NaN beside one stays where it is
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 y = __fmul2_rn(__fmul2_rn(v[k], a[k]), r2);
+          if (k >= turned) o[k] = pack2(y.x, y.y);
+        }
+      }
+      w.store(make_uint4(o[0], o[1], o[2], o[3]));
     }
   }
 }
 
 template <int kLanes, bool kHalf>
-__global__ void __launch_bounds__(kWarps * 32) rope_kernel(const RopeParams p) {
-  constexpr int kAng = kHalf ? 8 : 4;                   // angles of a lane's 8 values
+__global__ void __launch_bounds__(kWarps * 32, 8) rope_kernel(const __grid_constant__ RopeParams p) {
+  __shared__ float2 angles[kWarps * 128];               // cosine, sine of [token][pair]
   dev::griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, c = lane % kLanes;
-  const int R2 = p.R / 2;
-  // this lane's frequencies in turns per position, and their axes
-  double freq[kAng];
-  int axis[kAng];
-  // this lane's pairs of neighbouring values that turn: its first `turned`
-  const int turned = max(0, min(4, (p.R - 8 * c) / 2));
-#pragma unroll
-  for (int i = 0; i < kAng; ++i) {
-    int pr = kHalf ? 8 * c + i : 4 * c + i;
-    bool in = kHalf ? 8 * c + i < p.R : pr < R2;
-    if (kHalf && pr >= R2) pr -= R2;
-    freq[i] = 0.0;
-    axis[i] = 0;
-    if (in) {
-      int first = 0, a = 0;
-      while (a + 1 < p.axes && pr >= first + p.dim[a] / 2) first += p.dim[a++] / 2;
-      const double e = p.span ? 2.0 * pr / p.R : 2.0 * (pr - first) / p.dim[a];
-      freq[i] = exp2(-e * p.log2_theta) * 0.15915494309189533577;   // 1 / (2 pi)
-      axis[i] = a;
-    }
-  }
-  int partner = lane;
-  float sign = 1.0f;
-  if (kHalf && 8 * c < p.R) {
-    const bool first = 8 * c < R2;
-    partner = first ? lane + R2 / 8 : lane - R2 / 8;
-    sign = first ? -1.0f : 1.0f;
-  }
   dev::griddep_wait();                                  // q, k and the positions may be the preceding kernel's
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % kLanes;
+  const int R2 = p.R / 2, b = blockIdx.y, tok0 = blockIdx.x * (kWarps >> p.log2_splits);
+  const int tok = tok0 + (warp >> p.log2_splits), split = warp & ((1 << p.log2_splits) - 1);
+  Walk w = walk<kLanes>(p, p.q, b, tok, split);
+  uint4 raw[kUnroll];
+  w.load(raw);
 
-  const long long units = (long long)p.B * p.T * p.splits;
-  for (long long u = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); u < units;
-       u += (long long)gridDim.x * kWarps) {
-    const int split = (int)(u % p.splits);
-    const int row = (int)(u / p.splits), b = row / p.T, tok = row % p.T;
-    const float* pos = p.positions + b * p.pos_batch + (long long)tok * p.axes;
-    float cs[kAng], sn[kAng];
-#pragma unroll
-    for (int i = 0; i < kAng; ++i) {
-      const double turns = (double)pos[axis[i]] * freq[i];
-      sincospif(2.0f * (float)(turns - rint(turns)), &sn[i], &cs[i]);
-      if (kHalf) sn[i] *= sign;
+  // angles [token][2^log2_pairs]: no division to find a thread's token and pair
+  const float* pos = p.positions + b * p.pos_batch;
+  for (int i = threadIdx.x; i < (kWarps >> p.log2_splits) << p.log2_pairs; i += kWarps * 32) {
+    const int t = tok0 + (i >> p.log2_pairs), pr = i & ((1 << p.log2_pairs) - 1);
+    if (t < p.T && pr < R2) {
+      int axis = 0;
+      for (int last = p.dim[0] / 2; pr >= last; last += p.dim[axis] / 2) ++axis;
+      const double turns = (double)pos[(long long)t * p.axes + axis] * p.turns[pr];
+      float2 v;
+      sincospif(2.0f * (float)(turns - rint(turns)), &v.y, &v.x);
+      angles[i] = v;
     }
-    rotate_heads<kLanes, kHalf>(p, p.q, b, tok, split, cs, sn, partner, turned);
-    if (p.k.heads > 0) rotate_heads<kLanes, kHalf>(p, p.k, b, tok, split, cs, sn, partner, turned);
+  }
+  __syncthreads();
+  if (tok >= p.T) return;
+
+  // this lane's first `turned` pairs of neighbouring values turn (half-span
+  // pairs: all 8 values or none)
+  const int turned = kHalf ? (8 * c < p.R ? 4 : 0) : max(0, min(4, (p.R - 8 * c) / 2));
+  const bool second = kHalf && 8 * c >= R2;
+  int partner = lane;
+  if (kHalf && turned > 0) partner = second ? lane - R2 / 8 : lane + R2 / 8;
+  const float2* angle = angles + ((warp >> p.log2_splits) << p.log2_pairs) + (kHalf ? 8 * c - (second ? R2 : 0) : 4 * c);
+  const float sign = second ? 1.0f : -1.0f;
+  rotate_heads<kLanes, kHalf>(p, p.q, w, raw, angle, partner, turned, sign);
+  if (p.k.heads > 0) {
+    w = walk<kLanes>(p, p.k, b, tok, split);
+    w.load(raw);
+    rotate_heads<kLanes, kHalf>(p, p.k, w, raw, angle, partner, turned, sign);
   }
 }
 
 template <int kLanes>
-cudaError_t launch(const RopeParams& p, int grid, cudaStream_t stream) {
+cudaError_t launch(const RopeParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
+  const int tokens = kWarps >> p.log2_splits;
+  cfg.gridDim = dim3((unsigned)((p.T + tokens - 1) / tokens), (unsigned)p.B);
   cfg.blockDim = dim3(kWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -185,25 +229,26 @@ cudaError_t launch(const RopeParams& p, int grid, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_rope(RopeParams p, int num_sms, cudaStream_t stream) {
+cudaError_t launch_rope(RopeParams& p, int num_sms, cudaStream_t stream) {
   int lanes = 1;
   while (lanes * 8 < p.D) lanes *= 2;
-  // Enough warps to fill the GPU (32 per SM) by splitting a token's heads when
-  // there are few tokens; a split below one unrolled step brings nothing.
+  // Warps to a token: enough to leave each at most kSteps steps of heads, and with few
+  // tokens enough to fill the GPU (16 warps per SM).
   const long long rows = (long long)p.B * p.T;
-  const int heads = p.q.heads > p.k.heads ? p.q.heads : p.k.heads;
-  const int most = (heads * lanes + 31) / 32;
-  const long long want = (32LL * num_sms + rows - 1) / rows;
-  p.splits = (int)(want < 1 ? 1 : want > most ? most : want);
-  const long long units = rows * p.splits, blocks = (units + kWarps - 1) / kWarps;
-  const int grid = (int)(blocks < 8LL * num_sms ? blocks : 8LL * num_sms);
+  const int per = 32 / lanes, steps = (p.q.heads + per - 1) / per + (p.k.heads + per - 1) / per;
+  p.log2_splits = 0;
+  while ((1 << p.log2_splits) < kWarps &&
+         (steps > kSteps << p.log2_splits || (steps > 1 << p.log2_splits && rows << p.log2_splits < 16LL * num_sms)))
+    ++p.log2_splits;
+  p.log2_pairs = 0;
+  while (1 << p.log2_pairs < p.R / 2) ++p.log2_pairs;
   switch (lanes) {
-    case 1: return launch<1>(p, grid, stream);
-    case 2: return launch<2>(p, grid, stream);
-    case 4: return launch<4>(p, grid, stream);
-    case 8: return launch<8>(p, grid, stream);
-    case 16: return launch<16>(p, grid, stream);
-    default: return launch<32>(p, grid, stream);
+    case 1: return launch<1>(p, stream);
+    case 2: return launch<2>(p, stream);
+    case 4: return launch<4>(p, stream);
+    case 8: return launch<8>(p, stream);
+    case 16: return launch<16>(p, stream);
+    default: return launch<32>(p, stream);
   }
 }
 
