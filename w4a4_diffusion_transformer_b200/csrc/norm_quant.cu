@@ -23,14 +23,18 @@ namespace svdq {
 
 namespace {
 
-// A CTA of 8 warps handles tiles of 8 / W rows, W warps to a row; lane l of the
-// row's warp w owns the 8-value chunks (c W + w) 32 + l of the row and keeps
-// them, as BF16 pairs, in registers between the passes.  The columns'
+// A CTA of 8 warps handles tiles of 8 / W rows, W warps to a row; a lane of the
+// row's warp w owns the C chunks of 8 values 32 (C w + c) + lane and keeps them
+// in registers, as FP32, from the load to the codes (unpacking BF16 pairs again
+// for every pass took twice the instructions, and those are what bounds the
+// kernel before memory does).  Consecutive chunks lie a constant apart in every
+// operand and layout, so that their addresses are immediates.  The columns'
 // parameters w (1 + scale), shift and 1/lam sit in shared memory as FP32, filled
 // once per CTA and modulation row; chunk q's eight values are two 16-byte words
 // at q and q + K/8, so that a warp's reads are free of bank conflicts.
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
+constexpr int kNormChunks = 6, kNormChunksXl = 12;    // chunks a lane may hold, without and with a projection
 
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
@@ -81,11 +85,11 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int kFmt, int C>
-__global__ void __launch_bounds__(kThreads, 2) norm_quant_kernel(const NormParams p) {
+template <int kFmt, int C, int kBlocks>
+__global__ void __launch_bounds__(kThreads, kBlocks) norm_quant_kernel(const __grid_constant__ NormParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int K = p.K, M = p.M, nch = K >> 3;             // chunks of 8 values in a row
-  const int W = p.warps_per_row, rows = kWarps / W;
+  const int W = 1 << p.log2_warps, rows = kWarps >> p.log2_warps;
   float* slots = reinterpret_cast<float*>(smem);        // [2][3][8]: tile parity, reduction, warp
   float* rcp = slots + 2 * 3 * kWarps;                  // the NVFP4 quantizer's constants
   float4* gain = reinterpret_cast<float4*>(rcp + 16);   // w (1 + scale)
@@ -95,8 +99,9 @@ __global__ void __launch_bounds__(kThreads, 2) norm_quant_kernel(const NormParam
   const int ystride = 2 * K + 64;                       // 64 bytes: rows shifted by half the banks
   float* red = reinterpret_cast<float*>(ytile + rows * ystride);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rg = warp / W, w = warp % W;                // this warp's row of the tile, its place in the row
-  const int q0 = w * 32 + lane;                         // first chunk; the next are 32 W apart
+  const int rg = warp >> p.log2_warps, w = warp & (W - 1);   // this warp's row of the tile, its place in the row
+  const int q0 = w * (32 * C) + lane;                   // first chunk; the next are 32 apart
+  const int nc = min(C, max(0, (nch - q0 + 31) >> 5));  // this lane's chunks
 
   dev::griddep_launch_dependents();
   if (kFmt == kFmtNvfp4 && threadIdx.x < 16) rcp[threadIdx.x] = p.rcp[threadIdx.x];
@@ -107,72 +112,79 @@ __global__ void __launch_bounds__(kThreads, 2) norm_quant_kernel(const NormParam
   dev::griddep_wait();
 
   const float invK = 1.0f / (float)K;
-  const int tiles = (p.mpad + rows - 1) / rows;
+  const int tiles = p.mpad >> (3 - p.log2_warps);
   const int t0 = (int)((long long)tiles * blockIdx.x / gridDim.x);
   const int t1 = (int)((long long)tiles * (blockIdx.x + 1) / gridDim.x);
   int loaded = -1;                                      // modulation row in shared memory
   for (int tile = t0; tile < t1; ++tile) {
     const int row = tile * rows + rg;
     const bool live = row < M;                          // rows M .. mpad - 1: zero codes and scales
+    const int n = live ? nc : 0;                        // chunks to load and store
+    const size_t at = (size_t)row * K + 8 * q0;
     float* slot = slots + ((tile & 1) * 3) * kWarps + rg * W;
-    uint32_t h[C][4];
+    float2 f[C][4];                                     // h, then h - mu, then y / lam
     // ---- h = bf16(x + r)
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int q = q0 + c * 32 * W;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (live && q < nch) v = *reinterpret_cast<const uint4*>(p.x + (size_t)row * K + 8 * q);
-      h[c][0] = v.x; h[c][1] = v.y; h[c][2] = v.z; h[c][3] = v.w;
-    }
-    if (p.residual && live) {
+    {
+      uint4 v[C];
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const int q = q0 + c * 32 * W;
-        if (q < nch) {
-          const uint4 v = *reinterpret_cast<const uint4*>(p.residual + (size_t)row * K + 8 * q);
-          h[c][0] = add_bf16x2(h[c][0], v.x);
-          h[c][1] = add_bf16x2(h[c][1], v.y);
-          h[c][2] = add_bf16x2(h[c][2], v.z);
-          h[c][3] = add_bf16x2(h[c][3], v.w);
-        }
+        v[c] = make_uint4(0u, 0u, 0u, 0u);
+        if (c < n) v[c] = *reinterpret_cast<const uint4*>(p.x + at + 256 * c);
       }
-    }
-    if (p.sum && live) {
+      if (p.residual) {
+        const __nv_bfloat16* r = p.residual + at;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+          if (c < n) {
+            const uint4 u = *reinterpret_cast<const uint4*>(r + 256 * c);
+            v[c] = make_uint4(add_bf16x2(v[c].x, u.x), add_bf16x2(v[c].y, u.y), add_bf16x2(v[c].z, u.z),
+                              add_bf16x2(v[c].w, u.w));
+          }
+      }
+      if (p.sum) {
+        __nv_bfloat16* o = p.sum + at;
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+          if (c < n) *reinterpret_cast<uint4*>(o + 256 * c) = v[c];
+      }
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const int q = q0 + c * 32 * W;
-        if (q < nch)
-          *reinterpret_cast<uint4*>(p.sum + (size_t)row * K + 8 * q) = make_uint4(h[c][0], h[c][1], h[c][2], h[c][3]);
+        f[c][0] = unpack2(v[c].x);
+        f[c][1] = unpack2(v[c].y);
+        f[c][2] = unpack2(v[c].z);
+        f[c][3] = unpack2(v[c].w);
       }
     }
     // ---- the tile's modulation rows: one, but where two sequences meet
-    const int first = min(tile * rows, M - 1), last = min(tile * rows + rows, M) - 1;
-    const int m0 = p.rows_per_mod > 0 ? first / p.rows_per_mod : 0;
-    const int m1 = p.rows_per_mod > 0 ? last / p.rows_per_mod : 0;
-    const int mine = m0 == m1 ? m0 : min(row, M - 1) / p.rows_per_mod;
+    int m0 = 0, m1 = 0, mine = 0;
+    if (p.rows_per_mod > 0) {
+      m0 = min(tile * rows, M - 1) / p.rows_per_mod;
+      m1 = min(tile * rows + rows - 1, M - 1) / p.rows_per_mod;
+      mine = m0 == m1 ? m0 : min(row, M - 1) / p.rows_per_mod;
+    }
     // ---- statistics: the mean first (layer norm), then the mean square about it
-    float mu = 0.f;
     if (p.center) {
       float2 a = make_float2(0.f, 0.f);
 #pragma unroll
       for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a = __fadd2_rn(a, unpack2(h[c][i]));
-      mu = reduce_row<false>(a.x + a.y, slot, W, w, 1 + rg) * invK;
+        for (int i = 0; i < 4; ++i) a = __fadd2_rn(a, f[c][i]);
+      const float mu = reduce_row<false>(a.x + a.y, slot, W, w, 1 + rg) * invK;
+      const float2 nmu = make_float2(-mu, -mu);
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        if (c < nc) {                                   // a chunk past K keeps its zeros
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f[c][i] = __fadd2_rn(f[c][i], nmu);
+        }
     }
     float2 a2 = make_float2(0.f, 0.f);
-    const float2 nmu2 = make_float2(-mu, -mu);
 #pragma unroll
     for (int c = 0; c < C; ++c)
-      if (q0 + c * 32 * W < nch) {                       // a chunk past K holds zeros, not values
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 d = __fadd2_rn(unpack2(h[c][i]), nmu2);
-          a2 = __ffma2_rn(d, d, a2);
-        }
-      }
+      for (int i = 0; i < 4; ++i) a2 = __ffma2_rn(f[c][i], f[c][i], a2);
     const float rstd = rsqrtf(reduce_row<false>(a2.x + a2.y, slot + kWarps, W, w, 1 + rg) * invK + p.eps);
-    const float2 rstd2 = make_float2(rstd, rstd), off2 = make_float2(-mu * rstd, -mu * rstd);
+    const float2 rstd2 = make_float2(rstd, rstd);
 
     float amax = 0.f;
     for (int m = m0; m <= m1; ++m) {
@@ -202,48 +214,43 @@ __global__ void __launch_bounds__(kThreads, 2) norm_quant_kernel(const NormParam
       }
       if (m != mine) continue;
       // ---- y = bf16(n w (1 + scale) + shift), and the 4-bit quantizers
+      __nv_bfloat16* yout = p.y ? p.y + at : nullptr;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const int q = q0 + c * 32 * W;
-        const bool act = q < nch;
-        float2 g[4], sh[4], il[4], v[4];
+        const int q = q0 + 32 * c;
+        const bool act = c < nc;
         if (act) {
+          float2 g[4], sh[4], il[4];
           param8(gain, q, nch, g);
           param8(shift, q, nch, sh);
           param8(ilam, q, nch, il);
+          uint32_t y[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float2 n = __ffma2_rn(unpack2(h[c][i]), rstd2, off2);
-            h[c][i] = pack2(__ffma2_rn(n, g[i], sh[i]));
-            v[i] = __fmul2_rn(unpack2(h[c][i]), il[i]);
+            y[i] = pack2(__ffma2_rn(__fmul2_rn(f[c][i], rstd2), g[i], sh[i]));
+            f[c][i] = __fmul2_rn(unpack2(y[i]), il[i]);
           }
-          if (p.nmt > 0 && live)
-            *reinterpret_cast<uint4*>(ytile + rg * ystride + q * 16) =
-                make_uint4(h[c][0], h[c][1], h[c][2], h[c][3]);
-          if (p.y && live)
-            *reinterpret_cast<uint4*>(p.y + (size_t)row * K + 8 * q) = make_uint4(h[c][0], h[c][1], h[c][2], h[c][3]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = make_float2(0.f, 0.f);
+          if (p.nmt > 0 && live) *reinterpret_cast<uint4*>(ytile + rg * ystride + q * 16) = make_uint4(y[0], y[1], y[2], y[3]);
+          if (yout && live) *reinterpret_cast<uint4*>(yout + 256 * c) = make_uint4(y[0], y[1], y[2], y[3]);
         }
-        float a = fmaxf(fabsf(v[0].x), fabsf(v[0].y));
+        float a = fmaxf(fabsf(f[c][0].x), fabsf(f[c][0].y));
 #pragma unroll
-        for (int i = 1; i < 4; ++i) a = dev::fmax3(a, fabsf(v[i].x), fabsf(v[i].y));
+        for (int i = 1; i < 4; ++i) a = dev::fmax3(a, fabsf(f[c][i].x), fabsf(f[c][i].y));
         if (kFmt == kFmtInt8) {
           amax = fmaxf(amax, a);
         } else if (kFmt == kFmtNvfp4) {
           // a group of 16 is two lanes' chunks
           a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
           uint32_t codes = 0u;
-          const uint32_t sb = live ? dev::nvfp4_quant8(v, a, p.c_x, p.g_x_exp, rcp, codes) : 0u;
+          const uint32_t sb = live ? dev::nvfp4_quant8(f[c], a, p.c_x, p.g_x_exp, rcp, codes) : 0u;
           // four groups' scale bytes are one word of the layout
           uint32_t word = sb << (8 * ((lane >> 1) & 3));
           word |= __shfl_xor_sync(0xffffffffu, word, 2);
           word |= __shfl_xor_sync(0xffffffffu, word, 4);
           if (act) {
-            if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(p.scales + sf_offset(row, q >> 1, K)) = word;
-            *reinterpret_cast<uint32_t*>(p.codes + act_tile_offset(row, q >> 5, (q & 31) >> 2, p.nst) + (q & 3) * 4) =
-                codes;
+            if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(p.scales + sf_offset(row, q0 >> 1, K) + 2048 * c) = word;
+            *reinterpret_cast<uint32_t*>(p.codes + act_tile_offset(row, q0 >> 5, (lane & 31) >> 2, p.nst) + 16384 * c +
+                                         (lane & 3) * 4) = codes;
           }
         } else {
           // a group of 64 is eight lanes' chunks
@@ -260,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_quant_kernel(const NormParam
             for (int i = 0; i < 4; ++i) {
               // the sum with 1.5 * 2^23 holds the rounded integer in its low
               // bits; the product is rounded before (no fused multiply-add)
-              const float2 k = __fmul2_rn(v[i], i2);
+              const float2 k = __fmul2_rn(f[c][i], i2);
               codes |= (__float_as_uint(__fadd_rn(k.x, 12582912.0f)) & 0xFu) << (8 * i);
               codes |= (__float_as_uint(__fadd_rn(k.y, 12582912.0f)) & 0xFu) << (8 * i + 4);
             }
@@ -268,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_quant_kernel(const NormParam
           if (act) {
             if ((lane & 7) == 0)
               reinterpret_cast<uint16_t*>(p.scales)[(size_t)(q >> 3) * p.mpad + row] = __bfloat16_as_ushort(sb);
-            if (live) *reinterpret_cast<uint32_t*>(p.codes + (size_t)row * (K / 2) + q * 4) = codes;
+            if (live) *reinterpret_cast<uint32_t*>(p.codes + (size_t)row * (K / 2) + q0 * 4 + 128 * c) = codes;
           }
         }
       }
@@ -284,26 +291,25 @@ __global__ void __launch_bounds__(kThreads, 2) norm_quant_kernel(const NormParam
         sx[p.mpad + row] = inv;
       }
       const float2 i2 = make_float2(inv, inv);
+      // stages of 128 codes: chunk q is half of a 16-byte piece of stage q / 16
+      uint8_t* o = p.codes + act_tile_offset(row, q0 >> 4, (q0 & 15) >> 1, p.nst) + (lane & 1) * 8;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        const int q = q0 + c * 32 * W;
-        if (q < nch) {
-          float2 il[4];
-          param8(ilam, q, nch, il);
+        if (c < nc) {
           uint32_t t[8];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             // the sum with 1.5 * 2^23 holds the rounded integer, two's
             // complement, in its low byte (|q| <= 127 (1 + 2^-22): no clamp)
-            const float2 k = __fmul2_rn(__fmul2_rn(unpack2(h[c][i]), il[i]), i2);
+            const float2 k = __fmul2_rn(f[c][i], i2);
             t[2 * i] = __float_as_uint(__fadd_rn(k.x, 12582912.0f));
             t[2 * i + 1] = __float_as_uint(__fadd_rn(k.y, 12582912.0f));
           }
-          uint2 o;
-          o.x = __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
-          o.y = __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410);
-          if (sc == 0.f) o.x = o.y = 0u;
-          *reinterpret_cast<uint2*>(p.codes + act_tile_offset(row, q >> 4, (q & 15) >> 1, p.nst) + (q & 1) * 8) = o;
+          uint2 v;
+          v.x = __byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410);
+          v.y = __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410);
+          if (sc == 0.f) v.x = v.y = 0u;
+          *reinterpret_cast<uint2*>(o + 2 * 16384 * c) = v;
         }
       }
     }
@@ -359,17 +365,17 @@ __global__ void __launch_bounds__(kThreads, 2) norm_quant_kernel(const NormParam
   }
 }
 
-size_t smem_bytes(int K, int nmt, int W) {
+size_t smem_bytes(int K, int nmt, int log2_warps) {
   const size_t head = (2 * 3 * kWarps + 16) * 4, params = (size_t)K * 12;
-  const size_t tile = (size_t)(kWarps / W) * (2 * (size_t)K + 64), red = (size_t)kWarps * nmt * 16 * 8 * 4;
+  const size_t tile = (size_t)(kWarps >> log2_warps) * (2 * (size_t)K + 64), red = (size_t)kWarps * nmt * 16 * 8 * 4;
   return head + params + (nmt > 0 ? tile + red : 0);
 }
 
-template <int kFmt, int C>
+template <int kFmt, int C, int kBlocks>
 cudaError_t launch(const NormParams& p, int num_sms, cudaStream_t stream) {
-  const size_t smem = smem_bytes(p.K, p.nmt, p.warps_per_row);
+  const size_t smem = smem_bytes(p.K, p.nmt, p.log2_warps);
   if (smem > kNormMaxSmem) return cudaErrorInvalidValue;
-  auto kern = norm_quant_kernel<kFmt, C>;
+  auto kern = norm_quant_kernel<kFmt, C, kBlocks>;
   static thread_local int configured_device = -1;
   int dev = 0;
   cudaGetDevice(&dev);
@@ -378,9 +384,10 @@ cudaError_t launch(const NormParams& p, int num_sms, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
-  // persistent: as many CTAs as an SM holds, each a contiguous range of tiles
-  const int rows = kWarps / p.warps_per_row, tiles = (p.mpad + rows - 1) / rows;
-  const int per_sm = smem * 2 + 4096 <= kNormMaxSmem ? 2 : 1;
+  // persistent: as many CTAs as an SM holds (228 KB, 1 KB of it per CTA its
+  // own), each a contiguous range of tiles
+  const int tiles = p.mpad >> (3 - p.log2_warps);
+  const int fit = (int)(233472 / (smem + 1024)), per_sm = fit < kBlocks ? fit : kBlocks;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles < per_sm * num_sms ? tiles : per_sm * num_sms));
   cfg.blockDim = dim3(kThreads);
@@ -396,13 +403,14 @@ cudaError_t launch(const NormParams& p, int num_sms, cudaStream_t stream) {
 
 template <int kFmt>
 cudaError_t launch_fmt(const NormParams& p, int num_sms, cudaStream_t stream) {
-  const int chunks = (p.K / 8 + 32 * p.warps_per_row - 1) / (32 * p.warps_per_row);   // of a lane
-  if (chunks <= 1) return launch<kFmt, 1>(p, num_sms, stream);
-  if (chunks <= 2) return launch<kFmt, 2>(p, num_sms, stream);
-  if (chunks <= 4) return launch<kFmt, 4>(p, num_sms, stream);
-  if (chunks <= 6) return launch<kFmt, 6>(p, num_sms, stream);
-  if (chunks <= 8) return launch<kFmt, 8>(p, num_sms, stream);
-  return launch<kFmt, 12>(p, num_sms, stream);
+  const int chunks = (p.K / 8 + (32 << p.log2_warps) - 1) / (32 << p.log2_warps);   // of a lane
+  if (chunks <= 1) return launch<kFmt, 1, 4>(p, num_sms, stream);
+  if (chunks <= 2) return launch<kFmt, 2, 4>(p, num_sms, stream);
+  if (chunks <= 3) return launch<kFmt, 3, 4>(p, num_sms, stream);
+  if (chunks <= 4) return launch<kFmt, 4, 3>(p, num_sms, stream);
+  if (chunks <= 6) return launch<kFmt, 6, 3>(p, num_sms, stream);
+  if (chunks <= 8) return launch<kFmt, 8, 2>(p, num_sms, stream);
+  return launch<kFmt, 12, 2>(p, num_sms, stream);
 }
 
 }  // namespace
@@ -410,11 +418,13 @@ cudaError_t launch_fmt(const NormParams& p, int num_sms, cudaStream_t stream) {
 bool norm_supported(int K) { return K <= kNormMaxK; }
 
 cudaError_t launch_norm_quant(NormParams p, int fmt, int num_sms, cudaStream_t stream) {
-  // a lane holds at most 12 chunks of a row; with few rows, more warps to a row
-  int W = 1;
-  while (W < kWarps && p.K > 12 * 256 * W) W *= 2;
-  while (W < kWarps && (p.M + kWarps / W - 1) / (kWarps / W) < num_sms) W *= 2;
-  p.warps_per_row = W;
+  // A lane holds at most 6 chunks of a row (with a projection 12: it wants 8
+  // rows in a tile); with few rows, more warps to a row.
+  const int most = p.nmt > 0 ? kNormChunksXl : kNormChunks;
+  int l = 0;
+  while (l < 3 && p.K > (256 * most) << l) ++l;
+  while (l < 3 && (p.M + (kWarps >> l) - 1) / (kWarps >> l) < num_sms) ++l;
+  p.log2_warps = l;
   if (fmt == kFmtNvfp4) return launch_fmt<kFmtNvfp4>(p, num_sms, stream);
   if (fmt == kFmtInt4) return launch_fmt<kFmtInt4>(p, num_sms, stream);
   return launch_fmt<kFmtInt8>(p, num_sms, stream);
