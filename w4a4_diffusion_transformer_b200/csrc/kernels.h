@@ -176,10 +176,11 @@ struct NormParams {
   uint8_t* scales;
   __nv_bfloat16* xl;            // row stride xl_stride elements
   int xl_stride;
-  int nmt;                      // blocks of 16 branch columns to project (0..4)
+  int nmt;                      // blocks of 16 branch columns to project: 0, 1 (W8A8), 2 or 4
   const __nv_bfloat16* amat[4]; // [16][K] each: rows of L1d^T, then of the adapter's A^T
   int xl_col[4];                // XL column of each block's first
-  int log2_warps;               // warps to a row (set by the launcher)
+  int log2_warps;               // warps to a row, tiles of a CTA (set by the launcher)
+  int tiles_each, tiles_extra;
   int xl_zero;                  // > 0: 16 XL columns from here are zero (W8A8's padding)
 };
 constexpr int kNormMaxK = 14336;              // a row's parameters and its tile fit in shared memory

@@ -23,7 +23,7 @@ namespace svdq {
 
 namespace {
 
-// A CTA of 8 warps handles tiles of 8 / W rows, W warps to a row; a lane of the
+// A CTA of 8 warps (16 with a projection) handles tiles of 8 / W rows, W warps to a row; a lane of the
 // row's warp w owns the C chunks of 8 values 32 (C w + c) + lane and keeps them
 // in registers, as FP32, from the load to the codes (unpacking BF16 pairs again
 // for every pass took twice the instructions, and those are what bounds the
@@ -32,9 +32,9 @@ namespace {
 // parameters w (1 + scale), shift and 1/lam sit in shared memory as FP32, filled
 // once per CTA and modulation row; chunk q's eight values are two 16-byte words
 // at q and q + K/8, so that a warp's reads are free of bank conflicts.
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kNormChunks = 6, kNormChunksXl = 12;    // chunks a lane may hold, without and with a projection
+// A lane's chunks: at most 6 (12 with a projection, which wants many rows in a
+// tile, and for rows so long that 6 would leave 8 warps a single row).
+constexpr int kChunks = 6, kChunksMost = 12, kLongK = 6144;
 
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
@@ -85,12 +85,14 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int kFmt, int C, int kBlocks>
-__global__ void __launch_bounds__(kThreads, kBlocks) norm_quant_kernel(const __grid_constant__ NormParams p) {
+// kMt: blocks of 16 branch columns to project (0: no projection).
+template <int kFmt, int C, int kWarps, int kMt>
+__global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) norm_quant_kernel(const __grid_constant__ NormParams p) {
+  constexpr int kThreads = kWarps * 32;
   extern __shared__ __align__(16) uint8_t smem[];
   const int K = p.K, M = p.M, nch = K >> 3;             // chunks of 8 values in a row
   const int W = 1 << p.log2_warps, rows = kWarps >> p.log2_warps;
-  float* slots = reinterpret_cast<float*>(smem);        // [2][3][8]: tile parity, reduction, warp
+  float* slots = reinterpret_cast<float*>(smem);        // [2][3][kWarps]: tile parity, reduction, warp
   float* rcp = slots + 2 * 3 * kWarps;                  // the NVFP4 quantizer's constants
   float4* gain = reinterpret_cast<float4*>(rcp + 16);   // w (1 + scale)
   float4* shift = gain + 2 * nch;
@@ -112,9 +114,9 @@ __global__ void __launch_bounds__(kThreads, kBlocks) norm_quant_kernel(const __g
   dev::griddep_wait();
 
   const float invK = 1.0f / (float)K;
-  const int tiles = p.mpad >> (3 - p.log2_warps);
-  const int t0 = (int)((long long)tiles * blockIdx.x / gridDim.x);
-  const int t1 = (int)((long long)tiles * (blockIdx.x + 1) / gridDim.x);
+  // this CTA's tiles: p.tiles_each, and one more for the first p.tiles_extra CTAs
+  const int b = (int)blockIdx.x;
+  const int t0 = b * p.tiles_each + min(b, p.tiles_extra), t1 = t0 + p.tiles_each + (b < p.tiles_extra ? 1 : 0);
   int loaded = -1;                                      // modulation row in shared memory
   for (int tile = t0; tile < t1; ++tile) {
     const int row = tile * rows + rg;
@@ -230,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) norm_quant_kernel(const __g
             y[i] = pack2(__ffma2_rn(__fmul2_rn(f[c][i], rstd2), g[i], sh[i]));
             f[c][i] = __fmul2_rn(unpack2(y[i]), il[i]);
           }
-          if (p.nmt > 0 && live) *reinterpret_cast<uint4*>(ytile + rg * ystride + q * 16) = make_uint4(y[0], y[1], y[2], y[3]);
+          if (kMt > 0 && live) *reinterpret_cast<uint4*>(ytile + rg * ystride + q * 16) = make_uint4(y[0], y[1], y[2], y[3]);
           if (yout && live) *reinterpret_cast<uint4*>(yout + 256 * c) = make_uint4(y[0], y[1], y[2], y[3]);
         }
         float a = fmaxf(fabsf(f[c][0].x), fabsf(f[c][0].y));
@@ -313,49 +315,62 @@ __global__ void __launch_bounds__(kThreads, kBlocks) norm_quant_kernel(const __g
         }
       }
     }
-    if (p.nmt == 0 || tile * rows >= M) continue;       // uniform over the CTA
+    if (kMt == 0 || tile * rows >= M) continue;         // uniform over the CTA
 
     // ---- XL: 16 rank rows x 8 tokens per MMA, K split over the warps.  The
     // order of k inside a block of 32 is free as long as both operands agree:
     // lane (g, c) = (lane / 4, lane % 4) takes columns 8c .. 8c + 7 of the
-    // block, so each operand row is one 16-byte load and feeds two MMAs.
+    // block, so each operand row is one 16-byte load and feeds two MMAs.  The
+    // factor comes from L2 for every tile (rank 32: 64 K bytes), which is why a
+    // tile is 16 rows: with 8 this traffic alone cost 4608 x 3072 20 us.
     __syncthreads();                                    // the y tile is complete
+    constexpr int kAcc = kMt > 0 ? kMt : 1, kTok = kWarps;   // a tile has at most a row per warp
     const int g = lane >> 2, c = lane & 3;
-    float acc[4][4];
+    float acc[kAcc][2][4];
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
+    for (int mt = 0; mt < kAcc; ++mt)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[mt][i] = 0.f;
+      for (int i = 0; i < 8; ++i) acc[mt][i >> 2][i & 3] = 0.f;
     const uint8_t* yrow = ytile + g * ystride + c * 16;
-#pragma unroll 4
+    const bool first = g < rows, second = kTok > 8 && g + 8 < rows;
+#pragma unroll(kMt == 4 ? 2 : 3)
     for (int kb = warp; kb < K / 32; kb += kWarps) {
-      uint4 b = make_uint4(0u, 0u, 0u, 0u);
-      if (g < rows) b = *reinterpret_cast<const uint4*>(yrow + kb * 64);
+      uint4 lo[kAcc], hi[kAcc], b0 = make_uint4(0u, 0u, 0u, 0u), b1 = b0;
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt)
-        if (mt < p.nmt) {
-          const __nv_bfloat16* a = p.amat[mt] + (size_t)g * K + kb * 32 + c * 8;
-          const uint4 lo = *reinterpret_cast<const uint4*>(a);
-          const uint4 hi = *reinterpret_cast<const uint4*>(a + 8 * (size_t)K);
-          mma_16816(acc[mt], lo.x, hi.x, lo.y, hi.y, b.x, b.y);
-          mma_16816(acc[mt], lo.z, hi.z, lo.w, hi.w, b.z, b.w);
+      for (int mt = 0; mt < kMt; ++mt) {
+        const __nv_bfloat16* a = p.amat[mt] + (size_t)g * K + kb * 32 + c * 8;
+        lo[mt] = *reinterpret_cast<const uint4*>(a);
+        hi[mt] = *reinterpret_cast<const uint4*>(a + 8 * (size_t)K);
+      }
+      if (first) b0 = *reinterpret_cast<const uint4*>(yrow + kb * 64);
+      if (second) b1 = *reinterpret_cast<const uint4*>(yrow + 8 * ystride + kb * 64);
+#pragma unroll
+      for (int mt = 0; mt < kMt; ++mt) {
+        mma_16816(acc[mt][0], lo[mt].x, hi[mt].x, lo[mt].y, hi[mt].y, b0.x, b0.y);
+        mma_16816(acc[mt][0], lo[mt].z, hi[mt].z, lo[mt].w, hi[mt].w, b0.z, b0.w);
+        if (kTok > 8) {
+          mma_16816(acc[mt][1], lo[mt].x, hi[mt].x, lo[mt].y, hi[mt].y, b1.x, b1.y);
+          mma_16816(acc[mt][1], lo[mt].z, hi[mt].z, lo[mt].w, hi[mt].w, b1.z, b1.w);
         }
+      }
     }
+    constexpr int kRank = kMt * 16;
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
-      if (mt < p.nmt) {                                 // partials [warp][nmt 16][8]
-        float* o = red + ((size_t)(warp * p.nmt + mt) * 16 + g) * 8 + 2 * c;
-        *reinterpret_cast<float2*>(o) = make_float2(acc[mt][0], acc[mt][1]);
-        *reinterpret_cast<float2*>(o + 64) = make_float2(acc[mt][2], acc[mt][3]);
+    for (int mt = 0; mt < kMt; ++mt)                    // partials [warp][rank][token]
+#pragma unroll
+      for (int h = 0; h < kTok / 8; ++h) {
+        float* o = red + ((size_t)warp * kRank + mt * 16 + g) * kTok + 8 * h + 2 * c;
+        *reinterpret_cast<float2*>(o) = make_float2(acc[mt][h][0], acc[mt][h][1]);
+        *reinterpret_cast<float2*>(o + 8 * kTok) = make_float2(acc[mt][h][2], acc[mt][h][3]);
       }
     __syncthreads();                                    // ... and the y tile has been read
-    for (int i = threadIdx.x; i < p.nmt * 16 * rows; i += kThreads) {
-      const int j = i % (p.nmt * 16), r = tile * rows + i / (p.nmt * 16);   // rank row, token
+    for (int i = threadIdx.x; i < kRank * rows; i += kThreads) {
+      const int t = i & (rows - 1), j = i / rows, r = tile * rows + t;   // token, rank row
       if (r < M) {
-        float t = 0.f;
+        float v = 0.f;
 #pragma unroll
-        for (int u = 0; u < kWarps; ++u) t += red[((size_t)u * p.nmt * 16 + j) * 8 + i / (p.nmt * 16)];
-        p.xl[(size_t)r * p.xl_stride + p.xl_col[j >> 4] + (j & 15)] = __float2bfloat16_rn(t);
+        for (int u = 0; u < kWarps; ++u) v += red[((size_t)u * kRank + j) * kTok + t];
+        p.xl[(size_t)r * p.xl_stride + p.xl_col[j >> 4] + (j & 15)] = __float2bfloat16_rn(v);
       }
     }
     if (p.xl_zero > 0 && threadIdx.x < 16 * rows) {
@@ -365,17 +380,17 @@ __global__ void __launch_bounds__(kThreads, kBlocks) norm_quant_kernel(const __g
   }
 }
 
-size_t smem_bytes(int K, int nmt, int log2_warps) {
-  const size_t head = (2 * 3 * kWarps + 16) * 4, params = (size_t)K * 12;
-  const size_t tile = (size_t)(kWarps >> log2_warps) * (2 * (size_t)K + 64), red = (size_t)kWarps * nmt * 16 * 8 * 4;
+size_t smem_bytes(int K, int nmt, int warps, int log2_warps) {
+  const size_t head = (2 * 3 * warps + 16) * 4, params = (size_t)K * 12;
+  const size_t tile = (size_t)(warps >> log2_warps) * (2 * (size_t)K + 64), red = (size_t)warps * nmt * 16 * warps * 4;
   return head + params + (nmt > 0 ? tile + red : 0);
 }
 
-template <int kFmt, int C, int kBlocks>
-cudaError_t launch(const NormParams& p, int num_sms, cudaStream_t stream) {
-  const size_t smem = smem_bytes(p.K, p.nmt, p.log2_warps);
+template <int kFmt, int C, int kWarps, int kMt>
+cudaError_t launch(NormParams& p, int num_sms, cudaStream_t stream) {
+  const size_t smem = smem_bytes(p.K, kMt, kWarps, p.log2_warps);
   if (smem > kNormMaxSmem) return cudaErrorInvalidValue;
-  auto kern = norm_quant_kernel<kFmt, C, kBlocks>;
+  auto kern = norm_quant_kernel<kFmt, C, kWarps, kMt>;
   static thread_local int configured_device = -1;
   int dev = 0;
   cudaGetDevice(&dev);
@@ -386,11 +401,14 @@ cudaError_t launch(const NormParams& p, int num_sms, cudaStream_t stream) {
   }
   // persistent: as many CTAs as an SM holds (228 KB, 1 KB of it per CTA its
   // own), each a contiguous range of tiles
-  const int tiles = p.mpad >> (3 - p.log2_warps);
-  const int fit = (int)(233472 / (smem + 1024)), per_sm = fit < kBlocks ? fit : kBlocks;
+  const int rows = kWarps >> p.log2_warps, tiles = p.mpad / rows;
+  const int fit = (int)(233472 / (smem + 1024)), per_sm = fit < 16 / kWarps ? fit : 16 / kWarps;
+  const int grid = tiles < per_sm * num_sms ? tiles : per_sm * num_sms;
+  p.tiles_each = tiles / grid;
+  p.tiles_extra = tiles % grid;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(tiles < per_sm * num_sms ? tiles : per_sm * num_sms));
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kWarps * 32);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -401,16 +419,53 @@ cudaError_t launch(const NormParams& p, int num_sms, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
+// Chunks of a lane with 2^l warps to a row.
+int lane_chunks(int K, int l) { return (K / 8 + (32 << l) - 1) / (32 << l); }
+
+// Without a projection: 8 warps, two CTAs per SM.  More registers a thread and
+// all of a row's loads in flight beat more warps (4608 x 3072 W8A8: 23.1 us at 16
+// warps of 128 registers, 25.0 at 24 of 80).
 template <int kFmt>
-cudaError_t launch_fmt(const NormParams& p, int num_sms, cudaStream_t stream) {
-  const int chunks = (p.K / 8 + (32 << p.log2_warps) - 1) / (32 << p.log2_warps);   // of a lane
-  if (chunks <= 1) return launch<kFmt, 1, 4>(p, num_sms, stream);
-  if (chunks <= 2) return launch<kFmt, 2, 4>(p, num_sms, stream);
-  if (chunks <= 3) return launch<kFmt, 3, 4>(p, num_sms, stream);
-  if (chunks <= 4) return launch<kFmt, 4, 3>(p, num_sms, stream);
-  if (chunks <= 6) return launch<kFmt, 6, 3>(p, num_sms, stream);
-  if (chunks <= 8) return launch<kFmt, 8, 2>(p, num_sms, stream);
-  return launch<kFmt, 12, 2>(p, num_sms, stream);
+cudaError_t launch_plain(NormParams& p, int num_sms, cudaStream_t stream) {
+  int l = 0;
+  while (l < 3 && lane_chunks(p.K, l) > (p.K > kLongK ? kChunksMost : kChunks)) ++l;
+  // with few rows, more warps to a row
+  while (l < 3 && (p.M + (8 >> l) - 1) / (8 >> l) < num_sms) ++l;
+  p.log2_warps = l;
+  const int chunks = lane_chunks(p.K, l);
+  if (chunks <= 1) return launch<kFmt, 1, 8, 0>(p, num_sms, stream);
+  if (chunks <= 2) return launch<kFmt, 2, 8, 0>(p, num_sms, stream);
+  if (chunks <= 3) return launch<kFmt, 3, 8, 0>(p, num_sms, stream);
+  if (chunks <= 4) return launch<kFmt, 4, 8, 0>(p, num_sms, stream);
+  if (chunks <= 6) return launch<kFmt, 6, 8, 0>(p, num_sms, stream);
+  return launch<kFmt, 12, 8, 0>(p, num_sms, stream);
+}
+
+// With a projection: 16 warps, one CTA per SM, tiles of up to 16 rows; 8 warps
+// where 16 rows of so many columns do not fit in shared memory.
+template <int kFmt, int kMt>
+cudaError_t launch_project(NormParams& p, int num_sms, cudaStream_t stream) {
+  int l = 0;
+  while (l < 3 && lane_chunks(p.K, l) > kChunksMost) ++l;
+  if (smem_bytes(p.K, kMt, 16, l) > kNormMaxSmem) {
+    p.log2_warps = l;
+    return launch<kFmt, 12, 8, kMt>(p, num_sms, stream);
+  }
+  while (l < 3 && (p.M + (16 >> l) - 1) / (16 >> l) < num_sms) ++l;
+  p.log2_warps = l;
+  const int chunks = lane_chunks(p.K, l);
+  if (chunks <= 2) return launch<kFmt, 2, 16, kMt>(p, num_sms, stream);
+  if (chunks <= 4) return launch<kFmt, 4, 16, kMt>(p, num_sms, stream);
+  if (chunks <= 6) return launch<kFmt, 6, 16, kMt>(p, num_sms, stream);
+  return launch<kFmt, 12, 16, kMt>(p, num_sms, stream);
+}
+
+template <int kFmt>
+cudaError_t launch_4bit(NormParams& p, int num_sms, cudaStream_t stream) {
+  if (p.nmt == 0) return launch_plain<kFmt>(p, num_sms, stream);
+  if (p.nmt == 2) return launch_project<kFmt, 2>(p, num_sms, stream);
+  if (p.nmt == 4) return launch_project<kFmt, 4>(p, num_sms, stream);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
@@ -418,16 +473,11 @@ cudaError_t launch_fmt(const NormParams& p, int num_sms, cudaStream_t stream) {
 bool norm_supported(int K) { return K <= kNormMaxK; }
 
 cudaError_t launch_norm_quant(NormParams p, int fmt, int num_sms, cudaStream_t stream) {
-  // A lane holds at most 6 chunks of a row (with a projection 12: it wants 8
-  // rows in a tile); with few rows, more warps to a row.
-  const int most = p.nmt > 0 ? kNormChunksXl : kNormChunks;
-  int l = 0;
-  while (l < 3 && p.K > (256 * most) << l) ++l;
-  while (l < 3 && (p.M + (kWarps >> l) - 1) / (kWarps >> l) < num_sms) ++l;
-  p.log2_warps = l;
-  if (fmt == kFmtNvfp4) return launch_fmt<kFmtNvfp4>(p, num_sms, stream);
-  if (fmt == kFmtInt4) return launch_fmt<kFmtInt4>(p, num_sms, stream);
-  return launch_fmt<kFmtInt8>(p, num_sms, stream);
+  if (fmt == kFmtNvfp4) return launch_4bit<kFmtNvfp4>(p, num_sms, stream);
+  if (fmt == kFmtInt4) return launch_4bit<kFmtInt4>(p, num_sms, stream);
+  if (p.nmt == 0) return launch_plain<kFmtInt8>(p, num_sms, stream);
+  if (p.nmt == 1) return launch_project<kFmtInt8, 1>(p, num_sms, stream);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace svdq
