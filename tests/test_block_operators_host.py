@@ -1,0 +1,287 @@
+"""CPU tests of the refusals of the operators around the layer: the
+normalisation (svdq_norm), the residual epilogue (svdq_residual) and the rotary
+positions (svdq_rope, svdq_heads).  Layers are host-only and addresses made up:
+every call must be answered before any of them is used -- bad arguments with
+SVDQ_EINVAL, what is not built with SVDQ_EUNSUPPORTED, and a good call with
+SVDQ_ESTATE for want of a device copy.
+"""
+import ctypes
+
+import numpy as np
+import pytest
+
+import synthetic as syn
+
+import w4a4_diffusion_transformer_b200 as lib
+
+A = 1 << 30                                   # made-up 16-byte aligned addresses, a gigabyte apart
+B, C, D, E, F = 2 * A, 3 * A, 4 * A, 5 * A, 6 * A
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from w4a4_diffusion_transformer_b200 import build
+    build.build()
+    lib.load()
+
+
+def _layer(K=256, N=128, fmt="nvfp4", rank=32):
+    d = syn.custom_layer(61, M=16, K=K, N=N, calib_tokens=8)
+    return lib.Layer.prepare(syn.bf16_bits(d["W"]), None, None if fmt == "w4a16" else syn.bf16_bits(d["Xc"]), fmt=fmt,
+                             rank=rank if fmt != "w4a16" else 0, device=-1)
+
+
+@pytest.fixture(scope="module")
+def layer():
+    return _layer()
+
+
+def status(fn):
+    try:
+        fn()
+    except lib.SvdqError as e:
+        return e.status
+    return lib.OK
+
+
+# ------------------------------------------------------------------ normalisation
+
+def norm_call(L, M=4, X=A, codes=B, scales=C, xl=D, Y=None, **kw):
+    return status(lambda: L.norm_quantize_act(lib.Norm(**kw), X, M, codes, scales, xl, None, Y))
+
+
+def test_norm_good_call_wants_a_device(layer):
+    assert norm_call(layer) == lib.ESTATE
+    assert norm_call(layer, residual=E, sum=F, weight=E, scale=E, shift=E, mod_stride=512, rows_per_mod=2,
+                     center=True) == lib.ESTATE
+    assert norm_call(layer, sum=A) == lib.ESTATE                       # in place of X
+    assert norm_call(layer, residual=E, sum=E) == lib.ESTATE           # ... or of the residual
+    assert norm_call(_layer(fmt="w8a8", rank=0), xl=None) == lib.ESTATE
+
+
+@pytest.mark.parametrize("kw", [
+    dict(X=None), dict(X=A + 8), dict(codes=None), dict(codes=B + 2), dict(scales=None), dict(scales=C + 4),
+    dict(xl=D + 8), dict(M=0), dict(M=-3), dict(Y=F + 2),
+    dict(residual=E + 8), dict(sum=E + 8), dict(weight=E + 2), dict(scale=E + 4), dict(shift=E + 8),
+    dict(eps=0.0), dict(eps=-1e-6), dict(eps=float("nan")), dict(eps=float("inf")),
+    dict(scale=E, mod_stride=12, rows_per_mod=2), dict(scale=E, mod_stride=-8, rows_per_mod=2),
+    dict(shift=E, mod_stride=256, rows_per_mod=-1),
+    dict(sum=A + 16), dict(sum=A - 256), dict(residual=E, sum=E + 32),
+    dict(Y=A), dict(Y=A + 1024), dict(residual=E, Y=E), dict(sum=E, Y=E + 2032)])
+def test_norm_refuses(layer, kw):
+    assert norm_call(layer, **kw) == lib.EINVAL
+
+
+def test_norm_refuses_flags_missing_xl_and_null(layer):
+    n = lib.Norm()
+    n._c.flags = 2
+    f = lib.load().svdq_norm_quantize_act
+    assert f(layer._h, n._ref, A, 4, B, C, D, None, None) == lib.EINVAL
+    assert f(layer._h, None, A, 4, B, C, D, None, None) == lib.EINVAL
+    assert f(None, lib.Norm()._ref, A, 4, B, C, D, None, None) == lib.EINVAL
+    assert f(layer._h, lib.Norm()._ref, A, 4, B, C, None, None, None) == lib.EINVAL
+
+
+def test_norm_unsupported():
+    assert norm_call(_layer(fmt="w4a16")) == lib.EUNSUPPORTED
+    wide = _layer(K=14336 + 64, N=16, fmt="w8a8", rank=0)
+    assert norm_call(wide, xl=None) == lib.EUNSUPPORTED
+    assert norm_call(_layer(K=14336, N=16, fmt="w8a8", rank=0), xl=None) == lib.ESTATE
+
+
+def test_norm_forward_refuses(layer):
+    n, need = lib.Norm(), layer.workspace_bytes(4)
+
+    def call(X=A, Y=E, ws=F, wsb=need, flags=0, norm=n, M=4):
+        return status(lambda: layer.norm_forward(norm, X, M, Y, ws, wsb, None, flags))
+    assert call() == lib.ESTATE
+    assert call(flags=lib.FWD_GELU | lib.FWD_CHECK) == lib.ESTATE
+    for bad in (dict(X=None), dict(Y=None), dict(Y=E + 8), dict(ws=None), dict(ws=F + 16), dict(wsb=need - 1),
+                dict(Y=A), dict(Y=A + 16), dict(norm=lib.Norm(sum=E)), dict(M=0)):
+        assert call(**bad) == lib.EINVAL, bad
+    for flags in (lib.FWD_UNFUSED, lib.FWD_NO_BRANCH, 0x100):
+        assert call(flags=flags) == lib.EUNSUPPORTED
+
+
+# ------------------------------------------------------------------ residual
+
+def test_residual_refuses(layer):
+    def call(res=D, M=4, codes=A, scales=B, xl=C, Y=E, flags=0, L=layer, **kw):
+        return status(lambda: L.gemm_residual(codes, scales, xl, M, lib.Residual(res, **kw), Y, None, flags))
+    assert call() == lib.ESTATE
+    assert call(res=E) == lib.ESTATE                                   # in place
+    assert call(gate=F, gate_stride=256, rows_per_gate=2) == lib.ESTATE
+    for bad in (dict(res=None), dict(res=D + 8), dict(res=E + 16), dict(res=E - 512), dict(Y=None), dict(Y=E + 2),
+                dict(codes=None), dict(M=0), dict(gate=F + 8), dict(gate=F, gate_stride=4, rows_per_gate=1),
+                dict(gate=F, gate_stride=-8, rows_per_gate=1), dict(gate=F, gate_stride=128, rows_per_gate=-1),
+                dict(scales=B + 2), dict(xl=C + 4)):
+        assert call(**bad) == lib.EINVAL, bad
+    assert call(flags=lib.FWD_UNFUSED) == lib.EUNSUPPORTED
+    assert call(L=_layer(fmt="w4a16")) in (lib.EUNSUPPORTED, lib.ESTATE)
+    need = layer.workspace_bytes(4)
+
+    def fwd(X=A, Y=E, ws=F, wsb=need, flags=0, res=D):
+        return status(lambda: layer.forward_residual(X, 4, lib.Residual(res), Y, ws, wsb, None, flags))
+    assert fwd() == lib.ESTATE
+    for bad in (dict(X=None), dict(X=A + 2), dict(Y=A), dict(Y=A + 64), dict(res=None), dict(res=E + 32)):
+        assert fwd(**bad) == lib.EINVAL, bad
+    for flags in (lib.FWD_UNFUSED, lib.FWD_NO_BRANCH):
+        assert fwd(flags=flags) == lib.EUNSUPPORTED
+    assert lib.load().svdq_gemm_residual(layer._h, A, B, C, 4, None, E, None, 0) == lib.EINVAL
+
+
+def test_mlp_block_refuses():
+    fc1, fc2 = _layer(K=256, N=512), _layer(K=512, N=256)
+    f = lib.load().svdq_mlp_block_forward
+    n, r = lib.Norm(sum=A), lib.Residual(A)
+
+    def call(a=fc1, b=fc2, norm=n, X=A, M=4, res=r, Y=A, ws=F, wsb=1 << 28, flags=lib.FWD_GELU):
+        return f(a and a._h, b and b._h, norm and norm._ref, X, M, res and res._ref, Y, ws, wsb, None, flags)
+    assert call() == lib.ESTATE                                        # the stream in place throughout
+    assert call(norm=None, res=None, Y=E) == lib.ESTATE
+    for bad in (dict(X=None), dict(Y=None), dict(M=0), dict(b=None), dict(a=None), dict(norm=lib.Norm(eps=0.0)),
+                dict(res=lib.Residual(A + 16)), dict(norm=lib.Norm(sum=A + 64))):
+        assert call(**bad) == lib.EINVAL, bad
+
+
+# ------------------------------------------------------------------ rotary positions
+
+def heads(in_=A, out=B, n=2, weight=None, **strides):
+    h = lib.HeadsStruct()
+    h.in_, h.out, h.heads, h.weight = in_, out, n, weight
+    s = dict(in_batch=4 * 128, in_token=128, in_head=64, out_batch=4 * 128, out_token=128, out_head=64)
+    s.update(strides)
+    for k, v in s.items():
+        setattr(h, k, v)
+    return h
+
+
+def rope_call(rope=None, q="default", k=None, batch=2, T=4, positions=C, pos_batch=0):
+    rope = lib.Rope(64, (16, 24, 24)) if rope is None else rope
+    q = heads() if q == "default" else q
+    return lib.load().svdq_rope_heads(rope._ref, None if q is None else ctypes.addressof(q),
+                                      None if k is None else ctypes.addressof(k), batch, T, positions, pos_batch, None)
+
+
+def mended(**kw):
+    r = lib.Rope(64, (16, 24, 24))
+    for k, v in kw.items():
+        if k == "dim":
+            for i, d in enumerate(v):
+                r._c.dim[i] = d
+        else:
+            setattr(r._c, k, v)
+    return r
+
+
+@pytest.mark.parametrize("kw", [
+    dict(axes=0), dict(axes=5), dict(axes=-1), dict(dim=(16, 0, 24)), dict(dim=(15, 24, 24)), dict(dim=(-2, 24, 24)),
+    dict(dim=(16, 24, 26)), dict(head_dim=0), dict(theta=0.0), dict(theta=-1.0), dict(theta=float("nan")),
+    dict(theta=float("inf")), dict(flags=8), dict(flags=lib.ROPE_NORM, eps=0.0),
+    dict(flags=lib.ROPE_NORM, eps=float("nan"))])
+def test_rope_refuses_its_description(kw):
+    assert rope_call(mended(**kw)) == lib.EINVAL
+
+
+def test_rope_unsupported_sizes():
+    assert rope_call(lib.Rope(68, (16, 24, 24))) == lib.EUNSUPPORTED       # not a multiple of 8
+    assert rope_call(lib.Rope(264, (16, 24, 24))) == lib.EUNSUPPORTED
+    assert rope_call(lib.Rope(64, (16, 24, 20), half=True)) == lib.EUNSUPPORTED   # halves of 30 values
+
+
+@pytest.mark.parametrize("q", [
+    None, heads(in_=None), heads(out=None), heads(in_=A + 8), heads(out=B + 2), heads(weight=C + 4), heads(n=0),
+    heads(in_token=-128), heads(out_head=60), heads(in_head=4),
+    heads(out_head=0), heads(out_token=64), heads(out_batch=0), heads(out_head=56),       # outputs that meet
+    heads(out=A, out_head=256, out_token=64), heads(out=A + 128), heads(out=A, out_token=256, out_batch=1024),
+    heads(out=A + 16)])
+def test_rope_refuses_heads(q):
+    assert rope_call(q=q) == lib.EINVAL
+    if q is not None:
+        assert rope_call(k=q) == lib.EINVAL
+
+
+@pytest.mark.parametrize("kw", [dict(batch=0), dict(T=0), dict(batch=-1), dict(batch=70000), dict(positions=None),
+                                dict(positions=C + 2), dict(pos_batch=-1)])
+def test_rope_refuses_calls(kw):
+    assert rope_call(**kw) == lib.EINVAL
+    assert lib.load().svdq_rope_heads(None, ctypes.addressof(heads()), None, 2, 4, C, 0, None) == lib.EINVAL
+
+
+def test_rope_binding_checks_shapes():
+    import torch
+    x = torch.zeros((2, 4, 2, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        lib.Heads(x)                                                    # host memory
+    with pytest.raises(ValueError):
+        lib.Rope(64, ())
+    with pytest.raises(ValueError):
+        lib.Rope(64, (8,) * 5)
+
+
+def test_qkv_refuses():
+    L = _layer(K=256, N=64 * 6)
+    need = L.workspace_bytes(8)
+    rope = lib.Rope(64, (16, 24, 24), norm=True)
+
+    def call(norm=None, X=A, batch=2, T=4, rp=rope, hq=2, hk=2, qw=D, kw=D, pos=C, Y=E, ws=F, wsb=need, flags=0):
+        return status(lambda: L.qkv_forward(norm, X, batch, T, rp, hq, hk, pos, Y, ws, wsb, qw, kw, None, flags))
+    assert call() == lib.ESTATE
+    assert call(norm=lib.Norm(weight=D)) == lib.ESTATE
+    assert call(hk=0, qw=None, kw=None) == lib.ESTATE
+    for bad in (dict(X=None), dict(Y=None), dict(batch=0), dict(T=0), dict(hq=0), dict(hk=-1), dict(hq=5, hk=2),
+                dict(pos=None), dict(qw=D + 2), dict(Y=A), dict(norm=lib.Norm(eps=-1.0)), dict(rp=mended(axes=9))):
+        assert call(**bad) == lib.EINVAL, bad
+    assert call(flags=lib.FWD_GELU) == lib.EUNSUPPORTED
+
+
+# ------------------------------------------------------------------ the binding's own checks
+
+class FakeRows:
+    """A CUDA BF16 tensor's shape and strides, no memory."""
+
+    def __init__(self, shape, strides, dtype="torch.bfloat16", cuda=True):
+        self.shape, self._s, self.is_cuda = shape, strides, cuda
+        self.dtype = type("T", (), {"is_floating_point": True, "__str__": lambda s: dtype})()
+
+    def dim(self):
+        return len(self.shape)
+
+    def stride(self, i=None):
+        return self._s if i is None else self._s[i]
+
+    def element_size(self):
+        return 2
+
+    def numel(self):
+        return int(np.prod(self.shape))
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return D
+
+
+def test_binding_checks_modulation_rows(layer):
+    rows = lambda n, c, s=1536, **kw: FakeRows((n, c), (s, 1), **kw)  # noqa: E731
+    with pytest.raises(ValueError, match="rows"):
+        norm_call(layer, M=9, scale=rows(2, 256), rows_per_mod=4)      # three rows are read
+    with pytest.raises(ValueError, match="columns"):
+        norm_call(layer, scale=rows(2, 128), rows_per_mod=4)
+    with pytest.raises(ValueError, match="BF16"):
+        lib.Norm(scale=rows(1, 256, dtype="torch.float16"))
+    with pytest.raises(ValueError, match="CUDA"):
+        lib.Norm(shift=rows(1, 256, cuda=False))
+    with pytest.raises(ValueError, match="distance"):
+        lib.Norm(scale=rows(2, 256), shift=rows(2, 256, 512), rows_per_mod=4)
+    with pytest.raises(ValueError, match="contiguous"):
+        lib.Norm(scale=FakeRows((2, 256), (1, 2)))
+    n = lib.Norm(scale=rows(3, 256), shift=rows(3, 256), rows_per_mod=4)
+    assert n._c.mod_stride == 1536
+    assert status(lambda: layer.norm_quantize_act(n, A, 9, B, C, E)) == lib.ESTATE
+    r = lib.Residual(D, gate=rows(2, 128), rows_per_gate=4)
+    assert r._c.gate_stride == 1536
+    with pytest.raises(ValueError, match="rows"):
+        layer.gemm_residual(A, B, C, 9, r, E)
+    assert status(lambda: layer.gemm_residual(A, B, C, 8, r, E)) == lib.ESTATE

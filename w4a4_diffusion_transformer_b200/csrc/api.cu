@@ -1499,11 +1499,11 @@ svdq_status svdq_norm_quantize_act(const svdq_layer* L, const svdq_norm* norm, c
   if (!scales) return SVDQ_EINVAL;
   const svdq_status sn = check_norm(L, norm, X, M);
   if (sn != SVDQ_OK) return sn;
-  if (st != SVDQ_OK) return st;
   if ((L->host.rank > 0 || L->host.lora_r > 0) && !xl) return SVDQ_EINVAL;
   const size_t act = (size_t)M * L->host.K * 2;
   if (overlap(Y, act, X, act) || overlap(Y, act, norm->residual, act) || overlap(Y, act, norm->sum, act))
     return SVDQ_EINVAL;
+  if (st != SVDQ_OK) return st;
   DeviceGuard g(L->device);
   if (!g.ok) return SVDQ_ECUDA;
   return run_norm(L, norm, X, M, codes, scales, xl, Y, static_cast<cudaStream_t>(stream));
