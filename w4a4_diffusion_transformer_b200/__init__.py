@@ -258,9 +258,14 @@ class Norm:
 
     def __init__(self, residual=None, sum=None, weight=None, scale=None, shift=None, rows_per_mod: int = 0,
                  mod_stride: Optional[int] = None, eps: float = 1e-6, center: bool = False):
+        # placement and layout are checked once, here; the sizes at each call
+        self._held = []
         for t, what in ((residual, "residual"), (sum, "sum"), (weight, "weight")):
             if _is_tensor(t):
                 _bf16_tensor(t, what)
+            held = _held_bytes(t, what, True)
+            if held is not None:
+                self._held.append((held, what == "weight", what))
         rows = [_Rows(t, what, mod_stride) for t, what in ((scale, "scale"), (shift, "shift")) if t is not None]
         strides = {r.stride for r in rows if r.rows != 1 or mod_stride is not None}
         if len(strides) > 1:
@@ -273,13 +278,10 @@ class Norm:
         self._ref = ctypes.addressof(self._c)
 
     def _need(self, M: int, K: int):
-        residual, total, weight = self._keep[:3]
-        if residual is not None:
-            _need(residual, M * K * 2, "residual")
-        if total is not None:
-            _need(total, M * K * 2, "sum")
-        if weight is not None:
-            _need(weight, K * 2, "weight")
+        for held, one_row, what in self._held:
+            need = K * 2 if one_row else M * K * 2
+            if held < need:
+                raise ValueError(f"{what}: holds {held} bytes, the call accesses {need}")
         for r in self._rows:
             r.need(M, K, self._per)
 
@@ -292,6 +294,7 @@ class Residual:
     def __init__(self, residual, gate=None, rows_per_gate: int = 0, gate_stride: Optional[int] = None):
         if _is_tensor(residual):
             _bf16_tensor(residual, "residual")
+        self._held = _held_bytes(residual, "residual", True)
         self._keep = (residual, gate)
         self._rows = None if gate is None else _Rows(gate, "gate", gate_stride)
         self._per = int(rows_per_gate)
@@ -300,7 +303,8 @@ class Residual:
         self._ref = ctypes.addressof(self._c)
 
     def _need(self, M: int, N: int):
-        _need(self._keep[0], M * N * 2, "residual")
+        if self._held is not None and self._held < M * N * 2:
+            raise ValueError(f"residual: holds {self._held} bytes, the call accesses {M * N * 2}")
         if self._rows is not None:
             self._rows.need(M, N, self._per)
 
@@ -384,6 +388,7 @@ class Layer:
         self._h = ctypes.c_void_p(handle)
         info = self.info
         self._K, self._N = info["K"], info["N"]
+        self._act_last = (0, 0, 0)
         self._xl_cols = self._xl_width()
 
     def _xl_width(self) -> int:
@@ -496,6 +501,12 @@ class Layer:
     def act_code_bytes(self, M: int) -> int:
         return int(load().svdq_act_code_bytes(self._h, M))
 
+    def _act_bytes(self, M: int):
+        # (code, scale) bytes for M tokens, which a caller tends to ask for again and again
+        if self._act_last[0] != M:
+            self._act_last = (M, self.act_code_bytes(M), self.act_scale_bytes(M))
+        return self._act_last[1:]
+
     def act_codes_to_logical(self, device_layout: np.ndarray, M: int) -> np.ndarray:
         """Activation codes in the GEMM's layout -> uint8 [M][K/2] (two codes per
         byte); W8A8: int8 [M][K]."""
@@ -517,9 +528,9 @@ class Layer:
         if Y is not None:
             _need(Y, M * self._N * 2, "Y")
         if codes is not None:
-            _need(codes, self.act_code_bytes(M), "codes")
+            _need(codes, self._act_bytes(M)[0], "codes")
         if scales is not None:
-            _need(scales, self.act_scale_bytes(M), "scales")
+            _need(scales, self._act_bytes(M)[1], "scales")
         if xl is not None:
             _need(xl, M * self._xl_cols * 2, "xl")
 
