@@ -27,6 +27,7 @@ struct svdq_layer {
   // device buffers (owned)
   float* d_inv_lam = nullptr;
   __nv_bfloat16* d_l1t = nullptr;    // [32][K]   L1d^T
+  __nv_bfloat16* d_l1f = nullptr;    // L1d^T in the normalising kernel's operand order (pack_fragments)
   __nv_bfloat16* d_l2s = nullptr;    // [N][32]   (L2b / alpha)^T
   __nv_bfloat16* d_l2t = nullptr;    // [N][32]   L2b^T (unfused up projection)
   uint8_t* d_wq = nullptr;           // INT4: codes [N][K/2]; W4A16: the GEMV's packed weights
@@ -42,6 +43,7 @@ struct svdq_layer {
   int k2_kernel = 0;                     // NVFP4 GEMM: 0 = by size, 1 = single-CTA, 2 = CTA pairs
   // LoRA adapter (svdq_set_lora): A^T rows for the down pass, (s B)^T rows for the up pass
   __nv_bfloat16* d_lora_l1t = nullptr;   // [32][K]   A^T, zero rows past r
+  __nv_bfloat16* d_lora_l1f = nullptr;   // the same in pack_fragments order
   __nv_bfloat16* d_lora_l2s = nullptr;   // [N][32]   (bf16(s B) / alpha)^T (NVFP4 GEMM)
   __nv_bfloat16* d_lora_l2t = nullptr;   // [N][64]   [L2b^T | bf16(s B)^T] (unfused up projection)
   CUtensorMap tm_lora_l1t, tm_lora_l2s;
@@ -195,11 +197,26 @@ cudaError_t upload(T** dst, const void* src, size_t bytes) {
   return e;
 }
 
+// [32][K] rows (K a multiple of 64) in the order the normalising kernel's tensor
+// instructions read them: per block of 32 columns and half of 16 rows, rows
+// 0-7 and then rows 8-15, lane l's 16 bytes being columns 8 (l % 4) .. + 7 of
+// row l / 4: each load of a warp is 512 consecutive bytes.
+std::vector<uint16_t> pack_fragments(const std::vector<uint16_t>& rows, int K) {
+  std::vector<uint16_t> out(rows.size());
+  size_t o = 0;
+  for (int kb = 0; kb < K / 32; ++kb)
+    for (int r8 = 0; r8 < 4; ++r8)
+      for (int l = 0; l < 32; ++l)
+        for (int e = 0; e < 8; ++e) out[o++] = rows[(size_t)(8 * r8 + l / 4) * K + kb * 32 + 8 * (l % 4) + e];
+  return out;
+}
+
 void free_device(svdq_layer* L) {
   if (L->device < 0) return;
   DeviceGuard g(L->device);
   cudaFree(L->d_inv_lam);
   cudaFree(L->d_l1t);
+  cudaFree(L->d_l1f);
   cudaFree(L->d_l2s);
   cudaFree(L->d_l2t);
   cudaFree(L->d_wq);
@@ -209,10 +226,11 @@ void free_device(svdq_layer* L) {
   cudaFree(L->d_bias);
   cudaFree(L->d_err);
   cudaFree(L->d_lora_l1t);
+  cudaFree(L->d_lora_l1f);
   cudaFree(L->d_lora_l2s);
   cudaFree(L->d_lora_l2t);
   L->d_inv_lam = nullptr;
-  L->d_lora_l1t = L->d_lora_l2s = L->d_lora_l2t = nullptr;
+  L->d_lora_l1t = L->d_lora_l1f = L->d_lora_l2s = L->d_lora_l2t = nullptr;
 }
 
 svdq_status upload_layer(svdq_layer* L, int device) {
@@ -300,6 +318,7 @@ svdq_status upload_layer(svdq_layer* L, int device) {
       }
     }
     chk(upload(&L->d_l1t, l1t.data(), l1t.size() * 2));
+    if (r > 0) chk(upload(&L->d_l1f, pack_fragments(l1t, K).data(), l1t.size() * 2));
     chk(upload(&L->d_l2s, l2s.data(), l2s.size() * 2));
     chk(upload(&L->d_l2t, l2t.data(), l2t.size() * 2));
     if (e != cudaSuccess) return SVDQ_ECUDA;
@@ -565,9 +584,10 @@ svdq_status upload_lora(svdq_layer* L) {
   const HostPrep& h = L->host;
   const int K = h.K, N = h.N, r = h.lora_r;
   cudaFree(L->d_lora_l1t);
+  cudaFree(L->d_lora_l1f);
   cudaFree(L->d_lora_l2s);
   cudaFree(L->d_lora_l2t);
-  L->d_lora_l1t = L->d_lora_l2s = L->d_lora_l2t = nullptr;
+  L->d_lora_l1t = L->d_lora_l1f = L->d_lora_l2s = L->d_lora_l2t = nullptr;
   if (r == 0) return SVDQ_OK;
   // the GEMM's accumulator unit: alpha = g_x g_w (NVFP4) or 2^(ex + ew) (INT4)
   const int alpha_exp = h.format == SVDQ_NVFP4 ? h.g_x_exp + h.g_w_exp : L->i4_ex + L->i4_ew;
@@ -584,15 +604,17 @@ svdq_status upload_lora(svdq_layer* L) {
     }
   }
   cudaError_t e = upload(&L->d_lora_l1t, l1t.data(), l1t.size() * 2);
+  if (e == cudaSuccess) e = upload(&L->d_lora_l1f, pack_fragments(l1t, K).data(), l1t.size() * 2);
   if (e == cudaSuccess) e = upload(&L->d_lora_l2s, l2s.data(), l2s.size() * 2);
   if (e == cudaSuccess) e = upload(&L->d_lora_l2t, l2t.data(), l2t.size() * 2);
   if (e != cudaSuccess || !make_map_kchunks(&L->tm_lora_l1t, L->d_lora_l1t, K, 32, 32) ||
       !make_map(&L->tm_lora_l2s, L->d_lora_l2s, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, 32, N, 32, 256,
                 CU_TENSOR_MAP_SWIZZLE_64B)) {
     cudaFree(L->d_lora_l1t);
+    cudaFree(L->d_lora_l1f);
     cudaFree(L->d_lora_l2s);
     cudaFree(L->d_lora_l2t);
-    L->d_lora_l1t = L->d_lora_l2s = L->d_lora_l2t = nullptr;
+    L->d_lora_l1t = L->d_lora_l1f = L->d_lora_l2s = L->d_lora_l2t = nullptr;
     return e == cudaErrorMemoryAllocation ? SVDQ_ENOMEM : SVDQ_ECUDA;
   }
   return SVDQ_OK;
@@ -802,12 +824,12 @@ svdq_status run_norm(const svdq_layer* L, const svdq_norm* n, const void* X, int
   // rank 32 is two blocks of 16 columns, W8A8's rank 16 one (its XL columns
   // 16..31 are zero), an adapter two more
   for (int i = 0; i < (h.rank + 15) / 16; ++i, ++p.nmt) {
-    p.amat[p.nmt] = L->d_l1t + (size_t)16 * i * h.K;
+    p.amat[p.nmt] = L->d_l1f + 512 * i;
     p.xl_col[p.nmt] = 16 * i;
   }
   p.xl_zero = h.rank == 16 ? 16 : 0;
   for (int i = 0; h.lora_r > 0 && i < 2; ++i, ++p.nmt) {
-    p.amat[p.nmt] = L->d_lora_l1t + (size_t)16 * i * h.K;
+    p.amat[p.nmt] = L->d_lora_l1f + 512 * i;
     p.xl_col[p.nmt] = 32 + 16 * i;
   }
   const int fmt = h.format == SVDQ_NVFP4 ? kFmtNvfp4 : w8a8(h) ? kFmtInt8 : kFmtInt4;

@@ -177,7 +177,8 @@ struct NormParams {
   __nv_bfloat16* xl;            // row stride xl_stride elements
   int xl_stride;
   int nmt;                      // blocks of 16 branch columns to project: 0, 1 (W8A8), 2 or 4
-  const __nv_bfloat16* amat[4]; // [16][K] each: rows of L1d^T, then of the adapter's A^T
+  const __nv_bfloat16* amat[4]; // 16 rows each of L1d^T, then of the adapter's A^T, in 1 KB blocks of 32 columns,
+                                // 2 KB apart (pack_fragments)
   int xl_col[4];                // XL column of each block's first
   int log2_warps;               // warps to a row, tiles of a CTA (set by the launcher)
   int tiles_each, tiles_extra;

@@ -338,9 +338,9 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) norm_quant_kernel(co
       uint4 lo[kAcc], hi[kAcc], b0 = make_uint4(0u, 0u, 0u, 0u), b1 = b0;
 #pragma unroll
       for (int mt = 0; mt < kMt; ++mt) {
-        const __nv_bfloat16* a = p.amat[mt] + (size_t)g * K + kb * 32 + c * 8;
-        lo[mt] = *reinterpret_cast<const uint4*>(a);
-        hi[mt] = *reinterpret_cast<const uint4*>(a + 8 * (size_t)K);
+        const uint4* a = reinterpret_cast<const uint4*>(p.amat[mt]) + kb * 128 + lane;
+        lo[mt] = a[0];
+        hi[mt] = a[32];
       }
       if (first) b0 = *reinterpret_cast<const uint4*>(yrow + kb * 64);
       if (second) b1 = *reinterpret_cast<const uint4*>(yrow + 8 * ystride + kb * 64);
