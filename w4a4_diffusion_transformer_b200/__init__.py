@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sys
 from typing import Optional
 
 import numpy as np
@@ -160,6 +161,8 @@ def _ptr(x) -> Optional[int]:
     """Device/host address of a tensor-like object (data_ptr()), an int, or None."""
     if x is None:
         return None
+    if _plain_tensor(x):
+        return x.data_ptr()
     if isinstance(x, int):
         return x
     if hasattr(x, "data_ptr"):
@@ -189,7 +192,24 @@ def _held_bytes(x, what: str, device: bool) -> Optional[int]:
     return None
 
 
+_torch_tensor = None
+
+
+def _plain_tensor(x) -> bool:
+    """Whether x is a torch.Tensor itself (torch need not be importable)."""
+    global _torch_tensor
+    if _torch_tensor is None:
+        torch = sys.modules.get("torch")
+        if torch is None:
+            return False
+        _torch_tensor = torch.Tensor
+    return x.__class__ is _torch_tensor
+
+
 def _need(x, nbytes: int, what: str, device: bool = True):
+    # the usual operand, a contiguous tensor in the right place, without detours
+    if _plain_tensor(x) and x.is_cuda is device and x.is_contiguous() and x.nbytes >= nbytes:
+        return
     have = _held_bytes(x, what, device)
     if have is not None and have < nbytes:
         raise ValueError(f"{what}: holds {have} bytes, the call accesses {nbytes}")

@@ -789,7 +789,7 @@ svdq_status check_norm(const svdq_layer* L, const svdq_norm* n, const void* X, i
   const size_t act = (size_t)M * L->host.K * 2;
   if (n->sum != X && overlap(n->sum, act, X, act)) return SVDQ_EINVAL;
   if (n->sum != n->residual && overlap(n->sum, act, n->residual, act)) return SVDQ_EINVAL;
-  if (!w4a4(L) || !norm_supported(L->host.K)) return SVDQ_EUNSUPPORTED;
+  if (!w4a4(L) || L->host.K > kNormMaxK) return SVDQ_EUNSUPPORTED;
   return SVDQ_OK;
 }
 
@@ -832,8 +832,8 @@ svdq_status run_norm(const svdq_layer* L, const svdq_norm* n, const void* X, int
     p.amat[p.nmt] = L->d_lora_l1f + 512 * i;
     p.xl_col[p.nmt] = 32 + 16 * i;
   }
-  const int fmt = h.format == SVDQ_NVFP4 ? kFmtNvfp4 : w8a8(h) ? kFmtInt8 : kFmtInt4;
-  return launch_norm_quant(p, fmt, L->num_sms, stream) == cudaSuccess ? SVDQ_OK : SVDQ_ECUDA;
+  const auto launch = h.format == SVDQ_NVFP4 ? launch_norm_nvfp4 : w8a8(h) ? launch_norm_int8 : launch_norm_int4;
+  return launch(p, L->num_sms, stream) == cudaSuccess ? SVDQ_OK : SVDQ_ECUDA;
 }
 
 // ------------------------------------------------------------------ rotary positions

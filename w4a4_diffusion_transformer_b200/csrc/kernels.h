@@ -152,7 +152,7 @@ int k1_rows_per_cta();
 cudaError_t launch_rowscale(const __nv_bfloat16* x, const float* inv_lam, int M, int K, int mpad, float* sx,
                             float* inv_sx, cudaStream_t stream);
 
-// Normalisation fused with the first kernel's outputs (norm_quant.cu).
+// Normalisation fused with the first kernel's outputs (norm_quant.cuh).
 struct NormParams {
   int M, K;
   int mpad;                     // M rounded up to 128: rows of the scale layouts (and of tiled codes)
@@ -186,8 +186,10 @@ struct NormParams {
 };
 constexpr int kNormMaxK = 14336;              // a row's parameters and its tile fit in shared memory
 constexpr size_t kNormMaxSmem = 232448;
-bool norm_supported(int K);
-cudaError_t launch_norm_quant(NormParams p, int fmt, int num_sms, cudaStream_t stream);
+// one translation unit per code format; each sets the parameters its launch chooses
+cudaError_t launch_norm_nvfp4(NormParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_norm_int4(NormParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_norm_int8(NormParams& p, int num_sms, cudaStream_t stream);
 
 // Rotary positions with several axes (rope.cu).  Strides in elements.
 struct RopeTensor {

@@ -12,6 +12,8 @@
 // later layer reads, and y because it is the layer's BF16 input: the codes are
 // then bit for bit those of the unfused sequence on the same y.  Sums, means
 // and products are FP32.
+#pragma once
+
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -23,11 +25,11 @@ namespace svdq {
 
 namespace {
 
-// A CTA of 8 warps (16 with a projection) handles tiles of 8 / W rows, W warps to a row; a lane of the
-// row's warp w owns the C chunks of 8 values 32 (C w + c) + lane and keeps them
-// in registers, as FP32, from the load to the codes (unpacking BF16 pairs again
-// for every pass took twice the instructions, and those are what bounds the
-// kernel before memory does).  Consecutive chunks lie a constant apart in every
+// A CTA of 8 warps (16 with a projection) handles tiles of 8 / W (16 / W) rows, W
+// warps to a row; a lane of the row's warp w owns the C chunks of 8 values
+// 32 (C w + c) + lane and keeps them in registers, as FP32, from the load to the
+// codes (unpacking BF16 pairs again for every pass took twice the instructions,
+// and those are what bounds the kernel before memory does).  Consecutive chunks lie a constant apart in every
 // operand and layout, so that their addresses are immediates.  The columns'
 // parameters w (1 + scale), shift and 1/lam sit in shared memory as FP32, filled
 // once per CTA and modulation row; chunk q's eight values are two 16-byte words
@@ -85,8 +87,9 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// kMt: blocks of 16 branch columns to project (0: no projection).
-template <int kFmt, int C, int kWarps, int kMt>
+// kMt: blocks of 16 branch columns to project (0: no projection).  kFull: every
+// lane has C chunks (K = 256 C W), so that no access needs a predicate.
+template <int kFmt, int C, int kWarps, int kMt, bool kFull>
 __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) norm_quant_kernel(const __grid_constant__ NormParams p) {
   constexpr int kThreads = kWarps * 32;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -103,7 +106,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) norm_quant_kernel(co
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rg = warp >> p.log2_warps, w = warp & (W - 1);   // this warp's row of the tile, its place in the row
   const int q0 = w * (32 * C) + lane;                   // first chunk; the next are 32 apart
-  const int nc = min(C, max(0, (nch - q0 + 31) >> 5));  // this lane's chunks
+  const int nc = kFull ? C : min(C, max(0, (nch - q0 + 31) >> 5));   // this lane's chunks
 
   dev::griddep_launch_dependents();
   if (kFmt == kFmtNvfp4 && threadIdx.x < 16) rcp[threadIdx.x] = p.rcp[threadIdx.x];
@@ -121,8 +124,9 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) norm_quant_kernel(co
   for (int tile = t0; tile < t1; ++tile) {
     const int row = tile * rows + rg;
     const bool live = row < M;                          // rows M .. mpad - 1: zero codes and scales
-    const int n = live ? nc : 0;                        // chunks to load and store
-    const size_t at = (size_t)row * K + 8 * q0;
+    const uint32_t keep = live ? 0xFFFFFFFFu : 0u;
+    // a dead row computes on the last one's values and stores zeros
+    const size_t at = (size_t)min(row, M - 1) * K + 8 * q0;
     float* slot = slots + ((tile & 1) * 3) * kWarps + rg * W;
     float2 f[C][4];                                     // h, then h - mu, then y / lam
     // ---- h = bf16(x + r)
@@ -131,23 +135,23 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) norm_quant_kernel(co
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         v[c] = make_uint4(0u, 0u, 0u, 0u);
-        if (c < n) v[c] = *reinterpret_cast<const uint4*>(p.x + at + 256 * c);
+        if (c < nc) v[c] = *reinterpret_cast<const uint4*>(p.x + at + 256 * c);
       }
       if (p.residual) {
         const __nv_bfloat16* r = p.residual + at;
 #pragma unroll
         for (int c = 0; c < C; ++c)
-          if (c < n) {
+          if (c < nc) {
             const uint4 u = *reinterpret_cast<const uint4*>(r + 256 * c);
             v[c] = make_uint4(add_bf16x2(v[c].x, u.x), add_bf16x2(v[c].y, u.y), add_bf16x2(v[c].z, u.z),
                               add_bf16x2(v[c].w, u.w));
           }
       }
-      if (p.sum) {
+      if (p.sum && live) {
         __nv_bfloat16* o = p.sum + at;
 #pragma unroll
         for (int c = 0; c < C; ++c)
-          if (c < n) *reinterpret_cast<uint4*>(o + 256 * c) = v[c];
+          if (c < nc) *reinterpret_cast<uint4*>(o + 256 * c) = v[c];
       }
 #pragma unroll
       for (int c = 0; c < C; ++c) {
@@ -216,7 +220,13 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) norm_quant_kernel(co
       }
       if (m != mine) continue;
       // ---- y = bf16(n w (1 + scale) + shift), and the 4-bit quantizers
-      __nv_bfloat16* yout = p.y ? p.y + at : nullptr;
+      uint8_t* codes_at = nullptr;
+      uint8_t* scales_at = nullptr;
+      if (kFmt == kFmtNvfp4) {
+        codes_at = p.codes + act_tile_offset(row, q0 >> 5, lane >> 2, p.nst) + (lane & 3) * 4;
+        scales_at = p.scales + sf_offset(row, q0 >> 1, K);
+      }
+      __nv_bfloat16* yout = p.y && live ? p.y + at : nullptr;
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const int q = q0 + 32 * c;
@@ -232,8 +242,8 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) norm_quant_kernel(co
             y[i] = pack2(__ffma2_rn(__fmul2_rn(f[c][i], rstd2), g[i], sh[i]));
             f[c][i] = __fmul2_rn(unpack2(y[i]), il[i]);
           }
-          if (kMt > 0 && live) *reinterpret_cast<uint4*>(ytile + rg * ystride + q * 16) = make_uint4(y[0], y[1], y[2], y[3]);
-          if (yout && live) *reinterpret_cast<uint4*>(yout + 256 * c) = make_uint4(y[0], y[1], y[2], y[3]);
+          if (kMt > 0) *reinterpret_cast<uint4*>(ytile + rg * ystride + q * 16) = make_uint4(y[0], y[1], y[2], y[3]);
+          if (yout) *reinterpret_cast<uint4*>(yout + 256 * c) = make_uint4(y[0], y[1], y[2], y[3]);
         }
         float a = fmaxf(fabsf(f[c][0].x), fabsf(f[c][0].y));
 #pragma unroll
@@ -244,15 +254,14 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) norm_quant_kernel(co
           // a group of 16 is two lanes' chunks
           a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
           uint32_t codes = 0u;
-          const uint32_t sb = live ? dev::nvfp4_quant8(f[c], a, p.c_x, p.g_x_exp, rcp, codes) : 0u;
+          const uint32_t sb = dev::nvfp4_quant8(f[c], a, p.c_x, p.g_x_exp, rcp, codes) & keep;
           // four groups' scale bytes are one word of the layout
           uint32_t word = sb << (8 * ((lane >> 1) & 3));
           word |= __shfl_xor_sync(0xffffffffu, word, 2);
           word |= __shfl_xor_sync(0xffffffffu, word, 4);
           if (act) {
-            if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(p.scales + sf_offset(row, q0 >> 1, K) + 2048 * c) = word;
-            *reinterpret_cast<uint32_t*>(p.codes + act_tile_offset(row, q0 >> 5, (lane & 31) >> 2, p.nst) + 16384 * c +
-                                         (lane & 3) * 4) = codes;
+            if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(scales_at + 2048 * c) = word;
+            *reinterpret_cast<uint32_t*>(codes_at + 16384 * c) = codes & keep;
           }
         } else {
           // a group of 64 is eight lanes' chunks
@@ -262,17 +271,15 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) norm_quant_kernel(co
           const __nv_bfloat16 sb = __float2bfloat16_rn(live ? __fmul_rn(a, 1.0f / 7.0f) : 0.f);
           const float sc = __bfloat162float(sb);
           uint32_t codes = 0u;
-          if (sc != 0.f) {
-            const float inv = __frcp_rn(sc);
-            const float2 i2 = make_float2(inv, inv);
+          const float inv = sc == 0.f ? 0.f : __frcp_rn(sc);
+          const float2 i2 = make_float2(inv, inv);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              // the sum with 1.5 * 2^23 holds the rounded integer in its low
-              // bits; the product is rounded before (no fused multiply-add)
-              const float2 k = __fmul2_rn(f[c][i], i2);
-              codes |= (__float_as_uint(__fadd_rn(k.x, 12582912.0f)) & 0xFu) << (8 * i);
-              codes |= (__float_as_uint(__fadd_rn(k.y, 12582912.0f)) & 0xFu) << (8 * i + 4);
-            }
+          for (int i = 0; i < 4; ++i) {
+            // the sum with 1.5 * 2^23 holds the rounded integer in its low
+            // bits; the product is rounded before (no fused multiply-add)
+            const float2 k = __fmul2_rn(f[c][i], i2);
+            codes |= (__float_as_uint(__fadd_rn(k.x, 12582912.0f)) & 0xFu) << (8 * i);
+            codes |= (__float_as_uint(__fadd_rn(k.y, 12582912.0f)) & 0xFu) << (8 * i + 4);
           }
           if (act) {
             if ((lane & 7) == 0)
@@ -386,11 +393,11 @@ size_t smem_bytes(int K, int nmt, int warps, int log2_warps) {
   return head + params + (nmt > 0 ? tile + red : 0);
 }
 
-template <int kFmt, int C, int kWarps, int kMt>
-cudaError_t launch(NormParams& p, int num_sms, cudaStream_t stream) {
+template <int kFmt, int C, int kWarps, int kMt, bool kFull>
+cudaError_t launch_t(NormParams& p, int num_sms, cudaStream_t stream) {
   const size_t smem = smem_bytes(p.K, kMt, kWarps, p.log2_warps);
   if (smem > kNormMaxSmem) return cudaErrorInvalidValue;
-  auto kern = norm_quant_kernel<kFmt, C, kWarps, kMt>;
+  auto kern = norm_quant_kernel<kFmt, C, kWarps, kMt, kFull>;
   static thread_local int configured_device = -1;
   int dev = 0;
   cudaGetDevice(&dev);
@@ -417,6 +424,15 @@ cudaError_t launch(NormParams& p, int num_sms, cudaStream_t stream) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <int kFmt, int C, int kWarps, int kMt>
+cudaError_t launch(NormParams& p, int num_sms, cudaStream_t stream) {
+  // (the unpredicated form of rows with few chunks is not worth its code: with
+  // 12 chunks it took 26.1 instead of 28.6 us for 4608 x 3072 NVFP4 codes and XL)
+  constexpr bool kFull = C >= 6 && kWarps * (kMt > 0) != 8;
+  return kFull && p.K == (256 * C) << p.log2_warps ? launch_t<kFmt, C, kWarps, kMt, kFull>(p, num_sms, stream)
+                                          : launch_t<kFmt, C, kWarps, kMt, false>(p, num_sms, stream);
 }
 
 // Chunks of a lane with 2^l warps to a row.
@@ -460,24 +476,5 @@ cudaError_t launch_project(NormParams& p, int num_sms, cudaStream_t stream) {
   return launch<kFmt, 12, 16, kMt>(p, num_sms, stream);
 }
 
-template <int kFmt>
-cudaError_t launch_4bit(NormParams& p, int num_sms, cudaStream_t stream) {
-  if (p.nmt == 0) return launch_plain<kFmt>(p, num_sms, stream);
-  if (p.nmt == 2) return launch_project<kFmt, 2>(p, num_sms, stream);
-  if (p.nmt == 4) return launch_project<kFmt, 4>(p, num_sms, stream);
-  return cudaErrorInvalidValue;
-}
-
 }  // namespace
-
-bool norm_supported(int K) { return K <= kNormMaxK; }
-
-cudaError_t launch_norm_quant(NormParams p, int fmt, int num_sms, cudaStream_t stream) {
-  if (fmt == kFmtNvfp4) return launch_4bit<kFmtNvfp4>(p, num_sms, stream);
-  if (fmt == kFmtInt4) return launch_4bit<kFmtInt4>(p, num_sms, stream);
-  if (p.nmt == 0) return launch_plain<kFmtInt8>(p, num_sms, stream);
-  if (p.nmt == 1) return launch_project<kFmtInt8, 1>(p, num_sms, stream);
-  return cudaErrorInvalidValue;
-}
-
 }  // namespace svdq

@@ -54,18 +54,17 @@ __device__ __forceinline__ uint32_t nvfp4_quant32(const float2 (&v)[16], float c
 }
 
 // The same quantizer on half a group whose magnitude a is known: the scale
-// byte, and the codes of v's 8 values.
+// byte, and the codes of v's 8 values.  Without a branch: rcp[8] is 0, and a
+// zero scale's codes are cleared (a product with 0 would keep signs).
 __device__ __forceinline__ uint32_t nvfp4_quant8(const float2 (&v)[4], float a, float c_x, int g_x_exp,
                                                  const float* rcp, uint32_t& packed) {
   const uint32_t sb = cvt_e4m3x2(__fmul_rn(a, c_x), 0.f) & 0xFFu;
-  packed = 0u;
-  if (sb != 0u) {
-    const uint32_t e = sb >> 3, m = sb & 7u;
-    const int p2 = (e ? 7 - (int)e : 9) - g_x_exp;
-    const float invs = rcp[(e ? 0 : 8) + m] * __int_as_float((p2 + 127) << 23);
-    const float2 inv2 = make_float2(invs, invs);
-    packed = cvt_e2m1x8(__fmul2_rn(v[0], inv2), __fmul2_rn(v[1], inv2), __fmul2_rn(v[2], inv2), __fmul2_rn(v[3], inv2));
-  }
+  const uint32_t e = sb >> 3, m = sb & 7u;
+  const int p2 = (e ? 7 - (int)e : 9) - g_x_exp;
+  const float invs = rcp[(e ? 0 : 8) + m] * __int_as_float((p2 + 127) << 23);
+  const float2 inv2 = make_float2(invs, invs);
+  packed = cvt_e2m1x8(__fmul2_rn(v[0], inv2), __fmul2_rn(v[1], inv2), __fmul2_rn(v[2], inv2), __fmul2_rn(v[3], inv2));
+  if (sb == 0u) packed = 0u;
   return sb;
 }
 
