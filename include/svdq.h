@@ -465,9 +465,11 @@ typedef struct {
 /* svdq_norm_quantize_act -- normalisation and the first kernel in one pass:
  * writes what svdq_quantize_act(layer, y, M, codes, scales, xl, stream, 0)
  * would write for the normalised rows y, without y going through memory.  Codes
- * and scales are bit for bit those of that call on the same y; XL = bf16(y L1d)
- * (and bf16(y A) with an adapter) sums in another FP32 order and may differ by
- * a BF16 rounding.
+ * and scales are bit for bit those of that call on the same y (rows that hold a
+ * NaN or an infinity aside, which stay in their own row); XL = bf16(y L1d) (and
+ * bf16(y A) with an adapter) sums in another FP32 order and may differ by a BF16
+ * rounding.  A row's FP32 sums have an order of their own for each K, but also
+ * for each size class of M: the same row among fewer rows may round differently.
  *   norm        as above; read during the call only.
  *   X           device, [M][K] BF16, 16-byte aligned.
  *   codes, scales, xl   as for svdq_quantize_act.
@@ -538,7 +540,8 @@ typedef struct {
  *   positions  device, float [T][axes], or [batch][T][axes] with pos_batch
  *              elements between sequences (0: shared).  A non-finite position
  *              gives NaN in the pairs that use it.
- * Runs on the device that holds q->in, whichever is current.  Errors:
+ * Runs on the device that holds q->in, whichever is current; everything else
+ * must be on that device too.  Errors:
  * SVDQ_EINVAL (NULL rope, q, positions or a tensor's pointers, sizes below 1, a
  * batch above 65535, strides, alignment, overlap, flags, theta or eps out of range, memory that is
  * not device memory), SVDQ_EUNSUPPORTED (head_dim, dims as above), SVDQ_ECUDA. */

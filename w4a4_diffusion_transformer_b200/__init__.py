@@ -368,6 +368,10 @@ class Heads:
                 _bf16_tensor(weight, "weight")
             _need(weight, self.head_dim * 2, "weight")
 
+        self.device = x.get_device()
+        if any(_is_tensor(t) and t.get_device() != self.device for t in (out, weight)):
+            raise ValueError("x, out and weight must be on one device")
+
         def strides(t):
             s = tuple(t.stride())[:-1]
             s = s if t.dim() == 4 else (0,) + s
@@ -396,6 +400,8 @@ def rope_heads(rope: Rope, q: Heads, k: Optional[Heads], positions, stream=None)
     for t, what in ((q, "q"), (k, "k")):
         if t is not None and (t.head_dim != rope.head_dim or (t.batch, t.tokens) != (q.batch, q.tokens)):
             raise ValueError(f"{what}: [{t.batch}, {t.tokens}, heads, {t.head_dim}] does not fit the others")
+    if (k is not None and k.device != q.device) or (_is_tensor(positions) and positions.get_device() != q.device):
+        raise ValueError("q, k and the positions must be on one device")
     pos_batch = _positions(rope, positions, q.batch, q.tokens)
     _check(load().svdq_rope_heads(rope._ref, q._ref, None if k is None else k._ref, q.batch, q.tokens,
                                   _ptr(positions), pos_batch, _stream(stream)), "svdq_rope_heads")

@@ -349,6 +349,15 @@ svdq_status upload_layer(svdq_layer* L, int device) {
   return e == cudaSuccess ? SVDQ_OK : SVDQ_ECUDA;
 }
 
+// upload_layer lays the operands out in host memory first.
+svdq_status try_upload(svdq_layer* L, int device) {
+  try {
+    return upload_layer(L, device);
+  } catch (const std::bad_alloc&) {
+    return SVDQ_ENOMEM;
+  }
+}
+
 // Arguments first (SVDQ_EINVAL), then the layer's state (SVDQ_ESTATE).
 svdq_status check_forward_args(const svdq_layer* L, const void* X, int M, const void* Y) {
   if (!L || !X || !Y || M < 1) return SVDQ_EINVAL;
@@ -821,13 +830,13 @@ svdq_status run_norm(const svdq_layer* L, const svdq_norm* n, const void* X, int
   p.scales = k.scales;
   p.xl = k.xl;
   p.xl_stride = k.xl_stride;
-  // rank 32 is two blocks of 16 columns, W8A8's rank 16 one (its XL columns
-  // 16..31 are zero), an adapter two more
-  for (int i = 0; i < (h.rank + 15) / 16; ++i, ++p.nmt) {
+  // XL's 32 columns are two blocks of 16; W8A8 projects one (its rank) and has
+  // zeros in the other; an adapter adds two
+  for (int i = 0; h.rank > 0 && i < (w8a8(h) ? 1 : 2); ++i, ++p.nmt) {
     p.amat[p.nmt] = L->d_l1f + 512 * i;
     p.xl_col[p.nmt] = 16 * i;
   }
-  p.xl_zero = h.rank == 16 ? 16 : 0;
+  p.xl_zero = h.rank > 0 && w8a8(h) ? 16 : 0;
   for (int i = 0; h.lora_r > 0 && i < 2; ++i, ++p.nmt) {
     p.amat[p.nmt] = L->d_lora_l1f + 512 * i;
     p.xl_col[p.nmt] = 32 + 16 * i;
@@ -1019,7 +1028,7 @@ svdq_status svdq_prepare(const svdq_config* cfg, int K, int N, const uint16_t* W
   if (st == SVDQ_OK && L->host.format == SVDQ_NVFP4 && (L->host.g_x_exp < -40 || L->host.g_x_exp > 30))
     st = SVDQ_EUNSUPPORTED;
   if (st == SVDQ_OK && device >= 0) {
-    st = upload_layer(L, device);
+    st = try_upload(L, device);
     if (st != SVDQ_OK) free_device(L);
   }
   if (st != SVDQ_OK) {
@@ -1362,10 +1371,14 @@ svdq_status svdq_deserialize(const void* src, size_t bytes, int device, svdq_lay
   }
   svdq_status st = SVDQ_OK;
   if (device >= 0) {
-    st = upload_layer(L, device);
+    st = try_upload(L, device);
     if (st == SVDQ_OK && h.lora_r > 0) {
       DeviceGuard g(device);
-      st = g.ok ? upload_lora(L) : SVDQ_ECUDA;
+      try {
+        st = g.ok ? upload_lora(L) : SVDQ_ECUDA;
+      } catch (const std::bad_alloc&) {
+        st = SVDQ_ENOMEM;
+      }
     }
     if (st != SVDQ_OK) free_device(L);
   }
