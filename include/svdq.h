@@ -582,7 +582,10 @@ typedef struct {
  * kernels otherwise; SVDQ_NVFP4, SVDQ_INT4, SVDQ_W8A8_INT8).  res is read during
  * the call only.  flags: SVDQ_FWD_GELU, SVDQ_FWD_CHECK, and SVDQ_FWD_NO_BRANCH
  * for svdq_gemm_residual (others: SVDQ_EUNSUPPORTED).  Y must not overlap X.
- * Always the single-CTA GEMM, whatever SVDQ_K2_KERNEL says. */
+ * Never the CTA-pair GEMM, whatever SVDQ_K2_KERNEL says.  With few tokens these
+ * calls (and svdq_norm_linear_forward, svdq_mlp_block_forward) split K over the
+ * CTAs of a cluster and add their FP32 sums in a fixed order: deterministic, but
+ * not bit for bit svdq_gemm's order. */
 svdq_status svdq_gemm_residual(const svdq_layer* layer, const void* codes, const void* scales, const void* xl, int M,
                                const svdq_residual* res, void* Y, void* stream, unsigned flags);
 svdq_status svdq_linear_forward_residual(const svdq_layer* layer, const void* X, int M, const svdq_residual* res,

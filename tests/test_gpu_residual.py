@@ -3,8 +3,9 @@ svdq_linear_forward_residual, svdq_mlp_block_forward), and of a whole
 transformer block run through the operators around the layer.
 
 Bar: within the tolerance every forward is held to, of the BF16 rounding of
-residual + gate * layer(X) in float64; with a gate of one and a residual of
-zero the plain forward's output bit for bit, with a gate of zero the residual.
+residual + gate * layer(X) in float64; with a gate of zero the residual bit for
+bit, and the plain forward's output with a residual of zero where both sum in
+one order.
 """
 import numpy as np
 import pytest
@@ -95,18 +96,67 @@ def test_residual_after_gelu_and_with_adapter(fmt):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("M,K,N", [(100, 64, 256), (640, 1024, 1040), (2000, 512, 2304)])
-def test_residual_of_zero_and_gate_of_zero_are_exact(fmt, M, K, N):
-    """Also more tiles than CTAs (2000 x 2304 is 144 of 128 x 256; every CTA's
-    ring wraps), and a second call on the same buffers."""
+@pytest.mark.parametrize("M,K,N", [(100, 64, 256), (640, 1024, 1040), (2000, 128, 2304)])
+def test_residual_of_zero_and_gate_of_zero(fmt, M, K, N):
+    """A gate of zero gives the residual exactly; a residual of zero the plain
+    forward: bit for bit where K is too short to be split over CTAs, otherwise
+    the plain forward's bound."""
     d = syn.custom_layer(940 + K, M=M, K=K, N=N)
     L = prepare_gpu(d, fmt=fmt, rank=RANK[fmt])
     plain = run_forward(L, d["X"])
-    np.testing.assert_array_equal(_forward(L, d["X"], np.zeros((M, N), np.float32)), plain)
     ones = np.ones((1, N), np.float32)
-    np.testing.assert_array_equal(_forward(L, d["X"], np.zeros((M, N), np.float32), ones), plain)
+    for y in (_forward(L, d["X"], np.zeros((M, N), np.float32)), _forward(L, d["X"], np.zeros((M, N), np.float32), ones)):
+        if K <= 128:
+            np.testing.assert_array_equal(y, plain)
+        else:
+            assert_close_bf16(y, plain, "residual of zero")
     res = _bf(np.random.default_rng(5), M, N)
     np.testing.assert_array_equal(_forward(L, d["X"], res, 0 * ones, in_place=True), res)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,K,N", [
+    (1, 4096, 256),            # one tile, K over eight CTAs
+    (77, 2048, 512), (300, 1088, 144), (513, 1600, 528),   # odd shares of K, ragged tiles
+    (1100, 1024, 1936),        # 72 tiles: pairs
+    (128, 3072, 3072)])
+def test_few_tiles_split_over_k(fmt, M, K, N):
+    d = syn.custom_layer(945 + N, M=M, K=K, N=N)
+    L = prepare_gpu(d, fmt=fmt, rank=RANK[fmt])
+    rng = np.random.default_rng([6, M, N])
+    res, gate = _bf(rng, M, N, a=3.0), _bf(rng, 3, N)
+    rows = -(-M // 3)
+    y = _forward(L, d["X"], res, gate, rows)
+    assert_close_bf16(y, _reference(L, d["X"], res, gate, rows), f"{fmt} split, residual")
+    # the partial sums are added in a fixed order
+    np.testing.assert_array_equal(_forward(L, d["X"], res, gate, rows), y)
+    if fmt != "w8a8":
+        L.set_lora(syn.bf16_bits(_bf(rng, K, 12, a=0.05)), syn.bf16_bits(_bf(rng, 12, N, a=0.3)), 0.5)
+    y = _forward(L, d["X"], res, None, 0, flags=lib.FWD_GELU, in_place=True)
+    assert_close_bf16(y, _reference(L, d["X"], res, None, 0, gelu=True), f"{fmt} split, adapter, GELU, residual")
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,K,N", [(1, 2048, 272), (200, 1088, 528), (1003, 1216, 1040)])
+def test_few_tiles_split_over_k_behind_a_norm(fmt, M, K, N):
+    import torch
+    d = syn.custom_layer(948 + N, M=M, K=K, N=N)
+    L = prepare_gpu(d, fmt=fmt, rank=RANK[fmt])
+    x = torch_bf16(d["X"])
+    y = torch.full((M + 2, N), 9.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(L.workspace_bytes(M), dtype=torch.uint8, device="cuda")
+    yn = torch.empty((M, K), dtype=torch.bfloat16, device="cuda")
+    codes = torch.empty(L.act_code_bytes(M), dtype=torch.uint8, device="cuda")
+    scales = torch.empty(L.act_scale_bytes(M), dtype=torch.uint8, device="cuda")
+    xl = torch.empty((M, 32), dtype=torch.bfloat16, device="cuda")
+    n = lib.Norm(center=True)
+    L.norm_quantize_act(n, x, M, codes, scales, xl, None, yn)
+    for flags, gelu in ((lib.FWD_CHECK, False), (lib.FWD_CHECK | lib.FWD_GELU, True)):
+        L.norm_forward(n, x, M, y, ws, ws.numel(), None, flags)
+        torch.cuda.synchronize()
+        ref = o.forward(oracle_prep_from(L), to_numpy_f32(yn), gelu=gelu)["Y_bf16"]
+        assert_close_bf16(to_numpy_f32(y[:M]), ref, f"{fmt} split behind a norm")
+        assert bool((y[M:] == 9.0).all())
 
 
 @pytest.mark.parametrize("fmt", FORMATS)

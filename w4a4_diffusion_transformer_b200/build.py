@@ -25,7 +25,7 @@ LIB = os.path.join(PKG, "libsvdq.so")
 CUDA_SOURCES = ["api.cu", "k1_quant.cu", "k2_gemm.cu", "k2_pair.cu", "k2_int4.cu", "k2_int4_pair.cu", "upproj.cu", "static_ws.cu", "w4a16.cu", "selftest.cu", "chain.cu", "k2_int8.cu",
                 "norm_nvfp4.cu", "norm_int4.cu", "norm_int8.cu", "rope.cu"]
 CXX_SOURCES = ["prepare.cpp"]
-HEADERS = [os.path.join(CSRC, h) for h in ("sm100.cuh", "kernels.h", "svdq_internal.h", "nvfp4_quant.cuh", "residual.cuh", "norm_quant.cuh")] + [
+HEADERS = [os.path.join(CSRC, h) for h in ("sm100.cuh", "kernels.h", "svdq_internal.h", "nvfp4_quant.cuh", "residual.cuh", "split_k.cuh", "norm_quant.cuh")] + [
     os.path.join(INCLUDE, "svdq.h")]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

@@ -419,8 +419,14 @@ svdq_status run_k1(const svdq_layer* L, const void* X, int M, void* codes, void*
   return launch_k1(tm_x, L->tm_l1t, tm_c, p, fmt, mode, stream) == cudaSuccess ? SVDQ_OK : SVDQ_ECUDA;
 }
 
+// What a GEMM call may ask for beyond the plain layer.
+struct GemmOptions {
+  ResidualParams res = {};      // a residual epilogue
+  int split = 0;                // 1: K may be split over a cluster's CTAs (split_k.cuh): another FP32 order
+};
+
 svdq_status run_k2_int8(const svdq_layer* L, const void* codes, const void* scales, const void* xl, int M, void* Y,
-                        cudaStream_t stream, bool branch, bool gelu, const ResidualParams& res) {
+                        cudaStream_t stream, bool branch, bool gelu, const GemmOptions& opt) {
   const HostPrep& h = L->host;
   CUtensorMap tm_xl, tm_y;
   if (!make_map(&tm_y, Y, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, h.N, M, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
@@ -446,7 +452,8 @@ svdq_status run_k2_int8(const svdq_layer* L, const void* codes, const void* scal
   p.budget_ns = L->budget_ns;
   p.branch = branch ? 1 : 0;
   p.gelu = gelu ? 1 : 0;
-  p.res = res;
+  p.res = opt.res;
+  p.split = opt.split;
   return launch_k2_int8(tm_xl, L->tm_l2s, tm_y, p, L->num_sms, stream) == cudaSuccess ? SVDQ_OK : SVDQ_ECUDA;
 }
 
@@ -482,7 +489,7 @@ svdq_status run_upproj(const svdq_layer* L, const void* xl, int xlw, int width, 
 }
 
 svdq_status run_k2_int4(const svdq_layer* L, const void* codes, const void* scales, const void* xl, int M,
-                        void* Y, cudaStream_t stream, bool branch, bool gelu, bool lora_on, const ResidualParams& res) {
+                        void* Y, cudaStream_t stream, bool branch, bool gelu, bool lora_on, const GemmOptions& opt) {
   const HostPrep& h = L->host;
   const bool lora = h.lora_r > 0 && lora_on;
   CUtensorMap tm_a, tm_xl, tm_y, tm_xla;
@@ -522,10 +529,11 @@ svdq_status run_k2_int4(const svdq_layer* L, const void* codes, const void* scal
   p.branch = branch ? 1 : 0;
   p.gelu = gelu ? 1 : 0;
   p.lora = lora ? 1 : 0;
-  p.res = res;
+  p.res = opt.res;
+  p.split = opt.split;
   // the residual epilogue is the single-CTA kernel's
   const cudaError_t e =
-      L->k2_kernel == 2 && !lora && !res.residual
+      L->k2_kernel == 2 && !lora && !opt.res.residual
           ? launch_k2_int4_pair(tm_a, L->tm_wq_pair, tm_xl, L->tm_l2s_pair, tm_y, p, L->num_sms, stream)
           : launch_k2_int4(tm_a, L->tm_wq, tm_xl, L->tm_l2s, tm_y, tm_xla, lora ? L->tm_lora_l2s : L->tm_l2s, p,
                            L->num_sms, stream);
@@ -536,9 +544,9 @@ svdq_status run_k2_int4(const svdq_layer* L, const void* codes, const void* scal
 // XL_lora (s B) in its own ring stage, the INT4 GEMM by reloading its branch
 // buffer within the tile; either way into the same accumulator.
 svdq_status run_k2(const svdq_layer* L, const void* codes, const void* scales, const void* xl, int M, void* Y,
-                   cudaStream_t stream, bool branch, bool gelu, bool lora_on = true, const ResidualParams& res = {}) {
-  if (L->host.format == SVDQ_INT4) return run_k2_int4(L, codes, scales, xl, M, Y, stream, branch, gelu, lora_on, res);
-  if (w8a8(L->host)) return run_k2_int8(L, codes, scales, xl, M, Y, stream, branch, gelu, res);
+                   cudaStream_t stream, bool branch, bool gelu, bool lora_on = true, const GemmOptions& opt = {}) {
+  if (L->host.format == SVDQ_INT4) return run_k2_int4(L, codes, scales, xl, M, Y, stream, branch, gelu, lora_on, opt);
+  if (w8a8(L->host)) return run_k2_int8(L, codes, scales, xl, M, Y, stream, branch, gelu, opt);
   const HostPrep& h = L->host;
   const bool lora = h.lora_r > 0 && lora_on;
   CUtensorMap tm_xl, tm_y, tm_xla;
@@ -580,8 +588,9 @@ svdq_status run_k2(const svdq_layer* L, const void* codes, const void* scales, c
   // The CTA-pair kernel (256 x 256 tiles) is exact but measured slower than the
   // single-CTA kernel on this part; it runs only when SVDQ_K2_KERNEL=pair, and
   // only for layers without a LoRA adapter and calls without a residual.
-  p.res = res;
-  const bool pair = L->k2_kernel == 2 && !lora && !res.residual;
+  p.res = opt.res;
+  p.split = opt.split;
+  const bool pair = L->k2_kernel == 2 && !lora && !opt.res.residual;
   const cudaError_t e = pair ? launch_k2_pair(tm_xl, L->tm_l2s_pair, tm_y, p, L->num_sms, stream)
                              : launch_k2(tm_xl, L->tm_l2s, tm_y, tm_xla, L->tm_lora_l2s, p, L->num_sms, stream);
   return e == cudaSuccess ? SVDQ_OK : SVDQ_ECUDA;
@@ -943,8 +952,8 @@ svdq_status run_rope(const svdq_rope* r, const svdq_heads* q, const svdq_heads* 
 
 // The second kernel (the adapter, if any, is added inside it).
 svdq_status run_gemm_stage(const svdq_layer* L, const void* codes, const void* scales, const void* xl, int M,
-                           void* Y, cudaStream_t s, bool branch, bool gelu, bool lora_on, const ResidualParams& res = {}) {
-  return run_k2(L, codes, scales, xl, M, Y, s, branch, gelu, lora_on, res);
+                           void* Y, cudaStream_t s, bool branch, bool gelu, bool lora_on, const GemmOptions& opt = {}) {
+  return run_k2(L, codes, scales, xl, M, Y, s, branch, gelu, lora_on, opt);
 }
 
 svdq_status check_residual(const svdq_layer* L, const svdq_residual* r, int M, const void* Y, ResidualParams* out) {
@@ -960,7 +969,7 @@ svdq_status check_residual(const svdq_layer* L, const svdq_residual* r, int M, c
 }
 
 svdq_status gemm_call(const svdq_layer* L, const void* codes, const void* scales, const void* xl, int M, void* Y,
-                      void* stream, unsigned flags, const ResidualParams& res) {
+                      void* stream, unsigned flags, const GemmOptions& opt) {
   if ((reinterpret_cast<uintptr_t>(scales) & 15) || (reinterpret_cast<uintptr_t>(xl) & 15)) return SVDQ_EINVAL;
   svdq_status st = check_forward_args(L, codes, M, Y);
   if (st != SVDQ_OK) return st;
@@ -973,7 +982,7 @@ svdq_status gemm_call(const svdq_layer* L, const void* codes, const void* scales
   DeviceGuard g(L->device);
   if (!g.ok) return SVDQ_ECUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  st = run_gemm_stage(L, codes, scales, xl, M, Y, s, branch, (flags & SVDQ_FWD_GELU) != 0, lora, res);
+  st = run_gemm_stage(L, codes, scales, xl, M, Y, s, branch, (flags & SVDQ_FWD_GELU) != 0, lora, opt);
   if (st == SVDQ_OK && (flags & SVDQ_FWD_CHECK)) st = svdq_check(L, stream);
   return st;
 }
@@ -1562,9 +1571,11 @@ svdq_status svdq_norm_linear_forward(const svdq_layer* L, const svdq_norm* norm,
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   st = run_norm(L, norm, X, M, ws + w.codes, ws + w.scales, ws + w.xl, nullptr, s);
+  GemmOptions opt;
+  opt.split = 1;
   if (st == SVDQ_OK)
     st = run_gemm_stage(L, ws + w.codes, ws + w.scales, ws + w.xl, M, Y, s, L->host.rank > 0,
-                        (flags & SVDQ_FWD_GELU) != 0, L->host.lora_r > 0);
+                        (flags & SVDQ_FWD_GELU) != 0, L->host.lora_r > 0, opt);
   if (st == SVDQ_OK && (flags & SVDQ_FWD_CHECK)) st = svdq_check(L, stream);
   return st;
 }
@@ -1630,18 +1641,20 @@ svdq_status svdq_qkv_forward(const svdq_layer* L, const svdq_norm* norm, const v
 svdq_status svdq_gemm_residual(const svdq_layer* L, const void* codes, const void* scales, const void* xl, int M,
                                const svdq_residual* res, void* Y, void* stream, unsigned flags) {
   if (!L || !Y || M < 1) return SVDQ_EINVAL;
-  ResidualParams epi = {};
-  const svdq_status st = check_residual(L, res, M, Y, &epi);
+  GemmOptions opt;
+  opt.split = 1;
+  const svdq_status st = check_residual(L, res, M, Y, &opt.res);
   if (st != SVDQ_OK) return st;
   if (flags & ~(SVDQ_FWD_GELU | SVDQ_FWD_CHECK | SVDQ_FWD_NO_BRANCH)) return SVDQ_EUNSUPPORTED;
-  return gemm_call(L, codes, scales, xl, M, Y, stream, flags, epi);
+  return gemm_call(L, codes, scales, xl, M, Y, stream, flags, opt);
 }
 
 svdq_status svdq_linear_forward_residual(const svdq_layer* L, const void* X, int M, const svdq_residual* res, void* Y,
                                          void* workspace, size_t workspace_bytes, void* stream, unsigned flags) {
   if (!L || !X || !Y || M < 1) return SVDQ_EINVAL;
-  ResidualParams epi = {};
-  svdq_status st = check_residual(L, res, M, Y, &epi);
+  GemmOptions opt;
+  opt.split = 1;
+  svdq_status st = check_residual(L, res, M, Y, &opt.res);
   if (st != SVDQ_OK) return st;
   if (overlap(X, (size_t)M * L->host.K * 2, Y, (size_t)M * L->host.N * 2)) return SVDQ_EINVAL;
   if (!w4a4(L) || (flags & ~(SVDQ_FWD_GELU | SVDQ_FWD_CHECK))) return SVDQ_EUNSUPPORTED;
@@ -1651,7 +1664,7 @@ svdq_status svdq_linear_forward_residual(const svdq_layer* L, const void* X, int
   if (!workspace || workspace_bytes < w.total || (reinterpret_cast<uintptr_t>(workspace) & 255)) return SVDQ_EINVAL;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   st = svdq_quantize_act(L, X, M, ws + w.codes, ws + w.scales, ws + w.xl, stream, 0);
-  return st == SVDQ_OK ? gemm_call(L, ws + w.codes, ws + w.scales, ws + w.xl, M, Y, stream, flags, epi) : st;
+  return st == SVDQ_OK ? gemm_call(L, ws + w.codes, ws + w.scales, ws + w.xl, M, Y, stream, flags, opt) : st;
 }
 
 svdq_status svdq_mlp_block_forward(const svdq_layer* fc1, const svdq_layer* fc2, const svdq_norm* norm, const void* X,
@@ -1660,13 +1673,14 @@ svdq_status svdq_mlp_block_forward(const svdq_layer* fc1, const svdq_layer* fc2,
   svdq_status st = check_forward_args(fc1, X, M, Y);
   if (st == SVDQ_EINVAL) return st;
   if (!fc2) return SVDQ_EINVAL;
-  ResidualParams epi = {};
+  GemmOptions opt;
+  opt.split = 1;
   if (norm) {
     const svdq_status sn = check_norm(fc1, norm, X, M);
     if (sn != SVDQ_OK) return sn;
   }
   if (res) {
-    const svdq_status sr = check_residual(fc2, res, M, Y, &epi);
+    const svdq_status sr = check_residual(fc2, res, M, Y, &opt.res);
     if (sr != SVDQ_OK) return sr;
   }
   // Y may be X, the norm's residual or its sum: only the first kernel touches
@@ -1684,7 +1698,7 @@ svdq_status svdq_mlp_block_forward(const svdq_layer* fc1, const svdq_layer* fc2,
   st = run_chain_fc1(fc1, fc2, X, M, ws + c.codes2, ws + c.scales2, ws + c.xl2, ws + c.partials, c.S, ws, s,
                      (flags & SVDQ_FWD_GELU) != 0, norm);
   if (st == SVDQ_OK)
-    st = run_k2(fc2, ws + c.codes2, ws + c.scales2, ws + c.xl2, M, Y, s, fc2->host.rank > 0, false, true, epi);
+    st = run_k2(fc2, ws + c.codes2, ws + c.scales2, ws + c.xl2, M, Y, s, fc2->host.rank > 0, false, true, opt);
   if (st == SVDQ_OK && (flags & SVDQ_FWD_CHECK)) {
     st = svdq_check(fc1, stream);
     const svdq_status st2 = svdq_check(fc2, stream);

@@ -51,6 +51,7 @@
 #include "kernels.h"
 #include "residual.cuh"
 #include "sm100.cuh"
+#include "split_k.cuh"
 
 namespace svdq {
 
@@ -101,6 +102,7 @@ constexpr int kSmemBytes =
     kOStages * kOStageBytes + kBrBytes + kPStages * kPStageBytes + kEpiWarps * kEpiWarpBytes + 256 + kGateBytes + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory per block");
 constexpr int kTmemCols = 512;
+constexpr int kSplitGroups = 4;                      // a split leaves each CTA at least so many groups
 
 __device__ __forceinline__ void record_error(int* err, volatile int* abort_flag, int code) {
   atomicCAS(err, 0, code);
@@ -134,10 +136,10 @@ __device__ __forceinline__ void dequant_word(uint32_t w, __half2 s2, uint32_t (&
 // buffer's barriers then complete twice per tile; both sides count the phases.
 constexpr int kLoraLoadG = 2, kLoraMmaG = 5;
 
-//
-// kRes: the epilogue adds the gated output to the residual of tm_r (kResGelu:
-// GELU in front of it; without a residual p.gelu says).
-template <bool kRes, bool kResGelu>
+// kRes: the epilogue adds the gated output to a residual (kResGelu: GELU in
+// front of it; without a residual p.gelu says).  kSplit: the CTAs of a cluster
+// share a tile's groups (split_k.cuh); the branch is rank 0's.
+template <bool kRes, bool kResGelu, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     k2_int4_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                    const __grid_constant__ CUtensorMap tm_xl, const __grid_constant__ CUtensorMap tm_l2,
@@ -169,6 +171,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tiles_n = (N + kBN - 1) / kBN;
   const int num_tiles = tiles_m * tiles_n;
   const int G = K >> 6;
+  const int S = kSplit ? p.splits : 1, rank = kSplit ? (int)dev::cluster_rank() : 0;
+  const int g0 = kSplit ? G * rank / S : 0, g1 = kSplit ? G * (rank + 1) / S : G;   // this CTA's groups
+  const int tile0 = kSplit ? (int)blockIdx.x / S : (int)blockIdx.x;
+  const int tile_step = kSplit ? num_tiles : (int)gridDim.x;
+  const bool branch = p.branch && rank == 0, lora = p.lora && rank == 0;
 
   if (threadIdx.x == 0) {
     // the next kernel on the stream may launch now; it waits for this grid's
@@ -208,21 +215,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       dev::tma_prefetch_desc(&tm_a);
       dev::tma_prefetch_desc(&tm_b);
-      if (p.branch) {
+      if (branch) {
         dev::tma_prefetch_desc(&tm_xl);
         dev::tma_prefetch_desc(&tm_l2);
       }
-      if (p.lora) {
+      if (lora) {
         dev::tma_prefetch_desc(&tm_xla);
         dev::tma_prefetch_desc(&tm_l2a);
       }
-      const int lora_g = min(kLoraLoadG, G - 1);
+      const int lora_g = min(kLoraLoadG, g1 - 1);
       int it = 0, bc = 0;                           // bc: branch-buffer loads so far
       bool ok = true, deps_ready = false;
-      for (int tile = blockIdx.x; tile < num_tiles && ok; tile += gridDim.x) {
+      for (int tile = tile0; tile < num_tiles && ok; tile += tile_step) {
         const int m0 = (tile % tiles_m) * kBM;
         const int n0 = (tile / tiles_m) * kBN;
-        if (p.branch) {
+        if (branch) {
           if (!dev::mbar_wait(bempty, ((uint32_t)bc & 1u) ^ 1u, abort_flag, p.budget_ns)) {
             record_error(p.err, abort_flag, 0x301);
             break;
@@ -236,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           dev::tma_load_2d(brbuf, &tm_xl, bfull, 0, m0);
           ++bc;
         }
-        for (int g = 0; g < G; ++g, ++it) {
+        for (int g = g0; g < g1; ++g, ++it) {
           const int s = it % kPStages;
           if (!dev::mbar_wait(&pempty[s], ((uint32_t)(it / kPStages) & 1u) ^ 1u, abort_flag, p.budget_ns)) {
             record_error(p.err, abort_flag, 0x302);
@@ -254,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           dev::tma_load_2d(st + kPA, &tm_a, &pfull[s], g * 32, m0);
           dev::bulk_load(st + kPSA, p.sa + (size_t)g * p.mpad + m0, kBM * 2, &pfull[s]);
-          if (p.lora && g == lora_g) {
+          if (lora && g == lora_g) {
             // the adapter's tiles, once the tile's branch MMAs have read the buffer
             if (!dev::mbar_wait(bempty, ((uint32_t)bc & 1u) ^ 1u, abort_flag, p.budget_ns)) {
               record_error(p.err, abort_flag, 0x306);
@@ -281,10 +288,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       const uint32_t id16 = idesc_f16(kBM, kBN);
       const uint32_t idbf = dev::idesc_bf16(kBM, kBN);
-      const int lora_g = min(kLoraMmaG, G - 1);
+      const int lora_g = min(kLoraMmaG, g1 - 1);
       int it = 0, tcount = 0, bc = 0;               // bc: branch-buffer phases consumed
       bool ok = true;
-      for (int tile = blockIdx.x; tile < num_tiles && ok; tile += gridDim.x, ++tcount) {
+      for (int tile = tile0; tile < num_tiles && ok; tile += tile_step, ++tcount) {
         const int ab = tcount & 1;
         const uint32_t dacc = tmem + (uint32_t)(ab * 256);
         if (!dev::mbar_wait(&acc_empty[ab], ((uint32_t)(tcount >> 1) & 1u) ^ 1u, abort_flag, p.budget_ns)) {
@@ -293,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         dev::tc_fence_after();
         uint32_t accumulate = 0;
-        if (p.branch) {
+        if (branch) {
           if (!dev::mbar_wait(bfull, (uint32_t)bc & 1u, abort_flag, p.budget_ns)) {
             record_error(p.err, abort_flag, 0x304);
             break;
@@ -310,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           dev::tc_commit(bempty);
         }
-        for (int g = 0; g < G; ++g, ++it) {
+        for (int g = g0; g < g1; ++g, ++it) {
           const int s = it % kOStages;
           if (!dev::mbar_wait(&ofull[s], (uint32_t)(it / kOStages) & 1u, abort_flag, p.budget_ns)) {
             record_error(p.err, abort_flag, 0x305);
@@ -327,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             accumulate = 1;
           }
           dev::tc_commit(&oempty[s]);
-          if (p.lora && g == lora_g) {
+          if (lora && g == lora_g) {
             if (!dev::mbar_wait(bfull, (uint32_t)bc & 1u, abort_flag, p.budget_ns)) {
               record_error(p.err, abort_flag, 0x307);
               ok = false;
@@ -358,8 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float xs = p.xscale;                      // 2^-ex
     int it = 0;
     bool ok = true;
-    for (int tile = blockIdx.x; tile < num_tiles && ok; tile += gridDim.x) {
-      for (int g = 0; g < G; ++g, ++it) {
+    for (int tile = tile0; tile < num_tiles && ok; tile += tile_step) {
+      for (int g = g0; g < g1; ++g, ++it) {
         const int ps = it % kPStages, os = it % kOStages;
         const bool got =
             dev::mbar_wait(&pfull[ps], (uint32_t)(it / kPStages) & 1u, abort_flag, p.budget_ns) &&
@@ -422,6 +429,85 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3;                          // TMEM lane quarter of this warp
     uint8_t* wbuf = epi_buf + (warp - kEpiWarp0) * kEpiWarpBytes;
     if (lane == 0) dev::tma_prefetch_desc(&tm_y);
+    if (kSplit) {
+      const int m0 = (tile0 % tiles_m) * kBM, n0 = (tile0 / tiles_m) * kBN, row0 = m0 + q * 32;
+      const int c0 = rank * 8 / S, c1 = (rank + 1) * 8 / S;   // the chunks this CTA finishes
+      float* dump = reinterpret_cast<float*>(oring);
+      static_assert(dev::kDumpBytes <= kOStages * kOStageBytes, "the dump takes the operand ring's place");
+      const dev::ResidualLoads loads{p.res.residual, wbuf, M, N};
+      dev::Gate<256> gate;
+      if (kRes) {
+        gate.staged = gates + 32 * (warp - kEpiWarp0);
+        dev::griddep_wait();
+        gate.tile(p.res, row0, M, n0, N);
+        for (int i = 0; i < 2; ++i) {
+          if (c0 + i < c1) loads.issue(i, n0 + (c0 + i) * 32, row0);
+          else loads.skip();
+        }
+      }
+      const bool got = dev::mbar_wait(&acc_full[0], 0u, abort_flag, p.budget_ns);
+      const bool done = __all_sync(0xffffffffu, got);
+      if (done) {
+        dev::tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          uint32_t v[32];
+          dev::tmem_load_32cols(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(c * 32), v);
+          dev::tmem_load_wait(v);
+          dev::dump_chunk(dump, c, q * 32 + lane, v);
+        }
+      } else if (lane == 0) {
+        record_error(p.err, abort_flag, 0x309);
+      }
+      __syncwarp();
+      dev::cluster_sync();                           // every CTA's dump is complete
+#pragma unroll 1
+      for (int c = c0; c < c1; ++c) {
+        float sum[32];
+        dev::sum_chunk(dump, S, c, q * 32 + lane, sum);
+        float bias[32];
+#pragma unroll
+        for (int f = 0; f < 8; ++f) {
+          const int col = n0 + c * 32 + 4 * f;
+          const float4 b4 = col < N ? __ldg(reinterpret_cast<const float4*>(p.bias + col))
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+          bias[4 * f] = b4.x;
+          bias[4 * f + 1] = b4.y;
+          bias[4 * f + 2] = b4.z;
+          bias[4 * f + 3] = b4.w;
+        }
+        const auto y = [&](int i, float (&v)[8]) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = p.alpha * sum[i + e] + bias[i + e];
+        };
+        uint8_t* buf = wbuf + ((c - c0) & 1) * kEpiBufBytes;
+        if (kRes) {
+          loads.wait();
+          dev::residual_chunk<kResGelu>(buf, gate, c, n0, N, y);
+        } else {
+          if (lane == 0) dev::bulk_wait_group_read<1>();
+          __syncwarp();
+          dev::plain_chunk(buf, p.gelu != 0, y);
+        }
+        dev::fence_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          dev::tma_store_2d(&tm_y, buf, n0 + c * 32, row0);
+          dev::bulk_commit_group();
+        }
+        if (kRes) {
+          if (c + 2 < c1) {
+            if (lane == 0) dev::bulk_wait_group_read<0>();
+            __syncwarp();
+            loads.issue((c - c0) & 1, n0 + (c + 2) * 32, row0);
+          } else {
+            loads.skip();
+          }
+        }
+      }
+      if (kRes) dev::cp_async_wait_all();
+      if (lane == 0) dev::bulk_wait_group_all();
+    } else {
     int tcount = 0, chunk = 0;
     const dev::ResidualLoads loads{p.res.residual, wbuf, M, N};
     dev::Gate<256> gate;
@@ -532,9 +618,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (kRes) dev::cp_async_wait_all();
     if (lane == 0) dev::bulk_wait_group_all();
+    }
   }
 
   __syncwarp();                                      // single-lane roles rejoin their warps first
+  if (kSplit) {
+    if (warp < kEpiWarp0 || warp >= kConvWarp0) dev::cluster_sync();   // the epilogue's first one
+    dev::cluster_sync();                             // no peer reads this CTA's shared memory any more
+  }
   dev::tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -548,47 +639,60 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 namespace {
 
-template <bool kRes, bool kResGelu>
+template <bool kRes, bool kResGelu, bool kSplit>
 cudaError_t launch_k2_int4_impl(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const CUtensorMap& tm_xl,
                                 const CUtensorMap& tm_l2, const CUtensorMap& tm_y, const CUtensorMap& tm_xla,
-                                const CUtensorMap& tm_l2a, const K2Int4Params& p, int num_sms, cudaStream_t stream) {
+                                const CUtensorMap& tm_l2a, K2Int4Params& p, int num_sms, cudaStream_t stream) {
+  auto kern = k2_int4_kernel<kRes, kResGelu, kSplit>;
   static thread_local int configured_device = -1;
+  static thread_local int active[3] = {};
   int dev = 0;
   cudaGetDevice(&dev);
   if (configured_device != dev) {
-    cudaError_t e = cudaFuncSetAttribute(k2_int4_kernel<kRes, kResGelu>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     // the warpgroups' register budgets fit the launch allocation
     cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, k2_int4_kernel<kRes, kResGelu>);
+    e = cudaFuncGetAttributes(&fa, kern);
     if (e != cudaSuccess) return e;
     if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidConfiguration;
+    if (kSplit && (e = active_clusters(kern, kThreads, kSmemBytes, active)) != cudaSuccess) return e;
     configured_device = dev;
   }
   const int tiles = ((p.M + kBM - 1) / kBM) * ((p.N + kBN - 1) / kBN);
-  const int grid = tiles < num_sms ? tiles : num_sms;
+  p.splits = kSplit ? split_of(tiles, p.K / 64, kSplitGroups, active) : 1;
+  if (kSplit && p.splits == 1)                       // a tile per CTA fills the GPU
+    return launch_k2_int4_impl<kRes, kResGelu, false>(tm_a, tm_b, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, p, num_sms,
+                                                      stream);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = dim3((unsigned)(kSplit ? tiles * p.splits : tiles < num_sms ? tiles : num_sms));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)p.splits;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k2_int4_kernel<kRes, kResGelu>, tm_a, tm_b, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, p);
+  cfg.numAttrs = kSplit ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, tm_a, tm_b, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, p);
 }
 
 }  // namespace
 
 cudaError_t launch_k2_int4(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const CUtensorMap& tm_xl,
                            const CUtensorMap& tm_l2, const CUtensorMap& tm_y, const CUtensorMap& tm_xla,
-                           const CUtensorMap& tm_l2a, const K2Int4Params& p, int num_sms, cudaStream_t stream) {
-  if (!p.res.residual)
-    return launch_k2_int4_impl<false, false>(tm_a, tm_b, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, p, num_sms, stream);
-  return p.gelu ? launch_k2_int4_impl<true, true>(tm_a, tm_b, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, p, num_sms, stream)
-                : launch_k2_int4_impl<true, false>(tm_a, tm_b, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, p, num_sms, stream);
+                           const CUtensorMap& tm_l2a, K2Int4Params p, int num_sms, cudaStream_t stream) {
+  const auto launch = !p.split           ? p.res.residual == nullptr ? launch_k2_int4_impl<false, false, false>
+                                           : p.gelu                  ? launch_k2_int4_impl<true, true, false>
+                                                                     : launch_k2_int4_impl<true, false, false>
+                      : p.res.residual == nullptr ? launch_k2_int4_impl<false, false, true>
+                      : p.gelu                    ? launch_k2_int4_impl<true, true, true>
+                                                  : launch_k2_int4_impl<true, false, true>;
+  return launch(tm_a, tm_b, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, p, num_sms, stream);
 }
 
 }  // namespace svdq

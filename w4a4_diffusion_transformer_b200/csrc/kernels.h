@@ -79,6 +79,8 @@ struct K2Params {
   int lora;                     // 1: one more ring stage per tile adds XL_lora (s B / alpha) (tm_xla, tm_l2a)
   K2Chain chain;                // launch_k2_chain only
   ResidualParams res;
+  int split;                    // 1: K may be split over a cluster's CTAs (split_k.cuh)
+  int splits;                   // CTAs per tile (set by the launcher)
 };
 
 struct K2Int4Params {
@@ -96,6 +98,8 @@ struct K2Int4Params {
   int gelu;                     // 1: tanh-GELU epilogue
   int lora;                     // 1: add XL_lora (s B / alpha) too (tm_xla, tm_l2a), same accumulator
   ResidualParams res;
+  int split;                    // 1: K may be split over a cluster's CTAs (split_k.cuh)
+  int splits;                   // CTAs per tile (set by the launcher)
 };
 
 struct K2Int8Params {
@@ -111,6 +115,8 @@ struct K2Int8Params {
   int branch;                   // 1: add XL L2b (rank 16) from its own accumulator
   int gelu;
   ResidualParams res;
+  int split;                    // 1: K may be split over a cluster's CTAs (split_k.cuh)
+  int splits;                   // CTAs per tile (set by the launcher)
 };
 
 struct UpParams {
@@ -252,7 +258,7 @@ void k2_pair_pack_weights(const uint8_t* tiled_codes, const uint8_t* sf, int N, 
 // codes [N][K/2] (box 32 B x 256 rows), both unswizzled.
 cudaError_t launch_k2_int4(const CUtensorMap& tm_a, const CUtensorMap& tm_b, const CUtensorMap& tm_xl,
                            const CUtensorMap& tm_l2, const CUtensorMap& tm_y, const CUtensorMap& tm_xla,
-                           const CUtensorMap& tm_l2a, const K2Int4Params& p, int num_sms, cudaStream_t stream);
+                           const CUtensorMap& tm_l2a, K2Int4Params p, int num_sms, cudaStream_t stream);
 // The INT4 GEMM on CTA pairs (256 x 256 tiles, clusters of two): tm_b and tm_l2
 // with boxes of k2_int4_pair_rows_b() rows.
 int k2_int4_pair_rows_b();
