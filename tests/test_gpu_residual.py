@@ -119,7 +119,8 @@ def test_residual_of_zero_and_gate_of_zero(fmt, M, K, N):
     (1, 4096, 256),            # one tile, K over eight CTAs
     (77, 2048, 512), (300, 1088, 144), (513, 1600, 528),   # odd shares of K, ragged tiles
     (1100, 1024, 1936),        # 72 tiles: pairs
-    (128, 3072, 3072)])
+    (128, 3072, 3072),
+    (140, 12288, 272)])        # every format over eight
 def test_few_tiles_split_over_k(fmt, M, K, N):
     d = syn.custom_layer(945 + N, M=M, K=K, N=N)
     L = prepare_gpu(d, fmt=fmt, rank=RANK[fmt])
@@ -237,8 +238,8 @@ def _mlp(K, F, seed):
 
 @pytest.mark.parametrize("with_norm,with_res", [(False, False), (True, False), (False, True), (True, True)])
 def test_mlp_block(with_norm, with_res):
-    """Against the parts it is made of, on their own: bit for bit without a
-    residual, within a BF16 rounding of the MLP's output with one."""
+    """Against the parts it is made of, on their own, within a BF16 rounding of
+    the MLP's output."""
     import torch
     M, K, F = 333, 256, 512
     fc1, fc2 = _mlp(K, F, 970)
@@ -270,7 +271,9 @@ def test_mlp_block(with_norm, with_res):
     elif with_norm:
         assert np.linalg.norm(a - b) <= 2e-3 * np.linalg.norm(b)
     else:
-        np.testing.assert_array_equal(a, b)
+        # fc2's FP32 sums may be split over K: both sides round sums that agree to
+        # F 2^-24 of their terms, so each is off by half a step, 2^-8, at most
+        assert np.linalg.norm(a - b) <= 2.0 ** -8 * np.linalg.norm(b)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)

@@ -46,6 +46,7 @@
 #include "nvfp4_quant.cuh"
 #include "residual.cuh"
 #include "sm100.cuh"
+#include "split_k.cuh"
 
 namespace svdq {
 
@@ -108,14 +109,21 @@ constexpr int kSFStageCols = 12 * kKB;       // 4 columns of A + 8 of B per K bl
 constexpr int kModeLayer = 0, kModeChain = 1, kModeResidual = 2, kModeResidualGelu = 3;
 constexpr int kResBytes = kEpiWarps * 256;          // 128 gate values per epilogue warp
 
-template <int kMode>
+// A split leaves each CTA at least so many K stages: a stage takes 0.52 us, a
+// split in two costs 2.5 and each doubling more 2.6 (128 rows, N = 3072: 12
+// stages 11.2 us, in two 10.6, in four 11.5; 48 stages 29.9, 19.8, 16.4, in eight
+// 16.2; four stages 7.8, in two 9.3).
+constexpr int kSplitStages = 6;
+
+template <int kMode, bool kSplit>
 struct K2Layout {
-  static constexpr bool deep = kMode == kModeLayer && SVDQ_K2_DEEP;
+  static constexpr bool deep = kMode == kModeLayer && SVDQ_K2_DEEP && !kSplit;
   static constexpr int stages = deep ? 4 : 3;
   static constexpr int br_bytes = deep ? 0 : kBrBytes;
-  static constexpr int epi_warp_bytes = deep ? 512 : kEpiWarpBytes;   // deep: 128 bias floats only
+  // deep: 128 bias floats only; a split: the chunk buffers only, and 256 gate values
+  static constexpr int epi_warp_bytes = deep ? 512 : kSplit ? 2 * kEpiBufBytes : kEpiWarpBytes;
   static constexpr int smem = stages * kStageBytes + br_bytes + kEpiWarps * epi_warp_bytes + 1024 + 256 +
-                              (kMode >= kModeResidual ? kResBytes : 0);
+                              (kMode < kModeResidual ? 0 : kSplit ? 2 * kResBytes : kResBytes);
   static_assert(smem <= 232448, "shared memory per block");
   static_assert(kSFCol0 + stages * kSFStageCols <= kTmemCols, "TMEM budget");
 };
@@ -154,13 +162,16 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int kMode>
+// kSplit: the CTAs of a cluster share a tile's K stages (split_k.cuh); the
+// branch and the adapter are rank 0's.
+template <int kMode, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     k2_kernel(const __grid_constant__ CUtensorMap tm_xl, const __grid_constant__ CUtensorMap tm_l2,
               const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ CUtensorMap tm_xla,
               const __grid_constant__ CUtensorMap tm_l2a, K2Params p) {
-  using Lay = K2Layout<kMode>;
+  using Lay = K2Layout<kMode, kSplit>;
   constexpr bool kChain = kMode == kModeChain, kRes = kMode >= kModeResidual;
+  static_assert(!(kChain && kSplit), "the chain's CTAs split N");
   constexpr int kStages = Lay::stages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -193,10 +204,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   // BF16 MMAs; their scale-factor slots are moved but not read.  Stage 0: the
   // low-rank branch (deep mode; otherwise it has a buffer of its own); then a
   // LoRA adapter's XL_lora and (s B / alpha)^T.
-  const int lora = kChain ? 0 : p.lora;
+  const int S = kSplit ? p.splits : 1, rank = kSplit ? (int)dev::cluster_rank() : 0;
+  const int kt0 = kSplit ? ktiles * rank / S : 0, kt1 = kSplit ? ktiles * (rank + 1) / S : ktiles;   // this CTA's
+  // read where they are used: without a split they cost no register that way
+  const auto u0 = [&] { return kSplit ? (int)blockIdx.x / S : (int)blockIdx.x; };
+  const auto u_step = [&] { return kSplit ? ts.units() : (int)gridDim.x; };
+  const int lora = kChain || rank != 0 ? 0 : p.lora;
   const int br_stage = (Lay::deep && p.branch) ? 1 : 0;
   const int nextra = br_stage + lora;
-  const bool br_buf = p.branch && !Lay::deep;
+  const bool br_buf = p.branch && !Lay::deep && rank == 0;
 
   if (threadIdx.x == 0) {
     // the next kernel on the stream may launch now; it waits for this grid's
@@ -235,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     dev::setmaxnreg_dec<kRegsCtl>();
     if (lane == 0) {
       const bool pa = warp == kProdA;
-      if (p.branch) dev::tma_prefetch_desc(pa ? &tm_xl : &tm_l2);
+      if (p.branch && rank == 0) dev::tma_prefetch_desc(pa ? &tm_xl : &tm_l2);
       if (lora) dev::tma_prefetch_desc(pa ? &tm_xla : &tm_l2a);
       const CUtensorMap* xmap[2] = {pa ? &tm_xl : &tm_l2, pa ? &tm_xla : &tm_l2a};
       // the activations come from the preceding kernel (launched as a
@@ -243,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (pa) dev::griddep_wait();
       int it = 0, tcount = 0;
       bool ok = true;
-      for (int u = blockIdx.x; u < ts.units() && ok; u += gridDim.x) {
+      for (int u = u0(); u < ts.units() && ok; u += u_step()) {
         for (int t = ts.first(u); t < ts.last(u) && ok; ++t, ++tcount) {
           const int m0 = ts.m0(u);
           const int n0 = ts.n0(u, t);
@@ -281,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (!ok) break;
-          for (int kt = 0; kt < ktiles; ++kt, ++it) {
+          for (int kt = kt0; kt < kt1; ++kt, ++it) {
             const int s = it % kStages;
             if (!dev::mbar_wait(&empty[s], ((uint32_t)(it / kStages) & 1u) ^ 1u, abort_flag, p.budget_ns)) {
               record_error(p.err, abort_flag, 0x202);
@@ -325,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t idesc_h = dev::idesc_bf16(kBM, kBN);
       int it = 0, tcount = 0;
       bool ok = true;
-      for (int u = blockIdx.x; u < ts.units() && ok; u += gridDim.x) {
+      for (int u = u0(); u < ts.units() && ok; u += u_step()) {
         for (int t = ts.first(u); t < ts.last(u) && ok; ++t, ++tcount) {
           if (!dev::mbar_wait(acc_empty, ((uint32_t)tcount & 1u) ^ 1u, abort_flag, p.budget_ns)) {
             record_error(p.err, abort_flag, 0x203);
@@ -373,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             dev::tc_commit(&empty[s]);
           }
           if (!ok) break;
-          for (int kt = 0; kt < ktiles; ++kt, ++it) {
+          for (int kt = kt0; kt < kt1; ++kt, ++it) {
             const int s = it % kStages;
             if (!dev::mbar_wait(&full[s], (uint32_t)(it / kStages) & 1u, abort_flag, p.budget_ns) ||
                 !dev::mbar_wait(&sf_ready[s], (uint32_t)(it / kStages) & 1u, abort_flag, p.budget_ns)) {
@@ -414,9 +430,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanebase = (uint32_t)((warp & 3) * 32) << 16;
     int it = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < ts.units() && ok; u += gridDim.x) {
+    for (int u = u0(); u < ts.units() && ok; u += u_step()) {
       for (int t = ts.first(u); t < ts.last(u) && ok; ++t) {
-        for (int kt = 0; kt < ktiles + nextra; ++kt, ++it) {   // the extra stages' slots are moved too, unread
+        for (int kt = kt0; kt < kt1 + nextra; ++kt, ++it) {   // the extra stages' slots are moved too, unread
           const int st = it % kStages;
           const bool got = dev::mbar_wait(&sf_full[st], (uint32_t)(it / kStages) & 1u, abort_flag, p.budget_ns);
           if (!__all_sync(0xffffffffu, got)) {
@@ -454,7 +470,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     dev::setmaxnreg_inc<kRegsEpi>();
     const int q = warp & 3;                          // TMEM lane quarter of this warp
     const int half = (warp - kEpiWarp0) >> 2;       // which 128 of the 256 columns
-    if (!kChain) {
+    if (kSplit) {
+      // warps 8-11 take the even chunks of this CTA's share, warps 12-15 the odd ones
+      const int m0 = ts.m0(u0()), n0 = ts.n0(u0(), 0), row0 = m0 + q * 32;
+      const int c0 = rank * 8 / S + half, c1 = (rank + 1) * 8 / S;
+      float* dump = reinterpret_cast<float*>(smem);
+      static_assert(dev::kDumpBytes <= kStages * kStageBytes, "the dump takes the operand ring's place");
+      const dev::ResidualLoads loads{p.res.residual, epi_buf + (warp - kEpiWarp0) * Lay::epi_warp_bytes, M, N};
+      dev::Gate<256> gate;
+      if (lane == 0) dev::tma_prefetch_desc(&tm_y);
+      if (kRes) {
+        gate.staged = gates + 32 * (warp - kEpiWarp0);
+        dev::griddep_wait();
+        gate.tile(p.res, row0, M, n0, N);
+        dev::start_chunks(loads, c0, c1, 2, n0, row0);
+      }
+      const bool got = dev::mbar_wait(acc_full, 0u, abort_flag, p.budget_ns);
+      if (__all_sync(0xffffffffu, got)) {
+        dev::tc_fence_after();
+#pragma unroll 1
+        for (int c = half * 4; c < half * 4 + 4; ++c) {
+          uint32_t v[32];
+          dev::tmem_load_32cols(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(c * 32), v);
+          dev::tmem_load_wait(v);
+          dev::dump_chunk(dump, c, q * 32 + lane, v);
+        }
+      } else if (lane == 0) {
+        record_error(p.err, abort_flag, 0x20B);
+      }
+      __syncwarp();
+      dev::cluster_sync();                             // every CTA's dump is complete
+      dev::finish_chunks<kRes, kMode == kModeResidualGelu>(&tm_y, dump, S, c0, c1, 2, loads, gate, n0, row0, p.alpha,
+                                                           p.bias, p.gelu != 0);
+    } else if (!kChain) {
       uint8_t* wbuf = epi_buf + (warp - kEpiWarp0) * Lay::epi_warp_bytes;
       float* bias_s = reinterpret_cast<float*>(Lay::deep ? wbuf : wbuf + 2 * kEpiBufBytes);
       if (!Lay::deep && lane == 0) dev::tma_prefetch_desc(&tm_y);
@@ -782,6 +830,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   __syncwarp();                                      // single-lane roles rejoin their warps first
+  if (kSplit) {
+    if (warp < kEpiWarp0) dev::cluster_sync();       // the epilogue's first one
+    dev::cluster_sync();                             // no peer reads this CTA's shared memory any more
+  }
   dev::tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -825,57 +877,63 @@ void k2_pack_weights(const uint8_t* tiled_codes, const uint8_t* sf, int N, int K
 
 namespace {
 
-template <int kMode>
-cudaError_t configure_k2() {
+template <int kMode, bool kSplit>
+cudaError_t launch_k2_impl(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, const CUtensorMap& tm_y,
+                           const CUtensorMap& tm_xla, const CUtensorMap& tm_l2a, K2Params& p, int units, int num_sms,
+                           cudaStream_t stream) {
+  auto kern = k2_kernel<kMode, kSplit>;
+  constexpr int smem = K2Layout<kMode, kSplit>::smem;
   static thread_local int configured_device = -1;
+  static thread_local int active[9] = {};
   int dev = 0;
   cudaGetDevice(&dev);
-  if (configured_device == dev) return cudaSuccess;
-  cudaError_t e =
-      cudaFuncSetAttribute(k2_kernel<kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, K2Layout<kMode>::smem);
-  if (e != cudaSuccess) return e;
-  // the warpgroups' register budgets add up to exactly 128 per thread
-  cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, k2_kernel<kMode>);
-  if (e != cudaSuccess) return e;
-  if (fa.numRegs != 128) return cudaErrorInvalidConfiguration;
-  configured_device = dev;
-  return cudaSuccess;
-}
-
-template <int kMode>
-cudaError_t launch_k2_impl(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, const CUtensorMap& tm_y,
-                           const CUtensorMap& tm_xla, const CUtensorMap& tm_l2a, const K2Params& p, int grid,
-                           cudaStream_t stream) {
-  cudaError_t e = configure_k2<kMode>();
-  if (e != cudaSuccess) return e;
+  if (configured_device != dev) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    // the warpgroups' register budgets add up to exactly 128 per thread
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kern);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs != 128) return cudaErrorInvalidConfiguration;
+    if (kSplit && (e = active_clusters(kern, kThreads, smem, active)) != cudaSuccess) return e;
+    configured_device = dev;
+  }
+  p.splits = kSplit ? split_of(units, (p.K / 64 + kKB - 1) / kKB, kSplitStages, active) : 1;
+  if (kSplit && p.splits == 1)                       // a tile per CTA fills the GPU
+    return launch_k2_impl<kMode, false>(tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, p, units, num_sms, stream);
   // Programmatic dependent launch: the prologue (barriers, TMEM, descriptor
   // prefetch, weight stream) overlaps the tail of the kernel that produces the
   // activations; the activation producer waits for it before its first load.
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = dim3((unsigned)(kSplit ? units * p.splits : units < num_sms ? units : num_sms));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = K2Layout<kMode>::smem;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)p.splits;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k2_kernel<kMode>, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, p);
+  cfg.numAttrs = kSplit ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, p);
 }
 
 }  // namespace
 
 cudaError_t launch_k2(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, const CUtensorMap& tm_y,
-                      const CUtensorMap& tm_xla, const CUtensorMap& tm_l2a, const K2Params& p, int num_sms,
+                      const CUtensorMap& tm_xla, const CUtensorMap& tm_l2a, K2Params p, int num_sms,
                       cudaStream_t stream) {
   const int tiles = ((p.M + kBM - 1) / kBM) * ((p.N + kBN - 1) / kBN);
-  const int grid = tiles < num_sms ? tiles : num_sms;
-  if (p.res.residual)
-    return p.gelu ? launch_k2_impl<kModeResidualGelu>(tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, p, grid, stream)
-                  : launch_k2_impl<kModeResidual>(tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, p, grid, stream);
-  return launch_k2_impl<kModeLayer>(tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, p, grid, stream);
+  const auto launch = !p.split           ? p.res.residual == nullptr ? launch_k2_impl<kModeLayer, false>
+                                           : p.gelu                  ? launch_k2_impl<kModeResidualGelu, false>
+                                                                     : launch_k2_impl<kModeResidual, false>
+                      : p.res.residual == nullptr ? launch_k2_impl<kModeLayer, true>
+                      : p.gelu                    ? launch_k2_impl<kModeResidualGelu, true>
+                                                  : launch_k2_impl<kModeResidual, true>;
+  return launch(tm_xl, tm_l2, tm_y, tm_xla, tm_l2a, p, tiles, num_sms, stream);
 }
 
 int k2_chain_splits(int M, int N, int num_sms) {
@@ -886,11 +944,11 @@ int k2_chain_splits(int M, int N, int num_sms) {
   return S;
 }
 
-cudaError_t launch_k2_chain(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, const K2Params& p, int num_sms,
+cudaError_t launch_k2_chain(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, K2Params p, int num_sms,
                             cudaStream_t stream) {
   const int units = ((p.M + kBM - 1) / kBM) * p.chain.S;
   // tm_y and the LoRA maps are not used in chain mode: any valid map fills the slots
-  return launch_k2_impl<kModeChain>(tm_xl, tm_l2, tm_l2, tm_l2, tm_l2, p, units < num_sms ? units : num_sms, stream);
+  return launch_k2_impl<kModeChain, false>(tm_xl, tm_l2, tm_l2, tm_l2, tm_l2, p, units, num_sms, stream);
 }
 
 }  // namespace svdq

@@ -43,6 +43,9 @@
 // Within each 8-element chunk the k order in shared memory is (0,4,1,5,2,6,3,7)
 // of the packed codes -- the order in which nibble pairs come out of a 32-bit
 // word with one mask -- for both operands alike, so the sum over k is unchanged.
+// The converters bound it (0.9 us a group), so a GEMM of few tiles is long in K
+// alone; where the caller allows another order of the FP32 sums, its groups are
+// shared out over a cluster (split_k.cuh).
 // Every wait is bounded (sm100.cuh).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -102,7 +105,10 @@ constexpr int kSmemBytes =
     kOStages * kOStageBytes + kBrBytes + kPStages * kPStageBytes + kEpiWarps * kEpiWarpBytes + 256 + kGateBytes + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory per block");
 constexpr int kTmemCols = 512;
-constexpr int kSplitGroups = 4;                      // a split leaves each CTA at least so many groups
+// A split leaves each CTA at least so many groups (128 rows, N = 3072: 48 groups
+// 44.0 us, in two 28.7, in four 19.8, in eight 18.1; 8 groups at N = 512 14.1, in
+// two 12.5).
+constexpr int kSplitGroups = 4;
 
 __device__ __forceinline__ void record_error(int* err, volatile int* abort_flag, int code) {
   atomicCAS(err, 0, code);
@@ -440,10 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         gate.staged = gates + 32 * (warp - kEpiWarp0);
         dev::griddep_wait();
         gate.tile(p.res, row0, M, n0, N);
-        for (int i = 0; i < 2; ++i) {
-          if (c0 + i < c1) loads.issue(i, n0 + (c0 + i) * 32, row0);
-          else loads.skip();
-        }
+        dev::start_chunks(loads, c0, c1, 1, n0, row0);
       }
       const bool got = dev::mbar_wait(&acc_full[0], 0u, abort_flag, p.budget_ns);
       const bool done = __all_sync(0xffffffffu, got);
@@ -461,52 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       dev::cluster_sync();                           // every CTA's dump is complete
-#pragma unroll 1
-      for (int c = c0; c < c1; ++c) {
-        float sum[32];
-        dev::sum_chunk(dump, S, c, q * 32 + lane, sum);
-        float bias[32];
-#pragma unroll
-        for (int f = 0; f < 8; ++f) {
-          const int col = n0 + c * 32 + 4 * f;
-          const float4 b4 = col < N ? __ldg(reinterpret_cast<const float4*>(p.bias + col))
-                                    : make_float4(0.f, 0.f, 0.f, 0.f);
-          bias[4 * f] = b4.x;
-          bias[4 * f + 1] = b4.y;
-          bias[4 * f + 2] = b4.z;
-          bias[4 * f + 3] = b4.w;
-        }
-        const auto y = [&](int i, float (&v)[8]) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = p.alpha * sum[i + e] + bias[i + e];
-        };
-        uint8_t* buf = wbuf + ((c - c0) & 1) * kEpiBufBytes;
-        if (kRes) {
-          loads.wait();
-          dev::residual_chunk<kResGelu>(buf, gate, c, n0, N, y);
-        } else {
-          if (lane == 0) dev::bulk_wait_group_read<1>();
-          __syncwarp();
-          dev::plain_chunk(buf, p.gelu != 0, y);
-        }
-        dev::fence_async_shared();
-        __syncwarp();
-        if (lane == 0) {
-          dev::tma_store_2d(&tm_y, buf, n0 + c * 32, row0);
-          dev::bulk_commit_group();
-        }
-        if (kRes) {
-          if (c + 2 < c1) {
-            if (lane == 0) dev::bulk_wait_group_read<0>();
-            __syncwarp();
-            loads.issue((c - c0) & 1, n0 + (c + 2) * 32, row0);
-          } else {
-            loads.skip();
-          }
-        }
-      }
-      if (kRes) dev::cp_async_wait_all();
-      if (lane == 0) dev::bulk_wait_group_all();
+      dev::finish_chunks<kRes, kResGelu>(&tm_y, dump, S, c0, c1, 1, loads, gate, n0, row0, p.alpha, p.bias, p.gelu != 0);
     } else {
     int tcount = 0, chunk = 0;
     const dev::ResidualLoads loads{p.res.residual, wbuf, M, N};
@@ -645,7 +603,7 @@ cudaError_t launch_k2_int4_impl(const CUtensorMap& tm_a, const CUtensorMap& tm_b
                                 const CUtensorMap& tm_l2a, K2Int4Params& p, int num_sms, cudaStream_t stream) {
   auto kern = k2_int4_kernel<kRes, kResGelu, kSplit>;
   static thread_local int configured_device = -1;
-  static thread_local int active[3] = {};
+  static thread_local int active[9] = {};
   int dev = 0;
   cudaGetDevice(&dev);
   if (configured_device != dev) {

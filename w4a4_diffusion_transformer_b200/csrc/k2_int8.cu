@@ -31,6 +31,7 @@
 #include "kernels.h"
 #include "residual.cuh"
 #include "sm100.cuh"
+#include "split_k.cuh"
 
 namespace svdq {
 
@@ -54,7 +55,11 @@ constexpr int kBrXL = kBM * 64;              // XL rows (32 BF16, the rank in th
 constexpr int kBrBytes = kBrXL + kBN * 64;
 constexpr int kEpiBufBytes = 32 * 64;
 constexpr int kEpiWarpBytes = 2 * kEpiBufBytes + 1024;   // two chunk buffers + 128 bias + 128 s_w floats
-constexpr int kGateBytes = kEpiWarps * 256;              // 128 gate values per epilogue warp
+constexpr int kGateBytes = kEpiWarps * 512;              // 256 gate values per epilogue warp (a split's; else 128)
+// A split leaves each CTA at least so many K stages (128 rows, N = 3072: 24 stages
+// 15.1 us, in two 14.2, in four 13.8; 96 stages 49.8, 33.8, 24.5, in eight 21.9;
+// 16 stages at 1100 x 1936 12.9, in two 13.6).
+constexpr int kSplitStages = 12;
 constexpr int kSmemBytes = kStages * kStageBytes + kBrBytes + kEpiWarps * kEpiWarpBytes + 1024 + 256 + kGateBytes;
 static_assert(kSmemBytes <= 232448, "shared memory per block");
 constexpr int kTmemCols = 512;
@@ -80,8 +85,9 @@ __device__ __forceinline__ void record_error(int* err, volatile int* abort_flag,
 }
 
 // kRes: the epilogue adds the gated output to the residual of tm_r (kResGelu:
-// GELU in front of it; without a residual p.gelu says).
-template <bool kRes, bool kResGelu>
+// GELU in front of it; without a residual p.gelu says).  kSplit: the CTAs of a
+// cluster share a tile's K stages (split_k.cuh); the branch is rank 0's.
+template <bool kRes, bool kResGelu, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     k2_int8_kernel(const __grid_constant__ CUtensorMap tm_xl, const __grid_constant__ CUtensorMap tm_l2,
                    const __grid_constant__ CUtensorMap tm_y, K2Int8Params p) {
@@ -107,6 +113,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tiles_n = (N + kBN - 1) / kBN;
   const int num_tiles = tiles_m * tiles_n;
   const int ktiles = (K + 127) / 128;             // stages of 128 K (K is a multiple of 64)
+  const int S = kSplit ? p.splits : 1, rank = kSplit ? (int)dev::cluster_rank() : 0;
+  const int kt0 = kSplit ? ktiles * rank / S : 0, kt1 = kSplit ? ktiles * (rank + 1) / S : ktiles;   // this CTA's
+  const int tile0 = kSplit ? (int)blockIdx.x / S : (int)blockIdx.x;
+  const int tile_step = kSplit ? num_tiles : (int)gridDim.x;
+  const bool branch = p.branch && rank == 0;
 
   if (threadIdx.x == 0) {
     dev::griddep_launch_dependents();
@@ -137,14 +148,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     dev::setmaxnreg_dec<kRegsCtl>();
     if (lane == 0) {
       const bool pa = warp == kProdA;
-      if (p.branch) dev::tma_prefetch_desc(pa ? &tm_xl : &tm_l2);
+      if (branch) dev::tma_prefetch_desc(pa ? &tm_xl : &tm_l2);
       if (pa) dev::griddep_wait();                  // the codes, scales and XL come from the first kernels
       int it = 0, tcount = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; tile < num_tiles && ok; tile += gridDim.x, ++tcount) {
+      for (int tile = tile0; tile < num_tiles && ok; tile += tile_step, ++tcount) {
         const int m0 = (tile % tiles_m) * kBM;
         const int n0 = (tile / tiles_m) * kBN;
-        if (p.branch) {
+        if (branch) {
           if (!dev::mbar_wait(br_empty, ((uint32_t)tcount & 1u) ^ 1u, abort_flag, p.budget_ns)) {
             record_error(p.err, abort_flag, 0x501);
             ok = false;
@@ -158,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             dev::tma_load_2d(brbuf + kBrXL, &tm_l2, br_full, 0, n0);
           }
         }
-        for (int kt = 0; kt < ktiles; ++kt, ++it) {
+        for (int kt = kt0; kt < kt1; ++kt, ++it) {
           const int s = it % kStages;
           if (!dev::mbar_wait(&empty[s], ((uint32_t)(it / kStages) & 1u) ^ 1u, abort_flag, p.budget_ns)) {
             record_error(p.err, abort_flag, 0x502);
@@ -180,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Do not leave while copies into this CTA's shared memory are in flight.
       for (int j = max(0, it - kStages); j < it; ++j)
         if (!dev::mbar_wait(&full[j % kStages], (uint32_t)(j / kStages) & 1u, abort_flag, p.budget_ns)) break;
-      if (p.branch && tcount > 0) dev::mbar_wait(br_full, (uint32_t)(tcount - 1) & 1u, abort_flag, p.budget_ns);
+      if (branch && tcount > 0) dev::mbar_wait(br_full, (uint32_t)(tcount - 1) & 1u, abort_flag, p.budget_ns);
     }
   } else if (warp == kMmaWarp) {
     // ------------------------------------------------------------ MMA issuer
@@ -190,14 +201,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t idesc_h = dev::idesc_bf16(kBM, kBN);
       int it = 0, tcount = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; tile < num_tiles && ok; tile += gridDim.x, ++tcount) {
+      for (int tile = tile0; tile < num_tiles && ok; tile += tile_step, ++tcount) {
         if (!dev::mbar_wait(acc_empty, ((uint32_t)tcount & 1u) ^ 1u, abort_flag, p.budget_ns)) {
           record_error(p.err, abort_flag, 0x503);
           ok = false;
           break;
         }
         dev::tc_fence_after();
-        if (p.branch) {
+        if (branch) {
           if (!dev::mbar_wait(br_full, (uint32_t)tcount & 1u, abort_flag, p.budget_ns)) {
             record_error(p.err, abort_flag, 0x504);
             ok = false;
@@ -211,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           dev::tc_commit(br_empty);
         }
         uint32_t accumulate = 0;
-        for (int kt = 0; kt < ktiles; ++kt, ++it) {
+        for (int kt = kt0; kt < kt1; ++kt, ++it) {
           const int s = it % kStages;
           if (!dev::mbar_wait(&full[s], (uint32_t)(it / kStages) & 1u, abort_flag, p.budget_ns)) {
             record_error(p.err, abort_flag, 0x505);
@@ -247,6 +258,50 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* bias_s = reinterpret_cast<float*>(wbuf + 2 * kEpiBufBytes);
     float* sw_s = bias_s + 128;
     if (lane == 0) dev::tma_prefetch_desc(&tm_y);
+    if (kSplit) {
+      // warps 8-11 take the even chunks of this CTA's share, warps 12-15 the odd ones
+      const int m0 = (tile0 % tiles_m) * kBM, n0 = (tile0 / tiles_m) * kBN, row0 = m0 + q * 32;
+      const int c0 = rank * 8 / S + half, c1 = (rank + 1) * 8 / S;
+      float* dump = reinterpret_cast<float*>(smem);
+      static_assert(dev::kDumpBytes <= kStages * kStageBytes, "the dump takes the operand ring's place");
+      const dev::ResidualLoads loads{p.res.residual, wbuf, M, N};
+      dev::Gate<256> gate;
+      dev::griddep_wait();
+      const float sx = p.sx[row0 + lane];              // mpad entries
+      if (kRes) {
+        gate.staged = gates + 32 * (warp - kEpiWarp0);
+        gate.tile(p.res, row0, M, n0, N);
+        dev::start_chunks(loads, c0, c1, 2, n0, row0);
+      }
+      const bool got = dev::mbar_wait(acc_full, 0u, abort_flag, p.budget_ns);
+      if (__all_sync(0xffffffffu, got)) {
+        dev::tc_fence_after();
+        const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * 128);
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          // the partial sum s_x s_w acc_i (+ acc_b); a partial acc_i past 2^24 rounds to FP32 here
+          uint32_t v[32], br[32];
+          dev::tmem_load_32cols(taddr + 32 * c, v);
+          dev::tmem_load_wait(v);
+          if (branch) {
+            dev::tmem_load_32cols(taddr + kBranchCol + 32 * c, br);
+            dev::tmem_load_wait(br);
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int col = n0 + half * 128 + c * 32 + i;
+            const float y = __int2float_rn((int)v[i]) * (sx * (col < N ? __ldg(p.sw + col) : 0.f));
+            v[i] = __float_as_uint(branch ? y + __uint_as_float(br[i]) : y);
+          }
+          dev::dump_chunk(dump, half * 4 + c, q * 32 + lane, v);
+        }
+      } else if (lane == 0) {
+        record_error(p.err, abort_flag, 0x508);
+      }
+      __syncwarp();
+      dev::cluster_sync();                             // every CTA's dump is complete
+      dev::finish_chunks<kRes, kResGelu>(&tm_y, dump, S, c0, c1, 2, loads, gate, n0, row0, 1.f, p.bias, p.gelu != 0);
+    } else {
     int tcount = 0, chunk = 0;
     const dev::ResidualLoads loads{p.res.residual, wbuf, M, N};
     dev::Gate<128> gate;
@@ -258,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 2; ++c)
           loads.issue(c, (int)blockIdx.x / tiles_m * kBN + half * 128 + c * 32, (int)blockIdx.x % tiles_m * kBM + q * 32);
     }
-    for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++tcount) {
+    for (int tile = tile0; tile < num_tiles; tile += tile_step, ++tcount) {
       const int m0 = (tile % tiles_m) * kBM;
       const int n0 = (tile / tiles_m) * kBN + half * 128;
       {
@@ -300,14 +355,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < 4; ++c) {
         uint32_t (&cur)[32] = c == 0 ? va : c == 1 ? vb : c == 2 ? vc : vd;
         uint32_t br[32];
-        if (p.branch) {
+        if (branch) {
           dev::tmem_load_32cols(taddr + kBranchCol + 32 * c, br);
           dev::tmem_load_wait(br);
         }
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
           const float y = __int2float_rn((int)cur[i]) * (sx * sw_s[c * 32 + i]);
-          cur[i] = __float_as_uint(p.branch ? y + __uint_as_float(br[i]) : y);
+          cur[i] = __float_as_uint(branch ? y + __uint_as_float(br[i]) : y);
         }
       }
       dev::tc_fence_before();
@@ -373,9 +428,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (kRes) dev::cp_async_wait_all();
     if (lane == 0) dev::bulk_wait_group_all();
+    }
   }
 
   __syncwarp();
+  if (kSplit) {
+    if (warp < kEpiWarp0) dev::cluster_sync();       // the epilogue's first one
+    dev::cluster_sync();                             // no peer reads this CTA's shared memory any more
+  }
   dev::tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -393,42 +453,56 @@ size_t k2_int8_weight_bytes(int N, int K) {
 
 namespace {
 
-template <bool kRes, bool kResGelu>
+template <bool kRes, bool kResGelu, bool kSplit>
 cudaError_t launch_k2_int8_impl(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, const CUtensorMap& tm_y,
-                                const K2Int8Params& p, int num_sms, cudaStream_t stream) {
+                                K2Int8Params& p, int num_sms, cudaStream_t stream) {
+  auto kern = k2_int8_kernel<kRes, kResGelu, kSplit>;
   static thread_local int configured_device = -1;
+  static thread_local int active[9] = {};
   int dev = 0;
   cudaGetDevice(&dev);
   if (configured_device != dev) {
-    cudaError_t e = cudaFuncSetAttribute(k2_int8_kernel<kRes, kResGelu>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, k2_int8_kernel<kRes, kResGelu>);
+    e = cudaFuncGetAttributes(&fa, kern);
     if (e != cudaSuccess) return e;
     if (fa.numRegs != 128) return cudaErrorInvalidConfiguration;
+    if (kSplit && (e = active_clusters(kern, kThreads, kSmemBytes, active)) != cudaSuccess) return e;
     configured_device = dev;
   }
   const int tiles = ((p.M + kBM - 1) / kBM) * ((p.N + kBN - 1) / kBN);
+  p.splits = kSplit ? split_of(tiles, (p.K + 127) / 128, kSplitStages, active) : 1;
+  if (kSplit && p.splits == 1)                       // a tile per CTA fills the GPU
+    return launch_k2_int8_impl<kRes, kResGelu, false>(tm_xl, tm_l2, tm_y, p, num_sms, stream);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tiles < num_sms ? tiles : num_sms);
+  cfg.gridDim = dim3((unsigned)(kSplit ? tiles * p.splits : tiles < num_sms ? tiles : num_sms));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)p.splits;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k2_int8_kernel<kRes, kResGelu>, tm_xl, tm_l2, tm_y, p);
+  cfg.numAttrs = kSplit ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, tm_xl, tm_l2, tm_y, p);
 }
 
 }  // namespace
 
 cudaError_t launch_k2_int8(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, const CUtensorMap& tm_y,
-                           const K2Int8Params& p, int num_sms, cudaStream_t stream) {
-  if (!p.res.residual) return launch_k2_int8_impl<false, false>(tm_xl, tm_l2, tm_y, p, num_sms, stream);
-  return p.gelu ? launch_k2_int8_impl<true, true>(tm_xl, tm_l2, tm_y, p, num_sms, stream)
-                : launch_k2_int8_impl<true, false>(tm_xl, tm_l2, tm_y, p, num_sms, stream);
+                           K2Int8Params p, int num_sms, cudaStream_t stream) {
+  const auto launch = !p.split           ? p.res.residual == nullptr ? launch_k2_int8_impl<false, false, false>
+                                           : p.gelu                  ? launch_k2_int8_impl<true, true, false>
+                                                                     : launch_k2_int8_impl<true, false, false>
+                      : p.res.residual == nullptr ? launch_k2_int8_impl<false, false, true>
+                      : p.gelu                    ? launch_k2_int8_impl<true, true, true>
+                                                  : launch_k2_int8_impl<true, false, true>;
+  return launch(tm_xl, tm_l2, tm_y, p, num_sms, stream);
 }
 
 }  // namespace svdq

@@ -224,13 +224,13 @@ cudaError_t launch_rope(RopeParams& p, int num_sms, cudaStream_t stream);
 // tm_xla / tm_l2a the LoRA tiles (XL_lora [M][32], (s B / alpha)^T [N][32]; the
 // same boxes and swizzle as tm_xl / tm_l2).
 cudaError_t launch_k2(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, const CUtensorMap& tm_y,
-                      const CUtensorMap& tm_xla, const CUtensorMap& tm_l2a, const K2Params& p, int num_sms,
+                      const CUtensorMap& tm_xla, const CUtensorMap& tm_l2a, K2Params p, int num_sms,
                       cudaStream_t stream);
 int k2_block_n();
 // The same GEMM in chain mode (p.chain; Y is not written): CTA c owns 128-row
 // block c / S and the c % S-th of S contiguous ranges of N tiles.
 // k2_chain_splits gives S for an M x N GEMM on num_sms SMs.
-cudaError_t launch_k2_chain(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, const K2Params& p, int num_sms,
+cudaError_t launch_k2_chain(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, K2Params p, int num_sms,
                             cudaStream_t stream);
 int k2_chain_splits(int M, int N, int num_sms);
 // xl[m][j] = bf16(sum_{i < nparts} partials[m][i][j]) in order i = 0, 1, ...
@@ -269,7 +269,7 @@ cudaError_t launch_k2_int4_pair(const CUtensorMap& tm_a, const CUtensorMap& tm_b
 // W8A8 GEMM (tcgen05 kind::i8): tm_xl / tm_l2 the branch tiles (as for the
 // NVFP4 GEMM, L2b unscaled), tm_y the output.
 cudaError_t launch_k2_int8(const CUtensorMap& tm_xl, const CUtensorMap& tm_l2, const CUtensorMap& tm_y,
-                           const K2Int8Params& p, int num_sms, cudaStream_t stream);
+                           K2Int8Params p, int num_sms, cudaStream_t stream);
 size_t k2_int8_weight_bytes(int N, int K);
 
 // Y is read and rewritten through tm_y: a BF16 [M][N] map with boxes of 64
