@@ -28,12 +28,18 @@ namespace {
 // A CTA of 8 warps (16 with a projection) handles tiles of 8 / W (16 / W) rows, W
 // warps to a row; a lane of the row's warp w owns the C chunks of 8 values
 // 32 (C w + c) + lane and keeps them in registers, as FP32, from the load to the
-// codes (unpacking BF16 pairs again for every pass took twice the instructions,
-// and those are what bounds the kernel before memory does).  Consecutive chunks lie a constant apart in every
-// operand and layout, so that their addresses are immediates.  The columns'
-// parameters w (1 + scale), shift and 1/lam sit in shared memory as FP32, filled
-// once per CTA and modulation row; chunk q's eight values are two 16-byte words
-// at q and q + K/8, so that a warp's reads are free of bank conflicts.
+// codes: unpacking BF16 pairs again for every pass took twice the instructions,
+// and those are what bounds the kernel before memory does.  Twelve chunks of the
+// NVFP4 quantizer do not fit that way; kept as BF16 and unpacked per pass they
+// spill less (4608 x 3072 codes and XL: 24.3 against 26.1 us, with a residual
+// 32.2 against 35.0; INT4 38.2 against 38.0, so it keeps FP32).  Consecutive
+// chunks lie a constant apart in every operand and layout, so that their addresses
+// are immediates.  The columns' parameters w (1 + scale), shift and 1/lam sit in
+// shared memory as FP32, filled once per CTA and modulation row; chunk q's eight
+// values are two 16-byte words at q and q + K/8, so that a warp's reads are free
+// of bank conflicts.  (Two rows to a warp, which read the parameters once and
+// share a group's scale arithmetic, need the registers of both: 31.7 us.  Bringing
+// the next tile's rows into L2 meanwhile: 27.6 us.)
 // A lane's chunks: at most 6 (12 with a projection, which wants many rows in a
 // tile, and for rows so long that 6 would leave 8 warps a single row).
 constexpr int kChunks = 6, kChunksMost = 12, kLongK = 6144;
@@ -92,6 +98,7 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
 template <int kFmt, int C, int kWarps, int kMt, bool kFull>
 __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) norm_quant_kernel(const __grid_constant__ NormParams p) {
   constexpr int kThreads = kWarps * 32;
+  constexpr bool kPacked = kFmt == kFmtNvfp4 && C > 6;
   extern __shared__ __align__(16) uint8_t smem[];
   const int K = p.K, M = p.M, nch = K >> 3;             // chunks of 8 values in a row
   const int W = 1 << p.log2_warps, rows = kWarps >> p.log2_warps;
@@ -128,7 +135,22 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) norm_quant_kernel(co
     // a dead row computes on the last one's values and stores zeros
     const size_t at = (size_t)min(row, M - 1) * K + 8 * q0;
     float* slot = slots + ((tile & 1) * 3) * kWarps + rg * W;
-    float2 f[C][4];                                     // h, then h - mu, then y / lam
+    // Only one of the two is used: hp, the BF16 h, or f, its FP32 values -- in turn
+    // h, h - mu and y / lam.
+    uint4 hp[C];
+    float2 f[C][4], nmu = make_float2(0.f, 0.f);        // nmu: -mu
+    const auto centred = [&](int c, float2 (&t)[4]) {   // chunk c of h - mu; zeros past K
+      if (kPacked) {
+        const bool in = kFull || c < nc;
+        t[0] = in ? __fadd2_rn(unpack2(hp[c].x), nmu) : make_float2(0.f, 0.f);
+        t[1] = in ? __fadd2_rn(unpack2(hp[c].y), nmu) : make_float2(0.f, 0.f);
+        t[2] = in ? __fadd2_rn(unpack2(hp[c].z), nmu) : make_float2(0.f, 0.f);
+        t[3] = in ? __fadd2_rn(unpack2(hp[c].w), nmu) : make_float2(0.f, 0.f);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t[i] = f[c][i];
+      }
+    };
     // ---- h = bf16(x + r)
     {
       uint4 v[C];
@@ -155,10 +177,14 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) norm_quant_kernel(co
       }
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        f[c][0] = unpack2(v[c].x);
-        f[c][1] = unpack2(v[c].y);
-        f[c][2] = unpack2(v[c].z);
-        f[c][3] = unpack2(v[c].w);
+        if (kPacked) {
+          hp[c] = v[c];
+        } else {
+          f[c][0] = unpack2(v[c].x);
+          f[c][1] = unpack2(v[c].y);
+          f[c][2] = unpack2(v[c].z);
+          f[c][3] = unpack2(v[c].w);
+        }
       }
     }
     // ---- the tile's modulation rows: one, but where two sequences meet
@@ -172,23 +198,30 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) norm_quant_kernel(co
     if (p.center) {
       float2 a = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int c = 0; c < C; ++c)
+      for (int c = 0; c < C; ++c) {
+        float2 t[4];
+        centred(c, t);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a = __fadd2_rn(a, f[c][i]);
+        for (int i = 0; i < 4; ++i) a = __fadd2_rn(a, t[i]);
+      }
       const float mu = reduce_row<false>(a.x + a.y, slot, W, w, 1 + rg) * invK;
-      const float2 nmu = make_float2(-mu, -mu);
+      nmu = make_float2(-mu, -mu);
+      if (!kPacked)
 #pragma unroll
-      for (int c = 0; c < C; ++c)
-        if (c < nc) {                                   // a chunk past K keeps its zeros
+        for (int c = 0; c < C; ++c)
+          if (c < nc) {                                 // a chunk past K keeps its zeros
 #pragma unroll
-          for (int i = 0; i < 4; ++i) f[c][i] = __fadd2_rn(f[c][i], nmu);
-        }
+            for (int i = 0; i < 4; ++i) f[c][i] = __fadd2_rn(f[c][i], nmu);
+          }
     }
     float2 a2 = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int c = 0; c < C; ++c)
+    for (int c = 0; c < C; ++c) {
+      float2 t[4];
+      centred(c, t);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) a2 = __ffma2_rn(f[c][i], f[c][i], a2);
+      for (int i = 0; i < 4; ++i) a2 = __ffma2_rn(t[i], t[i], a2);
+    }
     const float rstd = rsqrtf(reduce_row<false>(a2.x + a2.y, slot + kWarps, W, w, 1 + rg) * invK + p.eps);
     const float2 rstd2 = make_float2(rstd, rstd);
 
@@ -231,6 +264,9 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) norm_quant_kernel(co
       for (int c = 0; c < C; ++c) {
         const int q = q0 + 32 * c;
         const bool act = c < nc;
+        float2 own[4];
+        if (kPacked) centred(c, own);
+        float2 (&t)[4] = kPacked ? own : f[c];
         if (act) {
           float2 g[4], sh[4], il[4];
           param8(gain, q, nch, g);
@@ -239,22 +275,22 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) norm_quant_kernel(co
           uint32_t y[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            y[i] = pack2(__ffma2_rn(__fmul2_rn(f[c][i], rstd2), g[i], sh[i]));
-            f[c][i] = __fmul2_rn(unpack2(y[i]), il[i]);
+            y[i] = pack2(__ffma2_rn(__fmul2_rn(t[i], rstd2), g[i], sh[i]));
+            t[i] = __fmul2_rn(unpack2(y[i]), il[i]);
           }
           if (kMt > 0) *reinterpret_cast<uint4*>(ytile + rg * ystride + q * 16) = make_uint4(y[0], y[1], y[2], y[3]);
           if (yout) *reinterpret_cast<uint4*>(yout + 256 * c) = make_uint4(y[0], y[1], y[2], y[3]);
         }
-        float a = fmaxf(fabsf(f[c][0].x), fabsf(f[c][0].y));
+        float a = fmaxf(fabsf(t[0].x), fabsf(t[0].y));
 #pragma unroll
-        for (int i = 1; i < 4; ++i) a = dev::fmax3(a, fabsf(f[c][i].x), fabsf(f[c][i].y));
+        for (int i = 1; i < 4; ++i) a = dev::fmax3(a, fabsf(t[i].x), fabsf(t[i].y));
         if (kFmt == kFmtInt8) {
           amax = fmaxf(amax, a);
         } else if (kFmt == kFmtNvfp4) {
           // a group of 16 is two lanes' chunks
           a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
           uint32_t codes = 0u;
-          const uint32_t sb = dev::nvfp4_quant8(f[c], a, p.c_x, p.g_x_exp, rcp, codes) & keep;
+          const uint32_t sb = dev::nvfp4_quant8(t, a, p.c_x, p.g_x_exp, rcp, codes) & keep;
           // four groups' scale bytes are one word of the layout
           uint32_t word = sb << (8 * ((lane >> 1) & 3));
           word |= __shfl_xor_sync(0xffffffffu, word, 2);
@@ -277,7 +313,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) norm_quant_kernel(co
           for (int i = 0; i < 4; ++i) {
             // the sum with 1.5 * 2^23 holds the rounded integer in its low
             // bits; the product is rounded before (no fused multiply-add)
-            const float2 k = __fmul2_rn(f[c][i], i2);
+            const float2 k = __fmul2_rn(t[i], i2);
             codes |= (__float_as_uint(__fadd_rn(k.x, 12582912.0f)) & 0xFu) << (8 * i);
             codes |= (__float_as_uint(__fadd_rn(k.y, 12582912.0f)) & 0xFu) << (8 * i + 4);
           }
