@@ -18,10 +18,9 @@
 // 4 / S tokens of a sequence, S warps to a token.  Its threads first form the
 // tokens' angles together (as every warp's own work, with the frequencies, they
 // cost more than the rotation itself) while each warp's first heads are already
-// on their way.  A lane then
-// owns 8 consecutive values of a head: the products of its weights with its
-// cosines and sines stay in registers for all heads, so that a head costs its
-// norm and two multiply-adds a value.
+// on their way.  A lane then owns 8 consecutive values of a head: the products of
+// its weights with its cosines and sines stay in registers for all heads, so that
+// a head costs its norm and two multiply-adds a value.
 //
 // 4608 tokens, 24 + 24 heads of 128: 21.6 us, 5.25 TB/s of a copy's 6.56 (a warp
 // per token with its own angles: 40.3); 2 x 14040 tokens, 12 + 12 heads: 70.0 us,
