@@ -436,7 +436,8 @@ svdq_status svdq_linear_forward_static(const svdq_layer* layer, const void* X, i
  *                                                    SVDQ_NORM_CENTER, else 0)
  *     y = bf16(n * weight * (1 + scale) + shift)
  *
- * with FP32 sums and products.  All pointers are device memory of the layer's
+ * with FP32 sums and products.  In this section nothing that a call writes may
+ * overlap anything else that it reads or writes, unless it says so.  All pointers are device memory of the layer's
  * device, BF16, 16-byte aligned; NULL leaves that step out.
  *   residual      [M][K] added to X.
  *   sum           [M][K], receives h; may be X or residual themselves, but not
@@ -524,7 +525,8 @@ typedef struct {
  * of strides: value (b, t, h, i) at in + b in_batch + t in_token + h in_head + i,
  * strides in elements, >= 0, multiples of 8, pointers 16-byte aligned.  out may
  * be in with the same strides (in place); otherwise the two must not overlap.
- * No two values of out may share an address.  weight: [head_dim] BF16 or NULL
+ * No two values of out, or of q's and k's, may share an address (heads of one
+ * fused buffer may lie between each other).  weight: [head_dim] BF16 or NULL
  * (ones); not read without SVDQ_ROPE_NORM. */
 typedef struct {
   const void* in;
@@ -543,8 +545,9 @@ typedef struct {
  * Runs on the device that holds q->in, whichever is current; everything else
  * must be on that device too.  Errors:
  * SVDQ_EINVAL (NULL rope, q, positions or a tensor's pointers, sizes below 1, a
- * batch above 65535, strides, alignment, overlap, flags, theta or eps out of range, memory that is
- * not device memory), SVDQ_EUNSUPPORTED (head_dim, dims as above), SVDQ_ECUDA. */
+ * batch above 65535, strides, alignment, overlap, flags, theta or eps out of
+ * range, memory that is not device memory), SVDQ_EUNSUPPORTED (head_dim, dims as
+ * above), SVDQ_ECUDA. */
 svdq_status svdq_rope_heads(const svdq_rope* rope, const svdq_heads* q, const svdq_heads* k, int batch, int T,
                             const float* positions, int64_t pos_batch, void* stream);
 

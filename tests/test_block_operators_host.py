@@ -67,6 +67,7 @@ def test_norm_good_call_wants_a_device(layer):
     dict(scale=E, mod_stride=12, rows_per_mod=2), dict(scale=E, mod_stride=-8, rows_per_mod=2),
     dict(shift=E, mod_stride=256, rows_per_mod=-1),
     dict(sum=A + 16), dict(sum=A - 256), dict(residual=E, sum=E + 32),
+    dict(sum=E, weight=E + 16), dict(sum=E, shift=E - 1024, mod_stride=512, rows_per_mod=2),
     dict(Y=A), dict(Y=A + 1024), dict(residual=E, Y=E), dict(sum=E, Y=E + 2032)])
 def test_norm_refuses(layer, kw):
     assert norm_call(layer, **kw) == lib.EINVAL
@@ -114,7 +115,7 @@ def test_residual_refuses(layer):
     for bad in (dict(res=None), dict(res=D + 8), dict(res=E + 16), dict(res=E - 512), dict(Y=None), dict(Y=E + 2),
                 dict(codes=None), dict(M=0), dict(gate=F + 8), dict(gate=F, gate_stride=4, rows_per_gate=1),
                 dict(gate=F, gate_stride=-8, rows_per_gate=1), dict(gate=F, gate_stride=128, rows_per_gate=-1),
-                dict(scales=B + 2), dict(xl=C + 4)):
+                dict(scales=B + 2), dict(xl=C + 4), dict(gate=E), dict(gate=E - 256, gate_stride=128, rows_per_gate=2)):
         assert call(**bad) == lib.EINVAL, bad
     assert call(flags=lib.FWD_UNFUSED) == lib.EUNSUPPORTED
     assert call(L=_layer(fmt="w4a16")) in (lib.EUNSUPPORTED, lib.ESTATE)
@@ -206,6 +207,12 @@ def test_rope_refuses_heads(q):
 def test_rope_refuses_calls(kw):
     assert rope_call(**kw) == lib.EINVAL
     assert lib.load().svdq_rope_heads(None, ctypes.addressof(heads()), None, 2, 4, C, 0, None) == lib.EINVAL
+
+
+def test_rope_refuses_queries_that_are_keys():
+    for q, k in ((heads(), heads(in_=D)),                               # both write B
+                 (heads(), heads(in_=B, out=D)), (heads(in_=D, out=E), heads(in_=A, out=D))):
+        assert rope_call(q=q, k=k) == lib.EINVAL
 
 
 def test_rope_binding_checks_shapes():

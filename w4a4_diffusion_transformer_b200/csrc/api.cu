@@ -807,6 +807,12 @@ svdq_status check_norm(const svdq_layer* L, const svdq_norm* n, const void* X, i
   const size_t act = (size_t)M * L->host.K * 2;
   if (n->sum != X && overlap(n->sum, act, X, act)) return SVDQ_EINVAL;
   if (n->sum != n->residual && overlap(n->sum, act, n->residual, act)) return SVDQ_EINVAL;
+  // every row's parameters are read while others' sums are written
+  const size_t last = n->rows_per_mod > 0 ? (size_t)((M - 1) / n->rows_per_mod) * (size_t)n->mod_stride : 0;
+  const size_t mod = (last + (size_t)L->host.K) * 2;
+  if (overlap(n->sum, act, n->weight, (size_t)L->host.K * 2) || overlap(n->sum, act, n->scale, mod) ||
+      overlap(n->sum, act, n->shift, mod))
+    return SVDQ_EINVAL;
   if (!w4a4(L) || L->host.K > kNormMaxK) return SVDQ_EUNSUPPORTED;
   return SVDQ_OK;
 }
@@ -961,6 +967,8 @@ svdq_status check_residual(const svdq_layer* L, const svdq_residual* r, int M, c
   if (r->gate && (r->rows_per_gate < 0 || r->gate_stride < 0 || r->gate_stride % 8)) return SVDQ_EINVAL;
   const size_t bytes = (size_t)M * L->host.N * 2;
   if (r->residual != Y && overlap(r->residual, bytes, Y, bytes)) return SVDQ_EINVAL;
+  const size_t last = r->gate && r->rows_per_gate > 0 ? (size_t)((M - 1) / r->rows_per_gate) * (size_t)r->gate_stride : 0;
+  if (overlap(r->gate, (last + (size_t)L->host.N) * 2, Y, bytes)) return SVDQ_EINVAL;
   out->residual = static_cast<const __nv_bfloat16*>(r->residual);
   out->gate = static_cast<const __nv_bfloat16*>(r->gate);
   out->gate_stride = r->gate_stride;
@@ -1589,6 +1597,8 @@ svdq_status svdq_rope_heads(const svdq_rope* rope, const svdq_heads* q, const sv
   if (st == SVDQ_OK) st = check_heads(rope, q, batch, T);
   if (st == SVDQ_OK && k) st = check_heads(rope, k, batch, T);
   if (st != SVDQ_OK) return st;
+  // (spans of heads of one fused buffer meet without sharing a value)
+  if (k && (q->out == k->out || q->out == k->in || k->out == q->in)) return SVDQ_EINVAL;
   cudaPointerAttributes at = {};
   if (cudaPointerGetAttributes(&at, q->in) != cudaSuccess) return SVDQ_ECUDA;
   if (at.type != cudaMemoryTypeDevice && at.type != cudaMemoryTypeManaged) return SVDQ_EINVAL;
