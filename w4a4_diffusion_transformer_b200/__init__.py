@@ -529,9 +529,10 @@ class Layer:
 
     def _act_bytes(self, M: int):
         # (code, scale) bytes for M tokens, which a caller tends to ask for again and again
-        if self._act_last[0] != M:
-            self._act_last = (M, self.act_code_bytes(M), self.act_scale_bytes(M))
-        return self._act_last[1:]
+        last = self._act_last              # one read: another thread may replace it
+        if last[0] != M:
+            self._act_last = last = (M, self.act_code_bytes(M), self.act_scale_bytes(M))
+        return last[1:]
 
     def act_codes_to_logical(self, device_layout: np.ndarray, M: int) -> np.ndarray:
         """Activation codes in the GEMM's layout -> uint8 [M][K/2] (two codes per
