@@ -46,9 +46,9 @@ namespace {
 // of bank conflicts.  (Two rows to a warp, which read the parameters once and
 // share a group's scale arithmetic, need the registers of both: 31.7 us.  Bringing
 // the next tile's rows into L2 meanwhile: 27.6 us.)
-// A lane's chunks: at most 6 (12 with a projection, which wants many rows in a
-// tile, and for rows so long that 6 would leave 8 warps a single row).
-constexpr int kChunks = 6, kChunksMost = 12, kLongK = 6144;
+// A lane's chunks: at most 6 (12 with a projection, which wants many rows in a tile).
+constexpr int kChunks = 6, kChunksMost = 12;
+constexpr size_t kSmSmem = 228 * 1024;                  // shared memory of an SM
 
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
@@ -448,10 +448,10 @@ cudaError_t launch_t(NormParams& p, int num_sms, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     configured_device = dev;
   }
-  // persistent: as many CTAs as an SM holds (228 KB, 1 KB of it per CTA its
+  // persistent: as many CTAs as an SM holds (1 KB of shared memory per CTA its
   // own), each a contiguous range of tiles
   const int rows = kWarps >> p.log2_warps, tiles = p.mpad / rows;
-  const int fit = (int)(233472 / (smem + 1024)), per_sm = fit < 16 / kWarps ? fit : 16 / kWarps;
+  const int fit = (int)(kSmSmem / (smem + 1024)), per_sm = fit < 16 / kWarps ? fit : 16 / kWarps;
   const int grid = tiles < per_sm * num_sms ? tiles : per_sm * num_sms;
   p.tiles_each = tiles / grid;
   p.tiles_extra = tiles % grid;
@@ -482,11 +482,21 @@ int lane_chunks(int K, int l) { return (K / 8 + (32 << l) - 1) / (32 << l); }
 
 // Without a projection: 8 warps, two CTAs per SM.  More registers a thread and
 // all of a row's loads in flight beat more warps (4608 x 3072 W8A8: 23.1 us at 16
-// warps of 128 registers, 25.0 at 24 of 80).
+// warps of 128 registers, 25.0 at 24 of 80).  Rows of more than 8192 columns, which
+// 8 warps could take only one at a time (and whose parameters soon leave no room
+// for a second CTA), get one CTA of 16 warps: 4608 x 9216 W8A8 78.3 instead of 88.4
+// us, x 12288 86.6 instead of 122; x 8192 67.8 instead of 66.6.
 template <int kFmt>
 cudaError_t launch_plain(NormParams& p, int num_sms, cudaStream_t stream) {
   int l = 0;
-  while (l < 3 && lane_chunks(p.K, l) > (p.K > kLongK ? kChunksMost : kChunks)) ++l;
+  if (lane_chunks(p.K, 3) > 4) {
+    while (l < 4 && lane_chunks(p.K, l) > kChunks) ++l;
+    while (l < 4 && (p.M + (16 >> l) - 1) / (16 >> l) < num_sms) ++l;
+    p.log2_warps = l;
+    return lane_chunks(p.K, l) <= 4 ? launch<kFmt, 4, 16, 0>(p, num_sms, stream)
+                                    : launch<kFmt, 6, 16, 0>(p, num_sms, stream);
+  }
+  while (l < 3 && lane_chunks(p.K, l) > kChunks) ++l;
   // with few rows, more warps to a row
   while (l < 3 && (p.M + (8 >> l) - 1) / (8 >> l) < num_sms) ++l;
   p.log2_warps = l;
@@ -495,8 +505,7 @@ cudaError_t launch_plain(NormParams& p, int num_sms, cudaStream_t stream) {
   if (chunks <= 2) return launch<kFmt, 2, 8, 0>(p, num_sms, stream);
   if (chunks <= 3) return launch<kFmt, 3, 8, 0>(p, num_sms, stream);
   if (chunks <= 4) return launch<kFmt, 4, 8, 0>(p, num_sms, stream);
-  if (chunks <= 6) return launch<kFmt, 6, 8, 0>(p, num_sms, stream);
-  return launch<kFmt, 12, 8, 0>(p, num_sms, stream);
+  return launch<kFmt, 6, 8, 0>(p, num_sms, stream);
 }
 
 // With a projection: 16 warps, one CTA per SM, tiles of up to 16 rows; 8 warps
