@@ -161,6 +161,38 @@ def test_few_tiles_split_over_k_behind_a_norm(fmt, M, K, N):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
+def test_split_captured_and_on_two_streams_at_once(fmt):
+    """The same bytes from a replayed graph and from two streams whose clusters
+    share the GPU."""
+    import torch
+    M, K, N = 100, 4096, 272
+    d = syn.custom_layer(953, M=M, K=K, N=N)
+    L = prepare_gpu(d, fmt=fmt, rank=RANK[fmt])
+    x, res = torch_bf16(d["X"]), torch_bf16(_bf(np.random.default_rng(12), M, N))
+    ws = [torch.empty(L.workspace_bytes(M), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    epi, norm = lib.Residual(res), lib.Norm(center=True)
+    y, yn = torch.empty_like(res), torch.empty_like(res)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s = torch.cuda.current_stream()
+        L.forward_residual(x, M, epi, y, ws[0], ws[0].numel(), s)
+        L.norm_forward(norm, x, M, yn, ws[0], ws[0].numel(), s)
+    graph.replay()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    out = [torch.empty_like(res) for _ in range(2)]
+    for _ in range(10):
+        for i in range(2):
+            L.forward_residual(x, M, epi, out[i], ws[i], ws[i].numel(), streams[i])
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], y) and torch.equal(out[1], y)
+    L.norm_forward(norm, x, M, out[0], ws[0], ws[0].numel(), flags=lib.FWD_CHECK)
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], yn)
+    assert_close_bf16(to_numpy_f32(y), _reference(L, d["X"], to_numpy_f32(res), None, 0), f"{fmt} captured split")
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_residual_over_several_waves(fmt):
     """More than two tiles per CTA: 4736 x 2560 is 370."""
     import torch
