@@ -292,3 +292,108 @@ def test_binding_checks_modulation_rows(layer):
     with pytest.raises(ValueError, match="rows"):
         layer.gemm_residual(A, B, C, 9, r, E)
     assert status(lambda: layer.gemm_residual(A, B, C, 8, r, E)) == lib.ESTATE
+
+
+def _other_storage(t, ptr, **kw):
+    """The same tensor object with another storage, as tensor.data = ... leaves it."""
+    for k, v in dict(data_ptr=lambda: ptr, **kw).items():
+        setattr(t, k, v)
+
+
+def test_binding_follows_operands_to_another_storage(layer):
+    """Addresses and placement are those at the call, not those when the object was made."""
+    made = {"residual": FakeRows((4, 256), (256, 1)), "sum": FakeRows((4, 256), (256, 1)),
+            "weight": FakeRows((256,), (1,)), "scale": FakeRows((2, 256), (1536, 1)),
+            "shift": FakeRows((2, 256), (1536, 1))}
+    for i, t in enumerate(made.values()):
+        t.data_ptr = lambda i=i: (10 + i) * A
+    n = lib.Norm(rows_per_mod=2, **made)
+    assert status(lambda: layer.norm_quantize_act(n, A, 4, B, C, E)) == lib.ESTATE
+    for i, (name, t) in enumerate(made.items()):
+        assert getattr(n._c, name) == (10 + i) * A
+        _other_storage(t, (20 + i) * A)
+        assert status(lambda: layer.norm_quantize_act(n, A, 4, B, C, E)) == lib.ESTATE
+        assert getattr(n._c, name) == (20 + i) * A
+    for t in (made["scale"], made["shift"]):
+        _other_storage(t, 30 * A, _s=(512, 1))          # rows another distance apart
+    assert status(lambda: layer.norm_quantize_act(n, A, 4, B, C, E)) == lib.ESTATE
+    assert n._c.mod_stride == 512
+    for name, t in made.items():                        # moved to the host, and back
+        _other_storage(t, 40 * A, is_cuda=False)
+        for call in (lambda: layer.norm_quantize_act(n, A, 4, B, C, E),
+                     lambda: layer.norm_forward(n, A, 4, E, F, layer.workspace_bytes(4)),
+                     lambda: lib.mlp_block_forward(layer, layer, n, A, 4, None, E, F, 0)):
+            with pytest.raises(ValueError, match=name):
+                call()
+        _other_storage(t, (50 + list(made).index(name)) * A, is_cuda=True)
+    assert status(lambda: layer.norm_quantize_act(n, A, 4, B, C, E)) == lib.ESTATE
+    _other_storage(made["weight"], 60 * A, shape=(128,))
+    with pytest.raises(ValueError, match="weight"):
+        layer.norm_quantize_act(n, A, 4, B, C, E)
+
+
+def test_binding_follows_a_residual_and_a_gate(layer):
+    res, gate = FakeRows((4, 128), (128, 1)), FakeRows((2, 128), (768, 1))
+    res.data_ptr, gate.data_ptr = (lambda: 10 * A), (lambda: 11 * A)
+    r = lib.Residual(res, gate, rows_per_gate=2)
+    assert status(lambda: layer.gemm_residual(A, B, C, 4, r, E)) == lib.ESTATE
+    _other_storage(res, 20 * A)
+    _other_storage(gate, 21 * A, _s=(256, 1))
+    assert status(lambda: layer.gemm_residual(A, B, C, 4, r, E)) == lib.ESTATE
+    assert (r._c.residual, r._c.gate, r._c.gate_stride) == (20 * A, 21 * A, 256)
+    _other_storage(res, E)                              # in place now
+    assert status(lambda: layer.gemm_residual(A, B, C, 4, r, E)) == lib.ESTATE
+    _other_storage(res, E + 64)                         # ... and over a part of Y
+    assert status(lambda: layer.gemm_residual(A, B, C, 4, r, E)) == lib.EINVAL
+    _other_storage(res, 22 * A)
+    for t, name in ((gate, "gate"), (res, "residual")):
+        _other_storage(t, 30 * A, is_cuda=False)
+        for call in (lambda: layer.gemm_residual(A, B, C, 4, r, E),
+                     lambda: layer.forward_residual(A, 4, r, E, F, layer.workspace_bytes(4)),
+                     lambda: lib.mlp_block_forward(layer, layer, None, A, 4, r, E, F, 0)):
+            with pytest.raises(ValueError, match=name):
+                call()
+        _other_storage(t, 31 * A, is_cuda=True)
+
+
+def test_binding_follows_heads():
+    def heads_of(ptr):
+        t = FakeRows((2, 4, 2, 64), (512, 128, 64, 1))
+        t.data_ptr, t.get_device = (lambda: ptr), (lambda: 0)
+        return t
+    x, out, w = heads_of(10 * A), heads_of(11 * A), FakeRows((64,), (1,))
+    w.get_device = lambda: 0
+    q = lib.Heads(x, out, w)
+    rope, calls = lib.Rope(64, (16, 24, 20), half=True), []    # refused after the heads are taken
+
+    def call():
+        calls.append(status(lambda: lib.rope_heads(rope, q, None, C)))
+        return q._c
+    c = call()
+    assert (c.in_, c.out, c.weight, c.out_token) == (10 * A, 11 * A, D, 128)
+    _other_storage(x, 20 * A)
+    _other_storage(out, 21 * A, _s=(1024, 256, 64, 1))
+    _other_storage(w, 22 * A)
+    c = call()
+    assert (c.in_, c.out, c.weight, c.out_token) == (20 * A, 21 * A, 22 * A, 256)
+    assert calls == [lib.EUNSUPPORTED] * 2
+    for t, name in ((x, "x"), (out, "out"), (w, "weight")):
+        _other_storage(t, 30 * A, is_cuda=False)
+        with pytest.raises(ValueError, match=name):
+            call()
+        _other_storage(t, 31 * A, is_cuda=True)
+
+
+def test_binding_refuses_a_released_storage():
+    import torch
+
+    class Released(FakeRows):
+        def storage_offset(self):
+            return 0
+
+        def untyped_storage(self):
+            return torch.zeros(0, dtype=torch.bfloat16).untyped_storage()
+    with pytest.raises(ValueError, match="released"):
+        lib.Norm(weight=Released((256,), (1,)))
+    with pytest.raises(ValueError, match="released"):
+        lib.Residual(D, gate=Released((2, 256), (256, 1)))

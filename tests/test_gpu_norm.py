@@ -288,3 +288,51 @@ def test_norm_captured_replayed_and_on_another_stream():
     L.norm_forward(n, x, M, y, ws, ws.numel(), torch.cuda.current_stream())
     torch.cuda.synchronize()
     assert torch.equal(y, replayed) and not torch.equal(y, first)
+
+
+def test_operands_that_get_another_storage_are_followed():
+    """A module's parameters keep their objects and change their storage when it is
+    moved; a call reads what they hold then, and refuses host memory."""
+    import torch
+    L = prepare_gpu(syn.custom_layer(851, M=8, K=256, N=64), fmt="nvfp4", rank=32)
+    M, d, d2 = 50, _inputs(10, 50, 256, mods=2), _inputs(11, 50, 256, mods=2)
+    x, s = torch_bf16(d["X"]), torch.empty((M, 256), dtype=torch.bfloat16, device="cuda")
+    made = {k: torch.nn.Parameter(torch_bf16(v), requires_grad=False)
+            for k, v in (("residual", d["res"]), ("weight", d["weight"]), ("scale", d["mod"][:, 256:512]),
+                         ("shift", d["mod"][:, :256]))}
+    n = lib.Norm(sum=s, rows_per_mod=d["rows"], eps=EPS, **made)
+    res = torch.nn.Parameter(torch.zeros((M, 64), dtype=torch.bfloat16, device="cuda"), requires_grad=False)
+    epi = lib.Residual(res)
+    codes = torch.empty(L.act_code_bytes(M), dtype=torch.uint8, device="cuda")
+    scales = torch.empty(L.act_scale_bytes(M), dtype=torch.uint8, device="cuda")
+    xl = torch.empty((M, 32), dtype=torch.bfloat16, device="cuda")
+    y, out = torch.empty_like(s), torch.empty_like(res)
+
+    def call():
+        L.norm_quantize_act(n, x, M, codes, scales, xl, Y=y)
+        L.gemm_residual(codes, scales, xl, M, epi, out)
+        torch.cuda.synchronize()
+        return to_numpy_f32(s), to_numpy_f32(y), to_numpy_f32(out)
+    h, got, base = call()
+    check(L, d, {"h": h, "y": got})
+    for k, v in (("residual", d2["res"]), ("weight", d2["weight"]), ("scale", d2["mod"][:, 256:512]),
+                 ("shift", d2["mod"][:, :256])):
+        made[k].data = torch_bf16(v)
+    s.zero_()
+    h, got, base = call()
+    check(L, dict(d2, X=d["X"]), {"h": h, "y": got})
+    big = np.full((M, 64), 1024.0, np.float32)
+    res.data = torch_bf16(big)
+    moved = call()[2]
+    # 1024 + y, rounded once: a step of 8 there
+    assert np.all(np.abs(moved - 1024.0 - base) <= 4.0 + 2.0 ** -8 * np.abs(base))
+    for p, name, f in ((made["weight"], "weight", call), (res, "residual", call)):
+        keep = p.data
+        p.data = p.data.cpu()
+        with pytest.raises(ValueError, match=name):
+            f()
+        p.data = keep
+    np.testing.assert_array_equal(call()[2], moved)
+    made["weight"].untyped_storage().resize_(0)
+    with pytest.raises(ValueError, match="released"):
+        call()

@@ -235,3 +235,27 @@ def test_qkv_forward(fmt, rank, with_norm):
         ref, tol = reference(b[:, :, sl], pos, (16, 24, 24), norm=True, w=wt)
         assert_within(got[:, :, sl], ref, tol)
     np.testing.assert_array_equal(got[:, :, H + HK:], b[:, :, H + HK:])
+
+
+def test_heads_that_get_another_storage_are_followed():
+    import torch
+    rng = np.random.default_rng(11)
+    a, b = _rand(rng, 1, 30, 4, 64), _rand(rng, 1, 30, 4, 64)
+    w = torch.nn.Parameter(torch_bf16(np.ones(64, np.float32)), requires_grad=False)
+    x, out = torch_bf16(a), torch.empty((1, 30, 4, 64), dtype=torch.bfloat16, device="cuda")
+    pos = _pos(rng, 1, 30, 1)
+    rope, h = lib.Rope(64, (64,), norm=True, eps=EPS), lib.Heads(x, out, w)
+
+    def call():
+        lib.rope_heads(rope, h, None, torch.from_numpy(pos).cuda())
+        torch.cuda.synchronize()
+        return to_numpy_f32(out)
+    assert_within(call(), *reference(a, pos, (64,), norm=True))
+    x.data, w2 = torch_bf16(b), _rand(rng, 64, a=0.2, b=1.0)
+    w.data = torch_bf16(w2)
+    assert_within(call(), *reference(b, pos, (64,), norm=True, w=w2))
+    out.data = torch.zeros_like(out)
+    assert_within(call(), *reference(b, pos, (64,), norm=True, w=w2))
+    w.data = w.data.cpu()
+    with pytest.raises(ValueError, match="weight"):
+        call()

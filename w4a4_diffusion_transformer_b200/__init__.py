@@ -237,6 +237,36 @@ def _bf16_tensor(x, what: str):
         raise ValueError(f"{what}: must be a CUDA tensor")
     if x.element_size() != 2 or not x.dtype.is_floating_point or str(x.dtype) != "torch.bfloat16":
         raise ValueError(f"{what}: must be BF16, got {x.dtype}")
+    if hasattr(x, "untyped_storage") and x.numel() > 0:
+        end = x.storage_offset() + sum((n - 1) * s for n, s in zip(x.shape, x.stride())) + 1
+        if x.untyped_storage().nbytes() < 2 * end:
+            raise ValueError(f"{what}: its storage has been released")
+
+
+class _Described:
+    """Operands that the library gets as one struct (_c).  The checks of placement
+    and layout run when the struct is filled; a tensor can get another storage
+    later (tensor.data = ..., a module moved between devices), so every call
+    compares the places first and fills the struct again where one changed."""
+
+    def _hold(self, *operands):
+        self._keep = operands
+        self._tensors = [x for x in operands if _is_tensor(x)]
+        self._others = [x for x in operands if hasattr(x, "data_ptr") and not _is_tensor(x)]
+        self._seen = None
+        self._now()
+
+    def _now(self):
+        """The struct as a call's argument, with the operands as they are now."""
+        seen = [(x.data_ptr(), x.shape, x.stride(), x.dtype) for x in self._tensors]
+        if self._others:
+            seen += [x.data_ptr() for x in self._others]
+        if seen != self._seen:
+            self._describe()
+            self._seen = seen
+        return ctypes.byref(self._c)
+
+    _ref = property(_now)
 
 
 class _Rows:
@@ -269,7 +299,7 @@ class _Rows:
             raise ValueError(f"{self.what}: {self.rows} rows, the call reads {need}")
 
 
-class Norm:
+class Norm(_Described):
     """A normalisation in front of a layer (svdq_norm): optional residual
     addition (``sum`` receives it), RMS norm -- or layer norm with ``center`` --
     times ``weight`` and modulated by rows of ``scale`` and ``shift``, of which
@@ -278,7 +308,12 @@ class Norm:
 
     def __init__(self, residual=None, sum=None, weight=None, scale=None, shift=None, rows_per_mod: int = 0,
                  mod_stride: Optional[int] = None, eps: float = 1e-6, center: bool = False):
-        # placement and layout are checked once, here; the sizes at each call
+        self._mod_stride, self._per, self._eps, self._center = mod_stride, int(rows_per_mod), float(eps), bool(center)
+        self._hold(residual, sum, weight, scale, shift)
+
+    def _describe(self):
+        residual, sum, weight, scale, shift = self._keep
+        mod_stride = self._mod_stride
         self._held = []
         for t, what in ((residual, "residual"), (sum, "sum"), (weight, "weight")):
             if _is_tensor(t):
@@ -291,42 +326,52 @@ class Norm:
         if len(strides) > 1:
             raise ValueError("scale and shift: their rows must be the same distance apart")
         stride = strides.pop() if strides else 0
-        self._keep = (residual, sum, weight, scale, shift)
-        self._rows, self._per = rows, int(rows_per_mod)
+        self._rows = rows
         self._c = NormStruct(_ptr(residual), _ptr(sum), _ptr(weight), _ptr(scale), _ptr(shift), int(stride or 0),
-                             int(rows_per_mod), float(eps), NORM_CENTER if center else 0)
-        self._ref = ctypes.addressof(self._c)
+                             self._per, self._eps, NORM_CENTER if self._center else 0)
 
-    def _need(self, M: int, K: int):
+    def _args(self, M: int, K: int):
+        """The struct for a call over M tokens, sizes checked."""
+        now = self._now()
+        if M <= 0:
+            return now                 # the library answers M <= 0 itself
         for held, one_row, what in self._held:
             need = K * 2 if one_row else M * K * 2
             if held < need:
                 raise ValueError(f"{what}: holds {held} bytes, the call accesses {need}")
         for r in self._rows:
             r.need(M, K, self._per)
+        return now
 
 
-class Residual:
+class Residual(_Described):
     """A residual in a GEMM's epilogue (svdq_residual): Y = residual + gate * y,
     token m gated by row m // rows_per_gate (0: row 0; no gate: 1).  Holds
     references to its tensors; one object can be used for any number of calls."""
 
     def __init__(self, residual, gate=None, rows_per_gate: int = 0, gate_stride: Optional[int] = None):
+        self._gate_stride, self._per = gate_stride, int(rows_per_gate)
+        self._hold(residual, gate)
+
+    def _describe(self):
+        residual, gate = self._keep
         if _is_tensor(residual):
             _bf16_tensor(residual, "residual")
         self._held = _held_bytes(residual, "residual", True)
-        self._keep = (residual, gate)
-        self._rows = None if gate is None else _Rows(gate, "gate", gate_stride)
-        self._per = int(rows_per_gate)
+        self._rows = None if gate is None else _Rows(gate, "gate", self._gate_stride)
         stride = 0 if self._rows is None or self._rows.rows == 1 else self._rows.stride or 0
         self._c = ResidualStruct(_ptr(residual), _ptr(gate), int(stride), self._per)
-        self._ref = ctypes.addressof(self._c)
 
-    def _need(self, M: int, N: int):
+    def _args(self, M: int, N: int):
+        """The struct for a call over M tokens, sizes checked."""
+        now = self._now()
+        if M <= 0:
+            return now
         if self._held is not None and self._held < M * N * 2:
             raise ValueError(f"residual: holds {self._held} bytes, the call accesses {M * N * 2}")
         if self._rows is not None:
             self._rows.need(M, N, self._per)
+        return now
 
 
 class Rope:
@@ -346,14 +391,17 @@ class Rope:
         self._ref = ctypes.addressof(self._c)
 
 
-class Heads:
+class Heads(_Described):
     """The heads of queries or keys (svdq_heads): BF16 CUDA tensors
     [batch, token, head, head_dim] -- or [token, head, head_dim] -- of any
     strides over contiguous values; out None is in place.  Holds references to
     its tensors; one object can be used for any number of calls."""
 
     def __init__(self, x, out=None, weight=None):
-        out = x if out is None else out
+        self._hold(x, x if out is None else out, weight)
+
+    def _describe(self):
+        x, out, weight = self._keep
         shapes = []
         for t, what in ((x, "x"), (out, "out")):
             _bf16_tensor(t, what)
@@ -377,9 +425,7 @@ class Heads:
             s = s if t.dim() == 4 else (0,) + s
             # the stride of an axis of one is not used
             return [v if n > 1 else 0 for v, n in zip(s, shapes[0])]
-        self._keep = (x, out, weight)
         self._c = HeadsStruct(_ptr(x), _ptr(out), self.heads, *strides(x), *strides(out), _ptr(weight))
-        self._ref = ctypes.addressof(self._c)
 
 
 def _positions(rope: Rope, positions, batch: int, tokens: int) -> int:
@@ -397,13 +443,14 @@ def _positions(rope: Rope, positions, batch: int, tokens: int) -> int:
 def rope_heads(rope: Rope, q: Heads, k: Optional[Heads], positions, stream=None):
     """Normalise and rotate the heads of q and k (svdq_rope_heads); positions:
     float32 [token, axis], or [batch, token, axis]."""
+    q_now, k_now = q._now(), None if k is None else k._now()
     for t, what in ((q, "q"), (k, "k")):
         if t is not None and (t.head_dim != rope.head_dim or (t.batch, t.tokens) != (q.batch, q.tokens)):
             raise ValueError(f"{what}: [{t.batch}, {t.tokens}, heads, {t.head_dim}] does not fit the others")
     if (k is not None and k.device != q.device) or (_is_tensor(positions) and positions.get_device() != q.device):
         raise ValueError("q, k and the positions must be on one device")
     pos_batch = _positions(rope, positions, q.batch, q.tokens)
-    _check(load().svdq_rope_heads(rope._ref, q._ref, None if k is None else k._ref, q.batch, q.tokens,
+    _check(load().svdq_rope_heads(rope._ref, q_now, k_now, q.batch, q.tokens,
                                   _ptr(positions), pos_batch, _stream(stream)), "svdq_rope_heads")
 
 
@@ -588,20 +635,18 @@ class Layer:
         """Normalisation and the first kernel in one pass (svdq_norm_quantize_act);
         Y, if given, receives the normalised rows."""
         self._need_act(M, X=X, codes=codes, scales=scales, xl=xl)
-        if M > 0:
-            norm._need(M, self._K)
-            if Y is not None:
-                _need(Y, M * self._K * 2, "Y")
-        _check(load().svdq_norm_quantize_act(self._h, norm._ref, _ptr(X), M, _ptr(codes), _ptr(scales), _ptr(xl),
+        n = norm._args(M, self._K)
+        if M > 0 and Y is not None:
+            _need(Y, M * self._K * 2, "Y")
+        _check(load().svdq_norm_quantize_act(self._h, n, _ptr(X), M, _ptr(codes), _ptr(scales), _ptr(xl),
                                              _ptr(Y), _stream(stream)), "svdq_norm_quantize_act")
 
     def norm_forward(self, norm: Norm, X, M: int, Y, workspace, workspace_bytes: int, stream=None, flags: int = 0):
         """Normalisation, then the layer (svdq_norm_linear_forward)."""
         self._need_act(M, X=X, Y=Y)
-        if M > 0:
-            norm._need(M, self._K)
+        n = norm._args(M, self._K)
         _need(workspace, workspace_bytes, "workspace")
-        _check(load().svdq_norm_linear_forward(self._h, norm._ref, _ptr(X), M, _ptr(Y), _ptr(workspace),
+        _check(load().svdq_norm_linear_forward(self._h, n, _ptr(X), M, _ptr(Y), _ptr(workspace),
                                                workspace_bytes, _stream(stream), flags), "svdq_norm_linear_forward")
 
     def qkv_forward(self, norm: Optional[Norm], X, batch: int, T: int, rope: Rope, q_heads: int, k_heads: int,
@@ -611,16 +656,13 @@ class Layer:
         k_heads heads of each row, in place (svdq_qkv_forward)."""
         M = batch * T
         self._need_act(M, X=X, Y=Y)
-        pos_batch = 0
-        if batch > 0 and T > 0:
-            if norm is not None:
-                norm._need(M, self._K)
-            pos_batch = _positions(rope, positions, batch, T)
+        n = None if norm is None else norm._args(M, self._K)
+        pos_batch = _positions(rope, positions, batch, T) if batch > 0 and T > 0 else 0
         for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
             if w is not None:
                 _need(w, rope.head_dim * 2, what)
         _need(workspace, workspace_bytes, "workspace")
-        _check(load().svdq_qkv_forward(self._h, None if norm is None else norm._ref, _ptr(X), batch, T, rope._ref,
+        _check(load().svdq_qkv_forward(self._h, n, _ptr(X), batch, T, rope._ref,
                                        q_heads, k_heads, _ptr(q_weight), _ptr(k_weight), _ptr(positions), pos_batch,
                                        _ptr(Y), _ptr(workspace), workspace_bytes, _stream(stream), flags),
                "svdq_qkv_forward")
@@ -628,19 +670,17 @@ class Layer:
     def gemm_residual(self, codes, scales, xl, M: int, residual: Residual, Y, stream=None, flags: int = 0):
         """The second kernel with a residual in its epilogue (svdq_gemm_residual)."""
         self._need_act(M, Y=Y, codes=codes, scales=scales, xl=xl)
-        if M > 0:
-            residual._need(M, self._N)
-        _check(load().svdq_gemm_residual(self._h, _ptr(codes), _ptr(scales), _ptr(xl), M, residual._ref, _ptr(Y),
+        r = residual._args(M, self._N)
+        _check(load().svdq_gemm_residual(self._h, _ptr(codes), _ptr(scales), _ptr(xl), M, r, _ptr(Y),
                                          _stream(stream), flags), "svdq_gemm_residual")
 
     def forward_residual(self, X, M: int, residual: Residual, Y, workspace, workspace_bytes: int, stream=None,
                          flags: int = 0):
         """Forward with a residual in the GEMM's epilogue (svdq_linear_forward_residual)."""
         self._need_act(M, X=X, Y=Y)
-        if M > 0:
-            residual._need(M, self._N)
+        r = residual._args(M, self._N)
         _need(workspace, workspace_bytes, "workspace")
-        _check(load().svdq_linear_forward_residual(self._h, _ptr(X), M, residual._ref, _ptr(Y), _ptr(workspace),
+        _check(load().svdq_linear_forward_residual(self._h, _ptr(X), M, r, _ptr(Y), _ptr(workspace),
                                                    workspace_bytes, _stream(stream), flags),
                "svdq_linear_forward_residual")
 
@@ -702,12 +742,8 @@ def mlp_block_forward(fc1: Layer, fc2: Layer, norm: Optional[Norm], X, M: int, r
     """[norm ->] fc1 -> [GELU] -> fc2 [-> residual] (svdq_mlp_block_forward)."""
     fc1._need_act(M, X=X)
     fc2._need_act(M, Y=Y)
-    if M > 0:
-        if norm is not None:
-            norm._need(M, fc1._K)
-        if residual is not None:
-            residual._need(M, fc2._N)
+    n = None if norm is None else norm._args(M, fc1._K)
+    r = None if residual is None else residual._args(M, fc2._N)
     _need(workspace, workspace_bytes, "workspace")
-    _check(load().svdq_mlp_block_forward(fc1._h, fc2._h, None if norm is None else norm._ref, _ptr(X), M,
-                                         None if residual is None else residual._ref, _ptr(Y), _ptr(workspace),
+    _check(load().svdq_mlp_block_forward(fc1._h, fc2._h, n, _ptr(X), M, r, _ptr(Y), _ptr(workspace),
                                          workspace_bytes, _stream(stream), flags), "svdq_mlp_block_forward")
