@@ -397,3 +397,19 @@ def test_binding_refuses_a_released_storage():
         lib.Norm(weight=Released((256,), (1,)))
     with pytest.raises(ValueError, match="released"):
         lib.Residual(D, gate=Released((2, 256), (256, 1)))
+
+
+def test_a_copied_rope_stands_on_its_own():
+    """A copy passes its own struct, not the address of the one it was copied from."""
+    import copy
+    import pickle
+
+    def passed(r):
+        return bytes(ctypes.string_at(ctypes.addressof(r._ref._obj), ctypes.sizeof(r._c)))
+    first = lib.Rope(64, (16, 24, 24), theta=1e4)
+    copies = [copy.deepcopy(first), pickle.loads(pickle.dumps(first))]
+    want = passed(first)
+    first._c.head_dim, first._c.theta = -1, 0.0
+    for r in copies:
+        assert passed(r) == want
+        assert r._ref._obj is r._c

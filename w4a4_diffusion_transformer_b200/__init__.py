@@ -388,7 +388,9 @@ class Rope:
         self.head_dim, self.axes = int(head_dim), len(dims)
         self._c = RopeStruct(len(dims), (ctypes.c_int * 4)(*dims), int(head_dim), float(theta), float(eps),
                              (ROPE_HALF if half else 0) | (ROPE_SPAN if span else 0) | (ROPE_NORM if norm else 0))
-        self._ref = ctypes.addressof(self._c)
+
+    # a reference made at the call: a copied or unpickled object has a struct of its own
+    _ref = property(lambda self: ctypes.byref(self._c))
 
 
 class Heads(_Described):
