@@ -336,3 +336,111 @@ def test_operands_that_get_another_storage_are_followed():
     made["weight"].untyped_storage().resize_(0)
     with pytest.raises(ValueError, match="released"):
         call()
+
+
+# ------------------------------------------------------------------ every form of the kernel
+
+def launched(fmt, M, K, nmt, sms):
+    """(chunks, warps, blocks projected, unpredicated) of the kernel form that
+    the launch rules choose."""
+    def chunks(l):
+        return -(-(K // 8) // (32 << l))
+
+    def few(warps, l):
+        return -(-M // (warps >> l)) < sms
+    l, warps = 0, 8
+    if nmt == 0:
+        if chunks(3) > 4:
+            warps = 16
+        most = 4 if warps == 16 else 3
+        while l < most and chunks(l) > 6:
+            l += 1
+        while l < most and few(warps, l):
+            l += 1
+        c = chunks(l)
+        C = (4 if c <= 4 else 6) if warps == 16 else c if c <= 4 else 6
+    else:
+        while l < 3 and chunks(l) > 12:
+            l += 1
+        smem = (2 * 3 * 16 + 16) * 4 + 12 * K + (16 >> l) * (2 * K + 64) + 16 * nmt * 16 * 16 * 4
+        C = 12
+        if smem <= 232448:
+            warps = 16
+            while l < 3 and few(16, l):
+                l += 1
+            c = chunks(l)
+            C = 2 if c <= 2 else 4 if c <= 4 else 6 if c <= 6 else 12
+    full = C >= 6 and not (nmt and warps == 8) and K == (256 * C) << l
+    return fmt, C, warps, nmt, full
+
+
+PLAIN = [  # M, K, options; rank 0, no adapter: codes and scales only
+    (1, 64, dict()),
+    (5, 3072, dict(center=True, mods=1)),           # few rows: eight warps to a row
+    (130, 320, dict(residual=False, center=True)),
+    (1201, 512, dict(mods=2, center=True)),
+    (1201, 576, dict(weight=False, mods=401, rows_per_mod=3)),   # three or four modulation rows to a tile
+    (1300, 128, dict(mods=1300, rows_per_mod=1, center=True)),   # ... one for each token
+    (1201, 1024, dict(residual=False)),
+    (1201, 1472, dict(mods=3)),
+    (1201, 1536, dict(mods=2, center=True)),        # every lane full: one, two, four warps to a row
+    (650, 3072, dict(mods=4, weight=False, center=True)),
+    (300, 6144, dict(residual=False)),
+    (300, 8192, dict(mods=2)),
+    (5, 8256, dict(mods=2, center=True)),           # above 8192 columns: CTAs of 16 warps
+    (300, 9216, dict(mods=2, center=True)),
+    (301, 12288, dict(weight=False, mods=2)),
+    (300, 14336, dict(center=True)),
+]
+PROJECT = [
+    (50, 256, dict(mods=2)),
+    (1201, 2048, dict(mods=2, center=True)),
+    (1201, 576, dict(weight=False, mods=401, rows_per_mod=3)),
+    (1201, 2816, dict(residual=False)),
+    (1201, 3072, dict(mods=3, center=True)),
+    (2401, 2944, dict(mods=2)),
+    (2401, 3072, dict(mods=2, weight=False, center=True)),
+    (1201, 6144, dict(residual=False, mods=1)),
+    (300, 14336, dict(mods=2, center=True)),        # 16 rows do not fit in shared memory: CTAs of 8 warps
+]
+FORMS = ([(f, 0, M, K, o_) for f in ("nvfp4", "int4", "w8a8") for M, K, o_ in PLAIN]
+         + [(f, n, M, K, o_) for f, n in (("w8a8", 1), ("nvfp4", 2), ("nvfp4", 4), ("int4", 2), ("int4", 4))
+            for M, K, o_ in PROJECT])
+_layers = {}
+
+
+def _layer_of(fmt, nmt, K):
+    """A layer whose norm projects nmt blocks of 16 branch columns: by its own
+    rank, and with four by an adapter too."""
+    key = (fmt, nmt, K)
+    if key not in _layers:
+        _layers.clear()                              # neighbours in FORMS differ in K
+        d = syn.custom_layer(860 + K, M=8, K=K, N=64, calib_tokens=16)
+        L = _layers[key] = prepare_gpu(d, fmt=fmt, rank=0 if nmt == 0 else RANK[fmt])
+        if nmt == 4:
+            rng = np.random.default_rng([32, K])
+            L.set_lora(syn.bf16_bits(_bf(rng, K, 20, a=0.05)), syn.bf16_bits(_bf(rng, 20, 64)), 0.5)
+    return _layers[key]
+
+
+@pytest.mark.parametrize("fmt,nmt,M,K,opt", FORMS)
+def test_every_form_of_the_kernel(fmt, nmt, M, K, opt):
+    """h, y, codes, scales (byte for byte those of svdq_quantize_act on y) and XL."""
+    L = _layer_of(fmt, nmt, K)
+    d = _inputs(12 + nmt, M, K, **opt)
+    got = run(L, d)
+    check(L, d, got)
+    compare_with_first_kernel(L, got, M, K)
+
+
+def test_the_forms_above_are_all():
+    import torch
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    reached = {launched(f, M, K, n, sms) for f, n, M, K, _ in FORMS}
+    plain = [(C, 8, 0, False) for C in (1, 2, 3, 4, 6)] + [(6, 8, 0, True), (4, 16, 0, False), (6, 16, 0, False),
+                                                           (6, 16, 0, True)]
+    want = {(f,) + v for f in ("nvfp4", "int4", "w8a8") for v in plain}
+    for f, n in (("w8a8", 1), ("nvfp4", 2), ("nvfp4", 4), ("int4", 2), ("int4", 4)):
+        want |= {(f, 12, 8, n, False), (f, 2, 16, n, False), (f, 4, 16, n, False)}
+        want |= {(f, C, 16, n, full) for C in (6, 12) for full in (False, True)}
+    assert want == reached
