@@ -413,3 +413,131 @@ def test_a_copied_rope_stands_on_its_own():
     for r in copies:
         assert passed(r) == want
         assert r._ref._obj is r._c
+
+
+# ------------------------------------------------------------------ outputs that meet anything else
+
+def _near(at, n):
+    """Addresses whose n bytes reach into those at `at`: from its start, its end, and from before."""
+    return [at, at + n - 16, at - 16]
+
+
+@pytest.mark.parametrize("name", ["residual", "weight", "scale", "shift", "sum"])
+def test_norm_outputs_may_not_meet_its_operands(layer, name):
+    M, K, N = 4, 256, 128
+    rows = dict(mod_stride=512, rows_per_mod=2) if name in ("scale", "shift") else {}
+    size = {"weight": 2 * K, "scale": 2 * (512 + K), "shift": 2 * (512 + K)}.get(name, 2 * M * K)
+    kw = {name: 20 * A, **rows}
+    assert norm_call(layer, Y=F, **kw) == lib.ESTATE
+    for at in _near(20 * A, size):
+        for out in ("Y", "codes", "scales", "xl"):
+            assert norm_call(layer, **{out: at}, **kw) == lib.EINVAL, (out, at)
+        assert norm_call(layer, Y=F, codes=B, **kw) == lib.ESTATE
+    # ... and past its last byte, or in front of its first
+    assert norm_call(layer, Y=20 * A + size, **kw) == lib.ESTATE
+    assert norm_call(layer, Y=20 * A - 2 * M * K, **kw) == lib.ESTATE
+    n, need = lib.Norm(**kw), layer.workspace_bytes(M)
+
+    def fwd(Y=E, ws=F):
+        return status(lambda: layer.norm_forward(n, A, M, Y, ws, need))
+    assert fwd() == lib.ESTATE
+    for at in _near(20 * A, size):
+        assert fwd(Y=at) == lib.EINVAL
+    for at in (20 * A, 20 * A - 256):
+        assert fwd(ws=at) == lib.EINVAL
+    assert fwd(Y=20 * A + size) == fwd(Y=20 * A - 2 * M * N) == lib.ESTATE
+
+
+def test_norm_outputs_may_not_meet_each_other(layer):
+    M = 4
+    size = {"codes": layer.act_code_bytes(M), "scales": layer.act_scale_bytes(M), "xl": M * 64, "Y": M * 512}
+    outs = dict(codes=B, scales=C, xl=D, Y=F)
+    assert norm_call(layer, **outs) == lib.ESTATE
+    for a in outs:
+        for b in outs:
+            if a != b:
+                for at in _near(outs[b], size[b]):
+                    assert norm_call(layer, **{**outs, a: at}) == lib.EINVAL, (a, b)
+        for at in _near(A, M * 512):
+            assert norm_call(layer, **{**outs, a: at}) == lib.EINVAL, a
+    need = layer.workspace_bytes(M)
+    for bad in (dict(ws=A), dict(ws=E), dict(Y=F + 512), dict(Y=F - 16)):
+        c = {**dict(Y=E, ws=F), **bad}
+        assert status(lambda: layer.norm_forward(lib.Norm(), A, M, c["Y"], c["ws"], need)) == lib.EINVAL, bad
+    # rank 0 without an adapter writes no XL: what is passed for it does not count
+    assert norm_call(_layer(fmt="w8a8", rank=0), xl=A) == lib.ESTATE
+
+
+def test_rows_whose_last_has_no_address_are_refused(layer):
+    far = (1 << 62) + 8
+    assert norm_call(layer, scale=E, mod_stride=far, rows_per_mod=2) == lib.EINVAL
+    assert norm_call(layer, scale=E, mod_stride=far, rows_per_mod=4) == lib.ESTATE     # one row
+    for rows, want in ((2, lib.EINVAL), (4, lib.ESTATE)):
+        r = lib.Residual(D, gate=F, gate_stride=far, rows_per_gate=rows)
+        assert status(lambda: layer.gemm_residual(A, B, C, 4, r, E)) == want
+
+
+def test_residual_outputs_may_not_meet_operands(layer):
+    M, need = 4, layer.workspace_bytes(4)
+    r = lib.Residual(D, gate=20 * A, gate_stride=256, rows_per_gate=2)
+
+    def gemm(Y=E, **kw):
+        c = {**dict(codes=A, scales=B, xl=C), **kw}
+        return status(lambda: layer.gemm_residual(c["codes"], c["scales"], c["xl"], M, r, Y, None, c.get("flags", 0)))
+    assert gemm() == lib.ESTATE
+    for at, n in ((A, layer.act_code_bytes(M)), (B, layer.act_scale_bytes(M)), (C, M * 64), (20 * A, 2 * (256 + 128))):
+        for y in _near(at, n):
+            assert gemm(Y=y) == lib.EINVAL
+        assert gemm(Y=at + n) == lib.ESTATE
+    assert gemm(Y=C, flags=lib.FWD_NO_BRANCH) == lib.ESTATE            # XL is not read
+
+    def fwd(Y=E, ws=F, X=A):
+        return status(lambda: layer.forward_residual(X, M, r, Y, ws, need))
+    assert fwd() == fwd(Y=D) == lib.ESTATE
+    for at, n in ((A, M * 512), (D, M * 256), (E, M * 256), (20 * A, 768)):
+        for ws in (at, at - 256, (at + n - 1) // 256 * 256):
+            assert fwd(ws=ws) == lib.EINVAL
+
+
+def test_qkv_outputs_may_not_meet_operands():
+    L = _layer(K=256, N=64 * 6)
+    M, need = 8, L.workspace_bytes(8)
+    rope, plain = lib.Rope(64, (16, 24, 24), norm=True), lib.Rope(64, (16, 24, 24))
+
+    def call(norm=None, qw=20 * A, kw=21 * A, pos=22 * A, Y=E, ws=F, rp=rope, hk=2):
+        return status(lambda: L.qkv_forward(norm, A, 2, 4, rp, 2, hk, pos, Y, ws, need, qw, kw))
+    norm = lib.Norm(sum=23 * A)
+    for n in (None, norm):
+        assert call(norm=n) == lib.ESTATE
+        for at, size in ((20 * A, 128), (21 * A, 128), (22 * A, 48)):
+            for y in _near(at, size):
+                assert call(norm=n, Y=y) == lib.EINVAL
+            assert call(norm=n, ws=at) == lib.EINVAL
+            assert call(norm=n, Y=at + 16 * ((size + 15) // 16)) == lib.ESTATE
+        assert call(norm=n, ws=E) == lib.EINVAL
+        assert call(norm=n, ws=A) == lib.EINVAL
+    for kw in (dict(qw=23 * A), dict(kw=23 * A + 64), dict(pos=23 * A + M * 512 - 4)):
+        assert call(norm=norm, **kw) == lib.EINVAL
+    assert call(Y=20 * A, rp=plain) == lib.ESTATE                      # weights are not read
+    assert call(Y=21 * A, hk=0) == lib.ESTATE
+
+
+def test_mlp_block_outputs_may_not_meet_operands():
+    fc1, fc2 = _layer(K=256, N=512), _layer(K=512, N=256)
+    M = 4
+    need = 1 << 28                                                     # (host-only layers give no size)
+
+    def call(norm=None, res=None, X=A, Y=E, ws=F):
+        return status(lambda: lib.mlp_block_forward(fc1, fc2, norm, X, M, res, Y, ws, need, None, lib.FWD_GELU))
+    rows = dict(mod_stride=512, rows_per_mod=2)
+    stream = lib.Norm(sum=A, scale=20 * A, shift=21 * A, weight=22 * A, **rows)
+    gated = lib.Residual(A, gate=24 * A, gate_stride=512, rows_per_gate=2)
+    assert call(stream, gated, Y=A) == lib.ESTATE                      # the stream in place throughout
+    assert call(lib.Norm(residual=23 * A, sum=B), lib.Residual(B), Y=23 * A) == lib.ESTATE
+    for at in (20, 21, 22, 24):
+        assert call(stream, gated, Y=at * A) == lib.EINVAL
+    assert call(lib.Norm(sum=24 * A), gated) == lib.EINVAL             # the gate, read after the sum
+    assert call(lib.Norm(sum=B), lib.Residual(B + 512)) == lib.EINVAL
+    for at in (20, 21, 22, 24, 1):
+        assert call(stream, gated, Y=A, ws=at * A) == lib.EINVAL
+    assert call(None, None, ws=E) == call(None, None, ws=A) == lib.EINVAL

@@ -10,6 +10,7 @@
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <new>
 #include <vector>
@@ -797,22 +798,61 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return x < y + nb && y < x + na;
 }
 
-svdq_status check_norm(const svdq_layer* L, const svdq_norm* n, const void* X, int M) {
+// Bytes that a call reads or writes at an address (none at NULL).
+struct Span {
+  const void* at;
+  size_t bytes;
+};
+
+bool meets(const Span& a, std::initializer_list<Span> others) {
+  for (const Span& b : others)
+    if (overlap(a.at, a.bytes, b.at, b.bytes)) return true;
+  return false;
+}
+
+// Rows of cols values shared by runs of `per` of M tokens (0: one row for all),
+// stride elements apart.  Strides whose last row has no address: false.
+bool shared_rows(const void* at, int M, int per, int64_t stride, int cols, Span* out) {
+  const int64_t last = per > 0 ? (M - 1) / per : 0;
+  if (last > 0 && stride > (INT64_MAX / 4 - cols) / last) return false;
+  *out = {at, (size_t)(last * stride + cols) * 2};
+  return true;
+}
+
+// What a normalisation reads and writes beside the codes, scales, XL and Y.
+struct NormSpans {
+  Span x, residual, sum, weight, scale, shift;
+};
+
+bool norm_spans(const svdq_layer* L, const svdq_norm* n, const void* X, int M, NormSpans* o) {
+  const size_t act = (size_t)M * L->host.K * 2;
+  o->x = {X, act};
+  o->residual = {n->residual, act};
+  o->sum = {n->sum, act};
+  o->weight = {n->weight, (size_t)L->host.K * 2};
+  return shared_rows(n->scale, M, n->rows_per_mod, n->mod_stride, L->host.K, &o->scale) &&
+         shared_rows(n->shift, M, n->rows_per_mod, n->mod_stride, L->host.K, &o->shift);
+}
+
+// Whether an output meets anything of the normalisation in front of it.
+bool meets_norm(const Span& out, const NormSpans& n) {
+  return meets(out, {n.x, n.residual, n.sum, n.weight, n.scale, n.shift});
+}
+
+svdq_status check_norm(const svdq_layer* L, const svdq_norm* n, const void* X, int M, NormSpans* spans) {
   if (!n || misaligned(n->residual) || misaligned(n->sum) || misaligned(n->weight) || misaligned(n->scale) ||
       misaligned(n->shift))
     return SVDQ_EINVAL;
   if (n->flags & ~SVDQ_NORM_CENTER) return SVDQ_EINVAL;
   if (!(n->eps > 0.0f) || !std::isfinite(n->eps)) return SVDQ_EINVAL;
   if ((n->scale || n->shift) && (n->rows_per_mod < 0 || n->mod_stride < 0 || n->mod_stride % 8)) return SVDQ_EINVAL;
-  const size_t act = (size_t)M * L->host.K * 2;
-  if (n->sum != X && overlap(n->sum, act, X, act)) return SVDQ_EINVAL;
-  if (n->sum != n->residual && overlap(n->sum, act, n->residual, act)) return SVDQ_EINVAL;
+  NormSpans o;
+  if (!norm_spans(L, n, X, M, &o)) return SVDQ_EINVAL;
+  if (n->sum != X && meets(o.sum, {o.x})) return SVDQ_EINVAL;
+  if (n->sum != n->residual && meets(o.sum, {o.residual})) return SVDQ_EINVAL;
   // every row's parameters are read while others' sums are written
-  const size_t last = n->rows_per_mod > 0 ? (size_t)((M - 1) / n->rows_per_mod) * (size_t)n->mod_stride : 0;
-  const size_t mod = (last + (size_t)L->host.K) * 2;
-  if (overlap(n->sum, act, n->weight, (size_t)L->host.K * 2) || overlap(n->sum, act, n->scale, mod) ||
-      overlap(n->sum, act, n->shift, mod))
-    return SVDQ_EINVAL;
+  if (meets(o.sum, {o.weight, o.scale, o.shift})) return SVDQ_EINVAL;
+  if (spans) *spans = o;
   if (!w4a4(L) || L->host.K > kNormMaxK) return SVDQ_EUNSUPPORTED;
   return SVDQ_OK;
 }
@@ -962,13 +1002,20 @@ svdq_status run_gemm_stage(const svdq_layer* L, const void* codes, const void* s
   return run_k2(L, codes, scales, xl, M, Y, s, branch, gelu, lora_on, opt);
 }
 
-svdq_status check_residual(const svdq_layer* L, const svdq_residual* r, int M, const void* Y, ResidualParams* out) {
+struct ResidualSpans {
+  Span residual, gate;
+};
+
+svdq_status check_residual(const svdq_layer* L, const svdq_residual* r, int M, const void* Y, ResidualParams* out,
+                           ResidualSpans* spans) {
   if (!r || !r->residual || misaligned(r->residual) || misaligned(r->gate)) return SVDQ_EINVAL;
   if (r->gate && (r->rows_per_gate < 0 || r->gate_stride < 0 || r->gate_stride % 8)) return SVDQ_EINVAL;
   const size_t bytes = (size_t)M * L->host.N * 2;
-  if (r->residual != Y && overlap(r->residual, bytes, Y, bytes)) return SVDQ_EINVAL;
-  const size_t last = r->gate && r->rows_per_gate > 0 ? (size_t)((M - 1) / r->rows_per_gate) * (size_t)r->gate_stride : 0;
-  if (overlap(r->gate, (last + (size_t)L->host.N) * 2, Y, bytes)) return SVDQ_EINVAL;
+  spans->residual = {r->residual, bytes};
+  if (!shared_rows(r->gate, M, r->gate ? r->rows_per_gate : 0, r->gate_stride, L->host.N, &spans->gate))
+    return SVDQ_EINVAL;
+  if (r->residual != Y && meets({Y, bytes}, {spans->residual})) return SVDQ_EINVAL;
+  if (meets({Y, bytes}, {spans->gate})) return SVDQ_EINVAL;
   out->residual = static_cast<const __nv_bfloat16*>(r->residual);
   out->gate = static_cast<const __nv_bfloat16*>(r->gate);
   out->gate_stride = r->gate_stride;
@@ -1549,11 +1596,16 @@ svdq_status svdq_norm_quantize_act(const svdq_layer* L, const svdq_norm* norm, c
   svdq_status st = check_forward_args(L, X, M, codes);
   if (st == SVDQ_EINVAL) return st;
   if (!scales) return SVDQ_EINVAL;
-  const svdq_status sn = check_norm(L, norm, X, M);
+  NormSpans n;
+  const svdq_status sn = check_norm(L, norm, X, M, &n);
   if (sn != SVDQ_OK) return sn;
-  if ((L->host.rank > 0 || L->host.lora_r > 0) && !xl) return SVDQ_EINVAL;
-  const size_t act = (size_t)M * L->host.K * 2;
-  if (overlap(Y, act, X, act) || overlap(Y, act, norm->residual, act) || overlap(Y, act, norm->sum, act))
+  const HostPrep& h = L->host;
+  const bool has_xl = h.rank > 0 || h.lora_r > 0;
+  if (has_xl && !xl) return SVDQ_EINVAL;
+  const Span y = {Y, (size_t)M * h.K * 2}, c = {codes, act_code_bytes(h, M)}, sc = {scales, act_scale_bytes(h, M)},
+             x = {has_xl ? xl : nullptr, (size_t)M * xl_width(h) * 2};
+  if (meets_norm(y, n) || meets_norm(c, n) || meets_norm(sc, n) || meets_norm(x, n) || meets(y, {c, sc, x}) ||
+      meets(c, {sc, x}) || meets(sc, {x}))
     return SVDQ_EINVAL;
   if (st != SVDQ_OK) return st;
   DeviceGuard g(L->device);
@@ -1565,14 +1617,14 @@ svdq_status svdq_norm_linear_forward(const svdq_layer* L, const svdq_norm* norm,
                                      void* workspace, size_t workspace_bytes, void* stream, unsigned flags) {
   svdq_status st = check_forward_args(L, X, M, Y);
   if (st == SVDQ_EINVAL) return st;
-  const svdq_status sn = check_norm(L, norm, X, M);
+  NormSpans n;
+  const svdq_status sn = check_norm(L, norm, X, M, &n);
   if (sn != SVDQ_OK) return sn;
   if (flags & ~(SVDQ_FWD_GELU | SVDQ_FWD_CHECK)) return SVDQ_EUNSUPPORTED;
   const WsLayout w = ws_layout(L->host, M);
   if (!workspace || workspace_bytes < w.total || (reinterpret_cast<uintptr_t>(workspace) & 255)) return SVDQ_EINVAL;
-  const size_t act = (size_t)M * L->host.K * 2, out = (size_t)M * L->host.N * 2;
-  if (overlap(Y, out, X, act) || overlap(Y, out, norm->residual, act) || overlap(Y, out, norm->sum, act))
-    return SVDQ_EINVAL;
+  const Span y = {Y, (size_t)M * L->host.N * 2}, work = {workspace, w.total};
+  if (meets_norm(y, n) || meets_norm(work, n) || meets(work, {y})) return SVDQ_EINVAL;
   if (st != SVDQ_OK) return st;
   DeviceGuard g(L->device);
   if (!g.ok) return SVDQ_ECUDA;
@@ -1633,10 +1685,19 @@ svdq_status svdq_qkv_forward(const svdq_layer* L, const svdq_norm* norm, const v
   for (int i = 0; i < (k_heads ? 2 : 1) && st == SVDQ_OK; ++i) st = check_heads(rope, &h[i], batch, T);
   if (st != SVDQ_OK) return st;
   if (!w4a4(L) || (flags & ~SVDQ_FWD_CHECK)) return SVDQ_EUNSUPPORTED;
+  const Span x = {X, (size_t)M * L->host.K * 2}, y = {Y, (size_t)M * N * 2}, work = {workspace, ws_layout(L->host, M).total};
+  // read last: nothing that the call writes before may lie over them
+  Span pos;
+  if (pos_batch > (INT64_MAX / 8 - (int64_t)T * rope->axes) / batch) return SVDQ_EINVAL;
+  pos = {positions, (size_t)((batch - 1) * pos_batch + (int64_t)T * rope->axes) * 4};
+  const Span qw = {(rope->flags & SVDQ_ROPE_NORM) ? q_weight : nullptr, (size_t)D * 2},
+             kw = {(rope->flags & SVDQ_ROPE_NORM) && k_heads ? k_weight : nullptr, (size_t)D * 2};
+  if (meets(y, {x, work, pos, qw, kw}) || meets(work, {x, pos, qw, kw}) ||
+      (norm && meets({norm->sum, x.bytes}, {pos, qw, kw})))
+    return SVDQ_EINVAL;
   if (norm) {
     st = svdq_norm_linear_forward(L, norm, X, M, Y, workspace, workspace_bytes, stream, 0);
   } else {
-    if (overlap(Y, (size_t)M * N * 2, X, (size_t)M * L->host.K * 2)) return SVDQ_EINVAL;
     st = svdq_linear_forward(L, X, M, Y, workspace, workspace_bytes, stream, 0);
   }
   if (st != SVDQ_OK) return st;
@@ -1653,9 +1714,15 @@ svdq_status svdq_gemm_residual(const svdq_layer* L, const void* codes, const voi
   if (!L || !Y || M < 1) return SVDQ_EINVAL;
   GemmOptions opt;
   opt.split = 1;
-  const svdq_status st = check_residual(L, res, M, Y, &opt.res);
+  ResidualSpans r;
+  const svdq_status st = check_residual(L, res, M, Y, &opt.res, &r);
   if (st != SVDQ_OK) return st;
-  if (flags & ~(SVDQ_FWD_GELU | SVDQ_FWD_CHECK | SVDQ_FWD_NO_BRANCH)) return SVDQ_EUNSUPPORTED;
+  if (!w4a4(L) || (flags & ~(SVDQ_FWD_GELU | SVDQ_FWD_CHECK | SVDQ_FWD_NO_BRANCH))) return SVDQ_EUNSUPPORTED;
+  const HostPrep& h = L->host;
+  const bool has_xl = (h.rank > 0 || h.lora_r > 0) && !(flags & SVDQ_FWD_NO_BRANCH);
+  if (meets({Y, (size_t)M * h.N * 2}, {{codes, act_code_bytes(h, M)}, {scales, act_scale_bytes(h, M)},
+                                       {has_xl ? xl : nullptr, (size_t)M * xl_width(h) * 2}}))
+    return SVDQ_EINVAL;
   return gemm_call(L, codes, scales, xl, M, Y, stream, flags, opt);
 }
 
@@ -1664,14 +1731,18 @@ svdq_status svdq_linear_forward_residual(const svdq_layer* L, const void* X, int
   if (!L || !X || !Y || M < 1) return SVDQ_EINVAL;
   GemmOptions opt;
   opt.split = 1;
-  svdq_status st = check_residual(L, res, M, Y, &opt.res);
+  ResidualSpans r;
+  svdq_status st = check_residual(L, res, M, Y, &opt.res, &r);
   if (st != SVDQ_OK) return st;
-  if (overlap(X, (size_t)M * L->host.K * 2, Y, (size_t)M * L->host.N * 2)) return SVDQ_EINVAL;
+  const Span x = {X, (size_t)M * L->host.K * 2}, y = {Y, (size_t)M * L->host.N * 2};
+  if (meets(y, {x})) return SVDQ_EINVAL;
   if (!w4a4(L) || (flags & ~(SVDQ_FWD_GELU | SVDQ_FWD_CHECK))) return SVDQ_EUNSUPPORTED;
-  st = check_forward_args(L, X, M, Y);
-  if (st != SVDQ_OK) return st;
+  const svdq_status state = check_forward_args(L, X, M, Y);
+  if (state == SVDQ_EINVAL) return state;
   const WsLayout w = ws_layout(L->host, M);
   if (!workspace || workspace_bytes < w.total || (reinterpret_cast<uintptr_t>(workspace) & 255)) return SVDQ_EINVAL;
+  if (meets({workspace, w.total}, {x, y, r.residual, r.gate})) return SVDQ_EINVAL;
+  if (state != SVDQ_OK) return state;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   st = svdq_quantize_act(L, X, M, ws + w.codes, ws + w.scales, ws + w.xl, stream, 0);
   return st == SVDQ_OK ? gemm_call(L, ws + w.codes, ws + w.scales, ws + w.xl, M, Y, stream, flags, opt) : st;
@@ -1685,22 +1756,31 @@ svdq_status svdq_mlp_block_forward(const svdq_layer* fc1, const svdq_layer* fc2,
   if (!fc2) return SVDQ_EINVAL;
   GemmOptions opt;
   opt.split = 1;
+  NormSpans n = {};
+  n.x = {X, (size_t)M * fc1->host.K * 2};
+  ResidualSpans r = {};
   if (norm) {
-    const svdq_status sn = check_norm(fc1, norm, X, M);
+    const svdq_status sn = check_norm(fc1, norm, X, M, &n);
     if (sn != SVDQ_OK) return sn;
   }
+  const Span y = {Y, (size_t)M * fc2->host.N * 2};
   if (res) {
-    const svdq_status sr = check_residual(fc2, res, M, Y, &opt.res);
+    const svdq_status sr = check_residual(fc2, res, M, Y, &opt.res, &r);
     if (sr != SVDQ_OK) return sr;
   }
   // Y may be X, the norm's residual or its sum: only the first kernel touches
-  // those, and the last one writes Y after every kernel before it has ended
-  if (st != SVDQ_OK) return st;
-  if (fc2->device < 0) return SVDQ_ESTATE;
-  if (!chainable(fc1, fc2)) return SVDQ_EUNSUPPORTED;
-  if (flags & ~(SVDQ_FWD_GELU | SVDQ_FWD_CHECK)) return SVDQ_EUNSUPPORTED;
+  // those, and the last one writes Y after every kernel before it has ended.
+  // The residual and the gate are read after the sum was written
+  if (meets(y, {n.weight, n.scale, n.shift}) || meets(n.sum, {r.gate}) ||
+      (r.residual.at != n.sum.at && meets(n.sum, {r.residual})))
+    return SVDQ_EINVAL;
+  if (!chainable(fc1, fc2)) return fc1->device < 0 || fc2->device < 0 ? SVDQ_ESTATE : SVDQ_EUNSUPPORTED;
   const ChainLayout c = chain_layout(fc1, fc2, M, false);
   if (!workspace || workspace_bytes < c.total || (reinterpret_cast<uintptr_t>(workspace) & 255)) return SVDQ_EINVAL;
+  if (meets_norm({workspace, c.total}, n) || meets({workspace, c.total}, {y, r.residual, r.gate})) return SVDQ_EINVAL;
+  if (st != SVDQ_OK) return st;
+  if (fc2->device < 0) return SVDQ_ESTATE;
+  if (flags & ~(SVDQ_FWD_GELU | SVDQ_FWD_CHECK)) return SVDQ_EUNSUPPORTED;
   DeviceGuard g(fc1->device);
   if (!g.ok) return SVDQ_ECUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
