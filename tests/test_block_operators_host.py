@@ -541,3 +541,88 @@ def test_mlp_block_outputs_may_not_meet_operands():
     for at in (20, 21, 22, 24, 1):
         assert call(stream, gated, Y=A, ws=at * A) == lib.EINVAL
     assert call(None, None, ws=E) == call(None, None, ws=A) == lib.EINVAL
+
+
+def _span(at, inner, terms):
+    """All bytes of nested runs."""
+    starts = np.array([at], dtype=np.int64)
+    for stride, n in terms:
+        starts = (starts[:, None] + stride * np.arange(n)[None]).reshape(-1)
+    return (starts[:, None] + np.arange(inner)[None]).reshape(-1)
+
+
+def _axes(h, side, heads_, B=2, T=4):
+    return [(2 * getattr(h, f"{side}_{a}"), n) for a, n in (("batch", B), ("token", T), ("head", heads_))]
+
+
+def test_rope_refuses_colliding_heads_and_takes_interleaved_ones():
+    """q's and k's outputs against every other operand, byte by byte: heads of one
+    fused buffer lie between each other, whatever their order; one value in common
+    is refused."""
+    rng = np.random.default_rng(20)
+    B, T, D = 2, 4, 64
+    rope, normed = lib.Rope(D, (16, 24, 24)), lib.Rope(D, (16, 24, 24), norm=True)
+    taken = refused = 0
+    for _ in range(700):
+        fused = int(rng.integers(3, 8))                  # heads of a token in the fused buffer
+        row = {"batch": T * fused * D, "token": fused * D, "head": D}
+        if rng.random() < 0.3:                           # heads in front of tokens
+            row = {"batch": T * fused * D, "head": T * D, "token": D}
+        if rng.random() < 0.3:                           # room between heads
+            row = {k: 2 * v for k, v in row.items()}
+
+        def tensor(away):
+            h, n = lib.HeadsStruct(), int(rng.integers(1, fused + 1))
+            step = int(rng.integers(1, 3)) if n <= fused // 2 else 1
+            h.heads, h.in_ = n, A + 16 * int(rng.choice([0, 8, 16, 24, 40])) * int(rng.integers(0, 3))
+            for a in ("batch", "token", "head"):
+                setattr(h, f"in_{a}", row[a] * (step if a == "head" else 1))
+                setattr(h, f"out_{a}", row[a] * (step if a == "head" else 1))
+            h.out = h.in_ + (away if rng.random() < 0.5 else 0)
+            h.weight = int(rng.choice([D * A, h.out + 16 * int(rng.integers(-8, 300))])) if rng.random() < 0.3 else None
+            return h
+        q, k = tensor(A), tensor(int(rng.choice([A, 2 * A])))
+        both = bool(rng.random() < 0.8)
+        r = normed if rng.random() < 0.5 else rope
+        pb = int(rng.choice([0, 12, 20]))
+        pos = int(rng.choice([C * 64, q.out + 4 * int(rng.integers(-30, 1500))]))
+        # each tensor by itself is taken where its outputs do not meet (checked elsewhere)
+        tensors = [q, k] if both else [q]
+        out = [_span(h.out, 2 * D, _axes(h, "out", h.heads)) for h in tensors]
+        if any(len(np.unique(o_)) != len(o_) for o_ in out):
+            continue
+        bad = False
+        for i, h in enumerate(tensors):
+            others = [_span(pos, T * 12, [(4 * pb, B)])]
+            others += [_span(g.weight, 2 * D, []) for g in tensors if r is normed and g.weight]
+            if both:
+                others += [_span(tensors[1 - i].in_, 2 * D, _axes(tensors[1 - i], "in", tensors[1 - i].heads)), out[1 - i]]
+            bad = bad or any(len(np.intersect1d(out[i], o_)) for o_ in others)
+        got = lib.load().svdq_rope_heads(r._ref, ctypes.addressof(q), ctypes.addressof(k) if both else None, B, T, pos,
+                                         pb, None)
+        assert (got == lib.EINVAL) == bad, ([[(f, getattr(h, f)) for f, _ in h._fields_] for h in tensors], pos, pb)
+        taken, refused = taken + (not bad), refused + bad
+    assert taken > 100 and refused > 100
+
+
+def test_rope_takes_fused_heads_of_any_grouping():
+    """Queries and keys of one buffer of grouped heads: one group's queries beside
+    all groups' keys, at sizes whose elements could not be listed."""
+    G, HK, D, B, T = 5, 8, 128, 300, 60000
+    tok = HK * (G + 2) * D
+    rope = lib.Rope(D, (32, 32, 64))
+
+    def tensor(first, n, head):
+        h = lib.HeadsStruct()
+        h.in_ = h.out = A + 2 * first * D
+        h.heads = n
+        h.in_batch = h.out_batch = T * tok
+        h.in_token = h.out_token = tok
+        h.in_head = h.out_head = head
+        return h
+
+    def call(q, k):
+        return lib.load().svdq_rope_heads(rope._ref, ctypes.addressof(q), ctypes.addressof(k), B, T, 1 << 50, 0, None)
+    for g in range(HK):
+        assert call(tensor(g * (G + 2), G, D), tensor(G, HK, (G + 2) * D)) != lib.EINVAL
+        assert call(tensor(g * (G + 2) + 1, G, D), tensor(G, HK, (G + 2) * D)) == lib.EINVAL

@@ -949,6 +949,108 @@ svdq_status check_heads(const svdq_rope* r, const svdq_heads* t, int B, int T) {
   return SVDQ_OK;
 }
 
+// The bytes of up to three nested runs: at + i0 stride0 + i1 stride1 + i2 stride2 + [0, inner).
+struct Lattice {
+  const void* at;
+  int64_t inner, stride[3], count[3];
+};
+
+Lattice heads_at(const void* at, const int64_t (&stride)[3], int heads, int D, int B, int T) {
+  Lattice o = {at, 2 * (int64_t)D, {}, {B, T, heads}};
+  for (int i = 0; i < 3; ++i) o.stride[i] = o.count[i] > 1 ? 2 * stride[i] : 0;   // (span_of has bounded these)
+  return o;
+}
+Lattice heads_in(const svdq_heads* t, int D, int B, int T) {
+  return heads_at(t->in, {t->in_batch, t->in_token, t->in_head}, t->heads, D, B, T);
+}
+Lattice heads_out(const svdq_heads* t, int D, int B, int T) {
+  return heads_at(t->out, {t->out_batch, t->out_token, t->out_head}, t->heads, D, B, T);
+}
+
+// Whether two of them share a byte.  Heads of one fused buffer lie between each
+// other without sharing one, so spans alone do not tell.  With d the distance of
+// two elements' starts, one of each, they share a byte when -b.inner < d <
+// a.inner; d is the bases' distance plus a sum of x s over the strides s, x in a
+// range of indices.  The strides are tried from the largest down, and of each only
+// the x that the smaller ones can still bring into reach: one or two for runs that
+// nest.  Runs for which that takes long do not nest: taken as sharing.
+struct LatticeSearch {
+  typedef __int128 wide;
+  struct Term {
+    int64_t stride, lo, hi;               // x in [lo, hi]
+    wide rest_lo, rest_hi;                // what the smaller strides add
+  };
+  Term terms[6];
+  int n = 0;
+  int64_t a_inner, b_inner;
+  int left = 4096;
+
+  void add(int64_t stride, int64_t lo, int64_t hi) {
+    if (stride == 0 || lo == hi) return;
+    for (int i = 0; i < n; ++i)
+      if (terms[i].stride == stride) {
+        terms[i].lo += lo;
+        terms[i].hi += hi;
+        return;
+      }
+    terms[n++] = {stride, lo, hi, 0, 0};
+  }
+  static wide floor_div(wide n, int64_t d) { return n >= 0 ? n / d : -((-n + d - 1) / d); }
+  bool reach(int i, wide d) {
+    if (i == n) return -b_inner < d && d < a_inner;
+    const Term& t = terms[i];
+    // -b_inner < d + x s + rest < a_inner for some rest in [rest_lo, rest_hi]
+    wide lo = -floor_div(d + t.rest_hi + b_inner - 1, t.stride), hi = floor_div(a_inner - 1 - d - t.rest_lo, t.stride);
+    if (lo < t.lo) lo = t.lo;
+    if (hi > t.hi) hi = t.hi;
+    for (wide x = lo; x <= hi; ++x)
+      if (--left < 0 || reach(i + 1, d + x * t.stride)) return true;
+    return false;
+  }
+};
+
+bool shares(const Lattice& a, const Lattice& b) {
+  if (!a.at || !b.at) return false;
+  LatticeSearch s;
+  s.a_inner = a.inner;
+  s.b_inner = b.inner;
+  for (int i = 0; i < 3; ++i) {
+    s.add(b.stride[i], 0, b.count[i] - 1);
+    s.add(a.stride[i], 1 - a.count[i], 0);
+  }
+  std::sort(s.terms, s.terms + s.n,
+            [](const LatticeSearch::Term& x, const LatticeSearch::Term& y) { return x.stride > y.stride; });
+  LatticeSearch::wide lo = 0, hi = 0;
+  for (int i = s.n; i-- > 0;) {
+    s.terms[i].rest_lo = lo;
+    s.terms[i].rest_hi = hi;
+    lo += (LatticeSearch::wide)s.terms[i].lo * s.terms[i].stride;
+    hi += (LatticeSearch::wide)s.terms[i].hi * s.terms[i].stride;
+  }
+  const LatticeSearch::wide d =
+      (LatticeSearch::wide)reinterpret_cast<uintptr_t>(b.at) - (LatticeSearch::wide)reinterpret_cast<uintptr_t>(a.at);
+  return s.reach(0, d);
+}
+
+// q's and k's outputs against everything else that the call touches.
+svdq_status check_rope_outputs(const svdq_rope* r, const svdq_heads* q, const svdq_heads* k, int B, int T,
+                               const float* positions, int64_t pos_batch) {
+  const int D = r->head_dim;
+  const bool norm = (r->flags & SVDQ_ROPE_NORM) != 0;
+  if (pos_batch > (INT64_MAX / 8 - (int64_t)T * r->axes) / B) return SVDQ_EINVAL;
+  const Lattice pos = {positions, (int64_t)T * r->axes * 4, {B > 1 ? pos_batch * 4 : 0, 0, 0}, {B, 1, 1}};
+  const svdq_heads* t[2] = {q, k};
+  for (int i = 0; i < (k ? 2 : 1); ++i) {
+    const Lattice out = heads_out(t[i], D, B, T);
+    if (shares(out, pos)) return SVDQ_EINVAL;
+    for (int j = 0; j < (k ? 2 : 1); ++j)
+      if (norm && shares(out, {t[j]->weight, 2 * (int64_t)D, {}, {1, 1, 1}})) return SVDQ_EINVAL;
+    if (k && shares(out, heads_in(t[1 - i], D, B, T))) return SVDQ_EINVAL;
+  }
+  if (k && shares(heads_out(q, D, B, T), heads_out(k, D, B, T))) return SVDQ_EINVAL;
+  return SVDQ_OK;
+}
+
 RopeTensor rope_tensor(const svdq_heads* t) {
   RopeTensor o = {};
   o.in = static_cast<const __nv_bfloat16*>(t->in);
@@ -1648,9 +1750,8 @@ svdq_status svdq_rope_heads(const svdq_rope* rope, const svdq_heads* q, const sv
   svdq_status st = check_rope(rope);
   if (st == SVDQ_OK) st = check_heads(rope, q, batch, T);
   if (st == SVDQ_OK && k) st = check_heads(rope, k, batch, T);
+  if (st == SVDQ_OK) st = check_rope_outputs(rope, q, k, batch, T, positions, pos_batch);
   if (st != SVDQ_OK) return st;
-  // (spans of heads of one fused buffer meet without sharing a value)
-  if (k && (q->out == k->out || q->out == k->in || k->out == q->in)) return SVDQ_EINVAL;
   cudaPointerAttributes at = {};
   if (cudaPointerGetAttributes(&at, q->in) != cudaSuccess) return SVDQ_ECUDA;
   if (at.type != cudaMemoryTypeDevice && at.type != cudaMemoryTypeManaged) return SVDQ_EINVAL;
