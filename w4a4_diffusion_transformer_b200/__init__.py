@@ -248,25 +248,27 @@ class _Described:
     and layout run when the struct is filled; a tensor can get another storage
     later (tensor.data = ..., a module moved between devices), so every call
     compares address, number of values and type first, and fills the struct again
-    where one changed.  (Shapes and strides too would cost twice as much, 2.3 us
+    where one changed.  (Shapes and strides too would cost twice as much, 2 us
     for the six operands of a rotation; a tensor transposed in place keeps the
     layout it was described with.)"""
 
     def _hold(self, *operands):
         self._keep = operands
-        self._tensors = [x for x in operands if _is_tensor(x)]
-        self._others = [x for x in operands if hasattr(x, "data_ptr") and not _is_tensor(x)]
-        self._seen = None
-        self._now()
+        self._fill()
+
+    def _fill(self):
+        self._seen = None                              # a refused operand is looked at again
+        self._describe()
+        self._seen = [(x, x.data_ptr(), x.numel(), x.dtype) for x in self._keep if _is_tensor(x)]
 
     def _now(self):
         """The struct as a call's argument, with the operands as they are now."""
-        seen = [(x.data_ptr(), x.numel(), x.dtype) for x in self._tensors]
-        if self._others:
-            seen += [x.data_ptr() for x in self._others]
-        if seen != self._seen:
-            self._describe()
-            self._seen = seen
+        if self._seen is None:
+            self._fill()
+        for x, ptr, n, dtype in self._seen:
+            if x.data_ptr() != ptr or x.numel() != n or x.dtype is not dtype:
+                self._fill()
+                break
         return ctypes.byref(self._c)
 
     _ref = property(_now)
