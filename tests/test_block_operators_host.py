@@ -384,6 +384,20 @@ def test_binding_follows_heads():
         _other_storage(t, 31 * A, is_cuda=True)
 
 
+def test_binding_asks_an_object_with_an_address_alone_each_time(layer):
+    class Buffer:
+        at = 10 * A
+
+        def data_ptr(self):
+            return self.at
+    b = Buffer()
+    n = lib.Norm(weight=b, sum=20 * A)
+    assert status(lambda: layer.norm_quantize_act(n, A, 4, B, C, E)) == lib.ESTATE
+    assert n._c.weight == 10 * A
+    b.at = 20 * A                                       # over the sum now
+    assert status(lambda: layer.norm_quantize_act(n, A, 4, B, C, E)) == lib.EINVAL
+
+
 def test_binding_refuses_a_released_storage():
     import torch
 

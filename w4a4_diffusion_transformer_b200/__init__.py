@@ -259,16 +259,19 @@ class _Described:
     def _fill(self):
         self._seen = None                              # a refused operand is looked at again
         self._describe()
-        self._seen = [(x, x.data_ptr(), x.numel(), x.dtype) for x in self._keep if _is_tensor(x)]
+        if not any(hasattr(x, "data_ptr") and not _is_tensor(x) for x in self._keep):   # (those: at every call)
+            self._seen = [(x, x.data_ptr(), x.numel(), x.dtype) for x in self._keep if _is_tensor(x)]
 
     def _now(self):
         """The struct as a call's argument, with the operands as they are now."""
-        if self._seen is None:
+        seen = self._seen                              # one read: another thread may fill it anew
+        if seen is None:
             self._fill()
-        for x, ptr, n, dtype in self._seen:
-            if x.data_ptr() != ptr or x.numel() != n or x.dtype is not dtype:
-                self._fill()
-                break
+        else:
+            for x, ptr, n, dtype in seen:
+                if x.data_ptr() != ptr or x.numel() != n or x.dtype is not dtype:
+                    self._fill()
+                    break
         return ctypes.byref(self._c)
 
     _ref = property(_now)
