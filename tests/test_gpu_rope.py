@@ -259,3 +259,37 @@ def test_heads_that_get_another_storage_are_followed():
     w.data = w.data.cpu()
     with pytest.raises(ValueError, match="weight"):
         call()
+
+
+@pytest.mark.parametrize("operand", ["q.in", "q.out", "q.weight", "k.in", "k.out", "k.weight", "positions"])
+@pytest.mark.parametrize("pinned", [False, True])
+def test_rope_refuses_host_memory_for_any_operand(operand, pinned):
+    import ctypes
+
+    import torch
+
+    def memory(*shape, dtype=torch.bfloat16, name):
+        if name != operand:
+            return torch.ones(shape, dtype=dtype, device="cuda")
+        t = torch.ones(shape, dtype=dtype)
+        return t.pin_memory() if pinned else t
+    hs, keep = [], []
+    for name in ("q", "k"):
+        t = [memory(1, 3, 2, 64, name=f"{name}.in"), memory(1, 3, 2, 64, name=f"{name}.out"),
+             memory(64, name=f"{name}.weight")]
+        h = lib.HeadsStruct()
+        h.in_, h.out, h.weight = (x.data_ptr() for x in t)
+        h.heads, h.in_token, h.in_head, h.out_token, h.out_head = 2, 128, 64, 128, 64
+        assert all(a % 16 == 0 for a in (h.in_, h.out, h.weight))
+        hs.append(h)
+        keep.append(t)
+    pos = memory(3, 1, dtype=torch.float32, name="positions")
+    f = lib.load().svdq_rope_heads
+
+    def call(rope):
+        return f(rope._ref, ctypes.addressof(hs[0]), ctypes.addressof(hs[1]), 1, 3, pos.data_ptr(), 0, None)
+    assert call(lib.Rope(64, (64,), norm=True)) == lib.EINVAL
+    if operand.endswith("weight"):                      # not read without the norm
+        assert call(lib.Rope(64, (64,))) == lib.OK
+    torch.cuda.synchronize()
+    assert bool((keep[1][1] == 1).all()) or operand.endswith("weight")

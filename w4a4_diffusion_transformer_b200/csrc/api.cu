@@ -1029,6 +1029,7 @@ bool shares(const Lattice& a, const Lattice& b) {
   }
   const LatticeSearch::wide d =
       (LatticeSearch::wide)reinterpret_cast<uintptr_t>(b.at) - (LatticeSearch::wide)reinterpret_cast<uintptr_t>(a.at);
+  if (d + hi <= -s.b_inner || d + lo >= s.a_inner) return false;   // the spans are apart: no search
   return s.reach(0, d);
 }
 
@@ -1755,6 +1756,20 @@ svdq_status svdq_rope_heads(const svdq_rope* rope, const svdq_heads* q, const sv
   cudaPointerAttributes at = {};
   if (cudaPointerGetAttributes(&at, q->in) != cudaSuccess) return SVDQ_ECUDA;
   if (at.type != cudaMemoryTypeDevice && at.type != cudaMemoryTypeManaged) return SVDQ_EINVAL;
+  const bool norm = (rope->flags & SVDQ_ROPE_NORM) != 0;
+  const void* others[] = {q->out, positions, norm ? q->weight : nullptr, k ? k->in : nullptr, k ? k->out : nullptr,
+                          k && norm ? k->weight : nullptr};
+  const int64_t n[3] = {batch, T, q->heads};
+  const size_t q_bytes = 2 * (size_t)span_of(rope->head_dim, {q->in_batch, q->in_token, q->in_head}, n, false);
+  for (const void* p : others) {
+    if (!p || overlap(p, 1, q->in, q_bytes)) continue;   // one buffer's heads: the same memory
+    cudaPointerAttributes b = {};
+    if (cudaPointerGetAttributes(&b, p) != cudaSuccess) return SVDQ_ECUDA;
+    // managed memory is every device's; the rest has to be q->in's device's
+    if (b.type != cudaMemoryTypeManaged &&
+        (b.type != cudaMemoryTypeDevice || (at.type == cudaMemoryTypeDevice && b.device != at.device)))
+      return SVDQ_EINVAL;
+  }
   DeviceGuard g(at.device);
   if (!g.ok) return SVDQ_ECUDA;
   int sms = 0;
