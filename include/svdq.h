@@ -545,7 +545,7 @@ typedef struct {
  * Runs on the device that holds q->in, whichever is current; everything else
  * must be on that device too.  Errors:
  * SVDQ_EINVAL (NULL rope, q, positions or a tensor's pointers, sizes below 1, a
- * batch above 65535, strides, alignment, overlap, flags, theta or eps out of
+ * batch above 65535, more than 2^31 - 5 tokens or 2^20 heads, strides, alignment, overlap, flags, theta or eps out of
  * range, memory that is not device memory), SVDQ_EUNSUPPORTED (head_dim, dims as
  * above), SVDQ_ECUDA. */
 svdq_status svdq_rope_heads(const svdq_rope* rope, const svdq_heads* q, const svdq_heads* k, int batch, int T,

@@ -640,3 +640,17 @@ def test_rope_takes_fused_heads_of_any_grouping():
     for g in range(HK):
         assert call(tensor(g * (G + 2), G, D), tensor(G, HK, (G + 2) * D)) != lib.EINVAL
         assert call(tensor(g * (G + 2) + 1, G, D), tensor(G, HK, (G + 2) * D)) == lib.EINVAL
+
+
+def test_rope_refuses_sizes_that_pass_an_int():
+    """Inputs of one broadcast head or token make such sizes possible; the
+    kernel's indices run a step past the last."""
+    for n in ((1 << 20) + 1, 2 ** 31 - 1):
+        for q, k in ((heads(n=n, in_head=0, out_token=64 * n, out_batch=256 * n), None),
+                     (heads(), heads(in_=D, out=1 << 45, n=n, in_head=0, out_token=64 * n, out_batch=256 * n))):
+            assert rope_call(q=q, k=k) == lib.EINVAL
+    assert rope_call(q=heads(in_=1 << 50, n=1 << 20, in_head=0, out_token=64 << 20, out_batch=256 << 20), batch=1,
+                     positions=1 << 52) != lib.EINVAL
+    one = dict(in_=1 << 50, n=1, in_token=0, out_token=64)
+    assert rope_call(q=heads(**one), batch=1, T=2 ** 31 - 1, positions=1 << 52) == lib.EINVAL
+    assert rope_call(q=heads(**one), batch=1, T=2 ** 31 - 5, positions=1 << 52) != lib.EINVAL

@@ -6,7 +6,6 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <climits>
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
@@ -934,7 +933,7 @@ svdq_status check_rope(const svdq_rope* r) {
 }
 
 svdq_status check_heads(const svdq_rope* r, const svdq_heads* t, int B, int T) {
-  if (!t->in || !t->out || t->heads < 1 || misaligned(t->in) || misaligned(t->out) || misaligned(t->weight))
+  if (!t->in || !t->out || t->heads < 1 || t->heads > kRopeMaxHeads || misaligned(t->in) || misaligned(t->out) || misaligned(t->weight))
     return SVDQ_EINVAL;
   const int64_t in[3] = {t->in_batch, t->in_token, t->in_head}, out[3] = {t->out_batch, t->out_token, t->out_head};
   const int64_t n[3] = {B, T, t->heads};
@@ -1745,7 +1744,7 @@ svdq_status svdq_norm_linear_forward(const svdq_layer* L, const svdq_norm* norm,
 
 svdq_status svdq_rope_heads(const svdq_rope* rope, const svdq_heads* q, const svdq_heads* k, int batch, int T,
                             const float* positions, int64_t pos_batch, void* stream) {
-  if (!q || !positions || batch < 1 || batch > 65535 || T < 1 || (int64_t)batch * T > INT_MAX || pos_batch < 0 ||
+  if (!q || !positions || batch < 1 || batch > 65535 || T < 1 || (int64_t)batch * T > kRopeMaxTokens || pos_batch < 0 ||
       (reinterpret_cast<uintptr_t>(positions) & 3))
     return SVDQ_EINVAL;
   svdq_status st = check_rope(rope);
@@ -1781,7 +1780,7 @@ svdq_status svdq_qkv_forward(const svdq_layer* L, const svdq_norm* norm, const v
                              const svdq_rope* rope, int q_heads, int k_heads, const void* q_weight,
                              const void* k_weight, const float* positions, int64_t pos_batch, void* Y,
                              void* workspace, size_t workspace_bytes, void* stream, unsigned flags) {
-  if (!L || !X || !Y || !positions || batch < 1 || batch > 65535 || T < 1 || (int64_t)batch * T > INT_MAX || pos_batch < 0 ||
+  if (!L || !X || !Y || !positions || batch < 1 || batch > 65535 || T < 1 || (int64_t)batch * T > kRopeMaxTokens || pos_batch < 0 ||
       (reinterpret_cast<uintptr_t>(positions) & 3) || q_heads < 1 || k_heads < 0)
     return SVDQ_EINVAL;
   svdq_status st = check_rope(rope);

@@ -217,6 +217,8 @@ struct RopeParams {
   long long pos_batch;
   int log2_splits, log2_pairs;  // warps that share a token, angles kept per token (set by the launcher)
 };
+// the kernel's indices of heads and tokens run up to a step past these as ints
+constexpr int kRopeMaxHeads = 1 << 20, kRopeMaxTokens = 0x7FFFFFFF - 4;
 cudaError_t launch_rope(RopeParams& p, int num_sms, cudaStream_t stream);
 
 // NVFP4 GEMM: operands from p.acodes / p.sfa (the first kernel's layouts) and
