@@ -654,3 +654,67 @@ def test_rope_refuses_sizes_that_pass_an_int():
     one = dict(in_=1 << 50, n=1, in_token=0, out_token=64)
     assert rope_call(q=heads(**one), batch=1, T=2 ** 31 - 1, positions=1 << 52) == lib.EINVAL
     assert rope_call(q=heads(**one), batch=1, T=2 ** 31 - 5, positions=1 << 52) != lib.EINVAL
+
+
+def test_binding_refuses_tensors_of_another_gpu(layer, monkeypatch):
+    """The layer claims device 0 here, so that tensors of device 1 are refused before
+    the library is called; the same call on device 0 reaches it."""
+    monkeypatch.setattr(layer, "_device", 0)
+
+    def on(dev, *shape, at=D):
+        strides = tuple(int(np.prod(shape[i + 1:])) for i in range(len(shape)))
+        t = FakeRows(shape, strides)
+        t.nbytes, t.data_ptr, t.get_device = 2 * int(np.prod(shape)), (lambda: at), (lambda: dev)
+        return t
+    need = layer.workspace_bytes(4)
+    norm, res = lib.Norm(), lib.Residual(20 * A)
+    rope = lib.Rope(64, (16, 24, 24))
+    act = {"X": ((4, 256), A), "codes": ((1 << 16,), B), "scales": ((1 << 16,), C), "xl": ((4, 32), D), "Y": ((4, 256), E),
+           "workspace": ((need,), F), "positions": ((4, 3), 8 * A), "q_weight": ((64,), 9 * A),
+           "k_weight": ((64,), 10 * A)}
+    calls = {
+        "norm_quantize_act": (("X", "codes", "scales", "xl", "Y"), lambda a: layer.norm_quantize_act(
+            norm, a["X"], 4, a["codes"], a["scales"], a["xl"], None, a["Y"])),
+        "norm_forward": (("X", "Y", "workspace"), lambda a: layer.norm_forward(
+            norm, a["X"], 4, a["Y"], a["workspace"], need)),
+        "gemm_residual": (("Y", "codes", "scales", "xl"), lambda a: layer.gemm_residual(
+            a["codes"], a["scales"], a["xl"], 4, res, a["Y"])),
+        "forward_residual": (("X", "Y", "workspace"), lambda a: layer.forward_residual(
+            a["X"], 4, res, a["Y"], a["workspace"], need)),
+        "qkv_forward": (("X", "Y", "workspace", "positions", "q_weight", "k_weight"), lambda a: layer.qkv_forward(
+            norm, a["X"], 1, 4, rope, 1, 1, a["positions"], a["Y"], a["workspace"], need, a["q_weight"], a["k_weight"])),
+        "mlp_block_forward": (("X", "Y", "workspace"), lambda a: lib.mlp_block_forward(
+            layer, layer, norm, a["X"], 4, res, a["Y"], a["workspace"], need)),
+    }
+    for name, (operands, call) in calls.items():
+        for wrong in (None,) + operands:
+            a = {}
+            for o_ in operands:
+                shape, at = act[o_]
+                a[o_] = on(1 if o_ == wrong else 0, *shape, at=at)
+                if o_ == "positions":
+                    a[o_].dtype = type("T", (), {"__str__": lambda s: "torch.float32"})()
+            if wrong is None:
+                assert status(lambda: call(a)) in (lib.ESTATE, lib.EUNSUPPORTED), name
+            else:
+                with pytest.raises(ValueError, match=f"{wrong}.*device 1"):
+                    call(a)
+    kw = {"residual": (4, 256), "sum": (4, 256), "weight": (256,), "scale": (1, 256), "shift": (1, 256)}
+    for k, shape in kw.items():
+        n = lib.Norm(**{k: on(1, *shape)})
+        for f in (lambda: layer.norm_quantize_act(n, A, 4, B, C, E), lambda: layer.norm_forward(n, A, 4, E, F, need),
+                  lambda: layer.qkv_forward(n, A, 1, 4, rope, 1, 1, C, E, F, need),
+                  lambda: lib.mlp_block_forward(layer, layer, n, A, 4, None, E, F, need)):
+            with pytest.raises(ValueError, match="Norm.*device 1"):
+                f()
+        with pytest.raises(ValueError, match="one device"):
+            lib.Norm(**{**{k: on(1, *shape)}, **{("weight" if k != "weight" else "sum"): on(0, 4, 256)}})
+    for r in (lib.Residual(on(1, 4, 128)), lib.Residual(B, gate=on(1, 1, 128))):
+        for f in (lambda: layer.gemm_residual(A, 7 * A, C, 4, r, E), lambda: layer.forward_residual(A, 4, r, E, F, need),
+                  lambda: lib.mlp_block_forward(layer, layer, None, A, 4, r, E, F, need)):
+            with pytest.raises(ValueError, match="Residual.*device 1"):
+                f()
+    with pytest.raises(ValueError, match="one device"):
+        lib.Residual(on(0, 4, 128), gate=on(1, 1, 128))
+    with pytest.raises(ValueError, match="one device"):
+        lib.Heads(on(0, 4, 2, 64), on(1, 4, 2, 64))

@@ -243,6 +243,15 @@ def _bf16_tensor(x, what: str):
             raise ValueError(f"{what}: its storage has been released")
 
 
+def _on(device: int, **operands):
+    """A GPU's layer takes no tensor of another GPU (a host-only layer, -1, none at all)."""
+    if device < 0:
+        return
+    for what, x in operands.items():
+        if (_plain_tensor(x) or hasattr(x, "get_device")) and x.get_device() != device:
+            raise ValueError(f"{what}: on device {x.get_device()}, the layer is on device {device}")
+
+
 class _Described:
     """Operands that the library gets as one struct (_c).  The checks of placement
     and layout run when the struct is filled; a tensor can get another storage
@@ -259,6 +268,10 @@ class _Described:
     def _fill(self):
         self._seen = None                              # a refused operand is looked at again
         self._describe()
+        on = {x.get_device() for x in self._keep if hasattr(x, "get_device")}
+        if len(on) > 1:
+            raise ValueError(f"{type(self).__name__}: its tensors must be on one device, got {sorted(on)}")
+        self.device = on.pop() if on else None
         if not any(hasattr(x, "data_ptr") and not _is_tensor(x) for x in self._keep):   # (those: at every call)
             self._seen = [(x, x.data_ptr(), x.numel(), x.dtype) for x in self._keep if _is_tensor(x)]
 
@@ -275,6 +288,14 @@ class _Described:
         return ctypes.byref(self._c)
 
     _ref = property(_now)
+
+    def _for(self, device: int):
+        """The struct for a call of a layer on that device."""
+        now = self._now()
+        if self.device is not None and self.device != device and device >= 0:
+            raise ValueError(f"{type(self).__name__}: its tensors are on device {self.device}, the layer is on "
+                             f"device {device}")
+        return now
 
 
 class _Rows:
@@ -338,9 +359,9 @@ class Norm(_Described):
         self._c = NormStruct(_ptr(residual), _ptr(sum), _ptr(weight), _ptr(scale), _ptr(shift), int(stride or 0),
                              self._per, self._eps, NORM_CENTER if self._center else 0)
 
-    def _args(self, M: int, K: int):
-        """The struct for a call over M tokens, sizes checked."""
-        now = self._now()
+    def _args(self, device: int, M: int, K: int):
+        """The struct for a layer's call over M tokens, sizes checked."""
+        now = self._for(device)
         if M <= 0:
             return now                 # the library answers M <= 0 itself
         for held, one_row, what in self._held:
@@ -370,9 +391,9 @@ class Residual(_Described):
         stride = 0 if self._rows is None or self._rows.rows == 1 else self._rows.stride or 0
         self._c = ResidualStruct(_ptr(residual), _ptr(gate), int(stride), self._per)
 
-    def _args(self, M: int, N: int):
-        """The struct for a call over M tokens, sizes checked."""
-        now = self._now()
+    def _args(self, device: int, M: int, N: int):
+        """The struct for a layer's call over M tokens, sizes checked."""
+        now = self._for(device)
         if M <= 0:
             return now
         if self._held is not None and self._held < M * N * 2:
@@ -426,10 +447,6 @@ class Heads(_Described):
                 _bf16_tensor(weight, "weight")
             _need(weight, self.head_dim * 2, "weight")
 
-        self.device = x.get_device()
-        if any(_is_tensor(t) and t.get_device() != self.device for t in (out, weight)):
-            raise ValueError("x, out and weight must be on one device")
-
         def strides(t):
             s = tuple(t.stride())[:-1]
             s = s if t.dim() == 4 else (0,) + s
@@ -470,7 +487,7 @@ class Layer:
     def __init__(self, handle: int):
         self._h = ctypes.c_void_p(handle)
         info = self.info
-        self._K, self._N = info["K"], info["N"]
+        self._K, self._N, self._device = info["K"], info["N"], info["device"]
         self._act_last = (0, 0, 0)
         self._xl_cols = self._xl_width()
 
@@ -645,7 +662,8 @@ class Layer:
         """Normalisation and the first kernel in one pass (svdq_norm_quantize_act);
         Y, if given, receives the normalised rows."""
         self._need_act(M, X=X, codes=codes, scales=scales, xl=xl)
-        n = norm._args(M, self._K)
+        _on(self._device, X=X, codes=codes, scales=scales, xl=xl, Y=Y)
+        n = norm._args(self._device, M, self._K)
         if M > 0 and Y is not None:
             _need(Y, M * self._K * 2, "Y")
         _check(load().svdq_norm_quantize_act(self._h, n, _ptr(X), M, _ptr(codes), _ptr(scales), _ptr(xl),
@@ -654,7 +672,8 @@ class Layer:
     def norm_forward(self, norm: Norm, X, M: int, Y, workspace, workspace_bytes: int, stream=None, flags: int = 0):
         """Normalisation, then the layer (svdq_norm_linear_forward)."""
         self._need_act(M, X=X, Y=Y)
-        n = norm._args(M, self._K)
+        _on(self._device, X=X, Y=Y, workspace=workspace)
+        n = norm._args(self._device, M, self._K)
         _need(workspace, workspace_bytes, "workspace")
         _check(load().svdq_norm_linear_forward(self._h, n, _ptr(X), M, _ptr(Y), _ptr(workspace),
                                                workspace_bytes, _stream(stream), flags), "svdq_norm_linear_forward")
@@ -666,7 +685,8 @@ class Layer:
         k_heads heads of each row, in place (svdq_qkv_forward)."""
         M = batch * T
         self._need_act(M, X=X, Y=Y)
-        n = None if norm is None else norm._args(M, self._K)
+        _on(self._device, X=X, Y=Y, workspace=workspace, positions=positions, q_weight=q_weight, k_weight=k_weight)
+        n = None if norm is None else norm._args(self._device, M, self._K)
         pos_batch = _positions(rope, positions, batch, T) if batch > 0 and T > 0 else 0
         for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
             if w is not None:
@@ -680,7 +700,8 @@ class Layer:
     def gemm_residual(self, codes, scales, xl, M: int, residual: Residual, Y, stream=None, flags: int = 0):
         """The second kernel with a residual in its epilogue (svdq_gemm_residual)."""
         self._need_act(M, Y=Y, codes=codes, scales=scales, xl=xl)
-        r = residual._args(M, self._N)
+        _on(self._device, Y=Y, codes=codes, scales=scales, xl=xl)
+        r = residual._args(self._device, M, self._N)
         _check(load().svdq_gemm_residual(self._h, _ptr(codes), _ptr(scales), _ptr(xl), M, r, _ptr(Y),
                                          _stream(stream), flags), "svdq_gemm_residual")
 
@@ -688,7 +709,8 @@ class Layer:
                          flags: int = 0):
         """Forward with a residual in the GEMM's epilogue (svdq_linear_forward_residual)."""
         self._need_act(M, X=X, Y=Y)
-        r = residual._args(M, self._N)
+        _on(self._device, X=X, Y=Y, workspace=workspace)
+        r = residual._args(self._device, M, self._N)
         _need(workspace, workspace_bytes, "workspace")
         _check(load().svdq_linear_forward_residual(self._h, _ptr(X), M, r, _ptr(Y), _ptr(workspace),
                                                    workspace_bytes, _stream(stream), flags),
@@ -752,8 +774,9 @@ def mlp_block_forward(fc1: Layer, fc2: Layer, norm: Optional[Norm], X, M: int, r
     """[norm ->] fc1 -> [GELU] -> fc2 [-> residual] (svdq_mlp_block_forward)."""
     fc1._need_act(M, X=X)
     fc2._need_act(M, Y=Y)
-    n = None if norm is None else norm._args(M, fc1._K)
-    r = None if residual is None else residual._args(M, fc2._N)
+    _on(fc1._device, X=X, Y=Y, workspace=workspace)
+    n = None if norm is None else norm._args(fc1._device, M, fc1._K)
+    r = None if residual is None else residual._args(fc2._device, M, fc2._N)
     _need(workspace, workspace_bytes, "workspace")
     _check(load().svdq_mlp_block_forward(fc1._h, fc2._h, n, _ptr(X), M, r, _ptr(Y), _ptr(workspace),
                                          workspace_bytes, _stream(stream), flags), "svdq_mlp_block_forward")
