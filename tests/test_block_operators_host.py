@@ -718,3 +718,23 @@ def test_binding_refuses_tensors_of_another_gpu(layer, monkeypatch):
         lib.Residual(on(0, 4, 128), gate=on(1, 1, 128))
     with pytest.raises(ValueError, match="one device"):
         lib.Heads(on(0, 4, 2, 64), on(1, 4, 2, 64))
+
+
+def test_binding_wants_the_stride_of_rows_given_by_address():
+    """Without one every token would use row 0."""
+    for kw in (dict(scale=E), dict(shift=E), dict(scale=E, shift=F)):
+        with pytest.raises(ValueError, match="mod_stride"):
+            lib.Norm(rows_per_mod=2, **kw)
+        assert lib.Norm(**kw)._c.mod_stride == 0                       # one row for all tokens
+        assert lib.Norm(rows_per_mod=2, mod_stride=512, **kw)._c.mod_stride == 512
+    with pytest.raises(ValueError, match="gate_stride"):
+        lib.Residual(D, gate=E, rows_per_gate=2)
+    assert lib.Residual(D, gate=E)._c.gate_stride == 0
+    assert lib.Residual(D, gate=E, rows_per_gate=2, gate_stride=256)._c.gate_stride == 256
+    # an address beside a tensor takes the tensor's distance only if it is said
+    rows = FakeRows((2, 256), (1536, 1))
+    with pytest.raises(ValueError, match="mod_stride"):
+        lib.Norm(scale=rows, shift=E, rows_per_mod=2)
+    assert lib.Norm(scale=rows, shift=E, rows_per_mod=2, mod_stride=1536)._c.mod_stride == 1536
+    with pytest.raises(ValueError, match="distance"):
+        lib.Norm(scale=rows, shift=E, rows_per_mod=2, mod_stride=512)

@@ -301,12 +301,14 @@ class _Described:
 class _Rows:
     """Rows of BF16 values shared by runs of tokens (modulation scale and
     shift, a gate): a 1D tensor is one row for all tokens, a 2D tensor -- a
-    column range of a wider one too -- row m // rows_per_row for token m.  A
-    raw address takes its stride from the caller and is not checked."""
+    column range of a wider one too -- row m // per for token m (per 0: row 0).
+    A raw address takes its stride from the caller and is not checked."""
 
-    def __init__(self, x, what: str, stride: Optional[int]):
+    def __init__(self, x, what: str, stride: Optional[int], stride_name: str, per: int):
         self.what, self.x, self.rows, self.cols = what, x, None, None
         self.stride = stride
+        if not _is_tensor(x) and per > 0 and stride is None:
+            raise ValueError(f"{what}: an address says nothing of its rows' distance: give {stride_name}")
         if _is_tensor(x):
             _bf16_tensor(x, what)
             if x.dim() not in (1, 2) or x.stride(-1) != 1:
@@ -350,7 +352,7 @@ class Norm(_Described):
             held = _held_bytes(t, what, True)
             if held is not None:
                 self._held.append((held, what == "weight", what))
-        rows = [_Rows(t, what, mod_stride) for t, what in ((scale, "scale"), (shift, "shift")) if t is not None]
+        rows = [_Rows(t, what, mod_stride, "mod_stride", self._per) for t, what in ((scale, "scale"), (shift, "shift")) if t is not None]
         strides = {r.stride for r in rows if r.rows != 1 or mod_stride is not None}
         if len(strides) > 1:
             raise ValueError("scale and shift: their rows must be the same distance apart")
@@ -387,7 +389,7 @@ class Residual(_Described):
         if _is_tensor(residual):
             _bf16_tensor(residual, "residual")
         self._held = _held_bytes(residual, "residual", True)
-        self._rows = None if gate is None else _Rows(gate, "gate", self._gate_stride)
+        self._rows = None if gate is None else _Rows(gate, "gate", self._gate_stride, "gate_stride", self._per)
         stride = 0 if self._rows is None or self._rows.rows == 1 else self._rows.stride or 0
         self._c = ResidualStruct(_ptr(residual), _ptr(gate), int(stride), self._per)
 
