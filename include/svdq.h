@@ -223,7 +223,8 @@ const char* svdq_status_string(svdq_status s);
  * device before replacing the adapter's device buffers, so no forward of this
  * layer may be pending on another thread.  Errors: SVDQ_EINVAL (r < 0, null
  * factors, non-finite scale), SVDQ_EUNSUPPORTED (r > 32, a SVDQ_W4A16_INT4 or
- * SVDQ_W8A8_INT8 layer), SVDQ_ENOMEM, SVDQ_ECUDA.  The fc1 -> fc2 chain (svdq_mlp_*) does not take
+ * SVDQ_W8A8_INT8 layer), SVDQ_ENOMEM, SVDQ_ECUDA; after an error the layer is
+ * usable, with its previous adapter or with none.  The fc1 -> fc2 chain (svdq_mlp_*) does not take
  * layers with an adapter (SVDQ_EUNSUPPORTED). */
 svdq_status svdq_set_lora(svdq_layer* layer, int r, const uint16_t* A_bf16, const uint16_t* B_bf16,
                           float scale);

@@ -115,3 +115,11 @@ def test_lora_static_forward_and_chain_rejection():
         lib.mlp_forward(L, L2, torch_bf16(d["X"]), 256, torch.empty((256, 256), dtype=torch.bfloat16, device="cuda"),
                         torch.empty(1 << 22, dtype=torch.uint8, device="cuda"), 1 << 22)
     assert e.value.status == lib.EUNSUPPORTED
+
+
+def test_adapter_while_host_allocations_fail(tmp_path):
+    """Each failure leaves a layer whose forwards are those of the base layer or of
+    the previous adapter: no kernel sees factors that are not there."""
+    from test_lora_host import run_with_failing_allocations
+    # both formats: two copies of the factors, four operands in the GPU's layouts
+    assert run_with_failing_allocations(tmp_path, 0) >= 12

@@ -111,3 +111,23 @@ def test_library_argument_errors(built):
     with pytest.raises(lib.SvdqError) as e:
         W.set_lora(syn.bf16_bits(A), syn.bf16_bits(B), 1.0)
     assert e.value.status == lib.EUNSUPPORTED
+
+
+def run_with_failing_allocations(tmp_path, device):
+    """alloc_fault.py in a child process with alloc_fault.cpp preloaded; the number of failures it saw."""
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    so = str(tmp_path / "alloc_fault.so")
+    subprocess.run(["g++", "-O1", "-shared", "-fPIC", "-o", so, os.path.join(here, "alloc_fault.cpp")], check=True)
+    env = dict(os.environ, LD_PRELOAD=so, PYTHONPATH=os.path.dirname(here))
+    r = subprocess.run([sys.executable, os.path.join(here, "alloc_fault.py"), str(device)], env=env, timeout=300,
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout + r.stderr
+    return int(r.stdout.split()[-1])
+
+
+def test_adapter_while_host_allocations_fail(tmp_path):
+    # both formats: the two copies of the factors
+    assert run_with_failing_allocations(tmp_path, -1) >= 4

@@ -596,46 +596,53 @@ svdq_status run_k2(const svdq_layer* L, const void* codes, const void* scales, c
   return e == cudaSuccess ? SVDQ_OK : SVDQ_ECUDA;
 }
 
-// (Re)build a layer's LoRA device buffers from the host copies (none when
-// lora_r == 0).  The device must be current and idle for this layer.
-svdq_status upload_lora(svdq_layer* L) {
-  const HostPrep& h = L->host;
-  const int K = h.K, N = h.N, r = h.lora_r;
+void free_lora(svdq_layer* L) {
   cudaFree(L->d_lora_l1t);
   cudaFree(L->d_lora_l1f);
   cudaFree(L->d_lora_l2s);
   cudaFree(L->d_lora_l2t);
   L->d_lora_l1t = L->d_lora_l1f = L->d_lora_l2s = L->d_lora_l2t = nullptr;
+}
+
+// (Re)build a layer's LoRA device buffers from the host copies (none when
+// lora_r == 0, and none on any error).  The device must be current and idle for
+// this layer.
+svdq_status upload_lora(svdq_layer* L) {
+  const HostPrep& h = L->host;
+  const int K = h.K, N = h.N, r = h.lora_r;
+  free_lora(L);
   if (r == 0) return SVDQ_OK;
   // the GEMM's accumulator unit: alpha = g_x g_w (NVFP4) or 2^(ex + ew) (INT4)
   const int alpha_exp = h.format == SVDQ_NVFP4 ? h.g_x_exp + h.g_w_exp : L->i4_ex + L->i4_ew;
-  // l2t: the unfused up projection's [N][64] = [L2b^T | bf16(s B)^T]
-  std::vector<uint16_t> l1t((size_t)32 * K, 0), l2s((size_t)N * 32, 0), l2t((size_t)N * 64, 0);
-  for (int i = 0; i < h.rank; ++i)
-    for (int n = 0; n < N; ++n) l2t[(size_t)n * 64 + i] = h.L2b[(size_t)i * N + n];
-  for (int i = 0; i < r; ++i) {
-    for (int k = 0; k < K; ++k) l1t[(size_t)i * K + k] = h.lora_A[(size_t)k * r + i];
-    for (int n = 0; n < N; ++n) {
-      const uint16_t v = h.lora_B[(size_t)i * N + n];
-      l2t[(size_t)n * 64 + 32 + i] = v;
-      l2s[(size_t)n * 32 + i] = bf16_from_double(std::ldexp((double)bf16_to_float(v), -alpha_exp));
+  cudaError_t e = cudaSuccess;
+  bool maps = false;
+  try {
+    // l2t: the unfused up projection's [N][64] = [L2b^T | bf16(s B)^T]
+    std::vector<uint16_t> l1t((size_t)32 * K, 0), l2s((size_t)N * 32, 0), l2t((size_t)N * 64, 0);
+    for (int i = 0; i < h.rank; ++i)
+      for (int n = 0; n < N; ++n) l2t[(size_t)n * 64 + i] = h.L2b[(size_t)i * N + n];
+    for (int i = 0; i < r; ++i) {
+      for (int k = 0; k < K; ++k) l1t[(size_t)i * K + k] = h.lora_A[(size_t)k * r + i];
+      for (int n = 0; n < N; ++n) {
+        const uint16_t v = h.lora_B[(size_t)i * N + n];
+        l2t[(size_t)n * 64 + 32 + i] = v;
+        l2s[(size_t)n * 32 + i] = bf16_from_double(std::ldexp((double)bf16_to_float(v), -alpha_exp));
+      }
     }
+    const std::vector<uint16_t> l1f = pack_fragments(l1t, K);
+    e = upload(&L->d_lora_l1t, l1t.data(), l1t.size() * 2);
+    if (e == cudaSuccess) e = upload(&L->d_lora_l1f, l1f.data(), l1f.size() * 2);
+    if (e == cudaSuccess) e = upload(&L->d_lora_l2s, l2s.data(), l2s.size() * 2);
+    if (e == cudaSuccess) e = upload(&L->d_lora_l2t, l2t.data(), l2t.size() * 2);
+    maps = e == cudaSuccess && make_map_kchunks(&L->tm_lora_l1t, L->d_lora_l1t, K, 32, 32) &&
+           make_map(&L->tm_lora_l2s, L->d_lora_l2s, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, 32, N, 32, 256,
+                    CU_TENSOR_MAP_SWIZZLE_64B);
+  } catch (const std::bad_alloc&) {
+    e = cudaErrorMemoryAllocation;
   }
-  cudaError_t e = upload(&L->d_lora_l1t, l1t.data(), l1t.size() * 2);
-  if (e == cudaSuccess) e = upload(&L->d_lora_l1f, pack_fragments(l1t, K).data(), l1t.size() * 2);
-  if (e == cudaSuccess) e = upload(&L->d_lora_l2s, l2s.data(), l2s.size() * 2);
-  if (e == cudaSuccess) e = upload(&L->d_lora_l2t, l2t.data(), l2t.size() * 2);
-  if (e != cudaSuccess || !make_map_kchunks(&L->tm_lora_l1t, L->d_lora_l1t, K, 32, 32) ||
-      !make_map(&L->tm_lora_l2s, L->d_lora_l2s, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, 32, N, 32, 256,
-                CU_TENSOR_MAP_SWIZZLE_64B)) {
-    cudaFree(L->d_lora_l1t);
-    cudaFree(L->d_lora_l1f);
-    cudaFree(L->d_lora_l2s);
-    cudaFree(L->d_lora_l2t);
-    L->d_lora_l1t = L->d_lora_l1f = L->d_lora_l2s = L->d_lora_l2t = nullptr;
-    return e == cudaErrorMemoryAllocation ? SVDQ_ENOMEM : SVDQ_ECUDA;
-  }
-  return SVDQ_OK;
+  if (e == cudaSuccess && maps) return SVDQ_OK;
+  free_lora(L);
+  return e == cudaErrorMemoryAllocation ? SVDQ_ENOMEM : SVDQ_ECUDA;
 }
 
 // ------------------------------------------------------------------ serialization
@@ -1540,11 +1547,7 @@ svdq_status svdq_deserialize(const void* src, size_t bytes, int device, svdq_lay
     st = try_upload(L, device);
     if (st == SVDQ_OK && h.lora_r > 0) {
       DeviceGuard g(device);
-      try {
-        st = g.ok ? upload_lora(L) : SVDQ_ECUDA;
-      } catch (const std::bad_alloc&) {
-        st = SVDQ_ENOMEM;
-      }
+      st = g.ok ? upload_lora(L) : SVDQ_ECUDA;
     }
     if (st != SVDQ_OK) free_device(L);
   }
@@ -1572,27 +1575,29 @@ svdq_status svdq_set_lora(svdq_layer* L, int r, const uint16_t* A_bf16, const ui
       for (size_t i = 0; i < b.size(); ++i)
         b[i] = bf16_from_double((double)bf16_to_float(B_bf16[i]) * (double)scale);   // one rounding of s B
     }
-    h.lora_r = r;
-    h.lora_A.swap(a);
-    h.lora_B.swap(b);
-    if (L->device >= 0) {
-      DeviceGuard g(L->device);
-      if (!g.ok) return SVDQ_ECUDA;
-      // no forward of this layer may be pending: the old buffers are released
-      if (cudaDeviceSynchronize() != cudaSuccess) return SVDQ_ECUDA;
-      const svdq_status st = upload_lora(L);
-      if (st != SVDQ_OK) {
-        h.lora_r = 0;
-        h.lora_A.clear();
-        h.lora_B.clear();
-        return st;
-      }
+    const auto set = [&] {
+      h.lora_r = r;
+      h.lora_A.swap(a);
+      h.lora_B.swap(b);
+    };
+    if (L->device < 0) {
+      set();
+      return SVDQ_OK;
     }
-    return SVDQ_OK;
+    DeviceGuard g(L->device);
+    // no forward of this layer may be pending: the old buffers are released
+    if (!g.ok || cudaDeviceSynchronize() != cudaSuccess) return SVDQ_ECUDA;
+    set();
+    const svdq_status st = upload_lora(L);
+    if (st != SVDQ_OK) {
+      h.lora_r = 0;
+      h.lora_A.clear();
+      h.lora_B.clear();
+    }
+    return st;
   } catch (const std::bad_alloc&) {
     return SVDQ_ENOMEM;
   }
-  return SVDQ_OK;
 }
 
 size_t svdq_mlp_workspace_bytes(const svdq_layer* fc1, const svdq_layer* fc2, int M, unsigned flags) {
