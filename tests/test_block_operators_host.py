@@ -738,3 +738,17 @@ def test_binding_wants_the_stride_of_rows_given_by_address():
     assert lib.Norm(scale=rows, shift=E, rows_per_mod=2, mod_stride=1536)._c.mod_stride == 1536
     with pytest.raises(ValueError, match="distance"):
         lib.Norm(scale=rows, shift=E, rows_per_mod=2, mod_stride=512)
+
+
+def test_qkv_binding_wants_bf16_head_weights():
+    L = _layer(K=256, N=64 * 6)
+    rope = lib.Rope(64, (16, 24, 24), norm=True)
+
+    def call(**kw):
+        return status(lambda: L.qkv_forward(None, A, 2, 4, rope, 2, 2, C, E, F, L.workspace_bytes(8), **kw))
+    assert call(q_weight=FakeRows((64,), (1,)), k_weight=FakeRows((64,), (1,))) == lib.ESTATE
+    for name in ("q_weight", "k_weight"):
+        with pytest.raises(ValueError, match=f"{name}.*BF16"):
+            call(**{name: FakeRows((64,), (1,), dtype="torch.float16")})
+        with pytest.raises(ValueError, match=f"{name}.*CUDA"):
+            call(**{name: FakeRows((64,), (1,), cuda=False)})

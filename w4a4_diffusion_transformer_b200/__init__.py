@@ -692,6 +692,8 @@ class Layer:
         pos_batch = _positions(rope, positions, batch, T) if batch > 0 and T > 0 else 0
         for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
             if w is not None:
+                if _is_tensor(w):
+                    _bf16_tensor(w, what)
                 _need(w, rope.head_dim * 2, what)
         _need(workspace, workspace_bytes, "workspace")
         _check(load().svdq_qkv_forward(self._h, n, _ptr(X), batch, T, rope._ref,
