@@ -293,3 +293,27 @@ def test_rope_refuses_host_memory_for_any_operand(operand, pinned):
         assert call(lib.Rope(64, (64,))) == lib.OK
     torch.cuda.synchronize()
     assert bool((keep[1][1] == 1).all()) or operand.endswith("weight")
+
+
+def test_positions_given_by_address_are_those_of_the_tensor():
+    """Shared by all sequences, or each its own with the distance given."""
+    import torch
+    B, T, H, D, K = 3, 20, 2, 64, 128
+    rng = np.random.default_rng(12)
+    L = prepare_gpu(syn.custom_layer(871, M=8, K=K, N=3 * H * D))
+    x = torch_bf16(_rand(rng, B * T, K))
+    pos = torch.from_numpy(_pos(rng, B, T, 2)).cuda()
+    rope = lib.Rope(D, (32, 32))
+    ws = torch.empty(L.workspace_bytes(B * T), dtype=torch.uint8, device="cuda")
+    q = torch_bf16(_rand(rng, B, T, H, D))
+    for tensor, stride in ((pos, T * 2), (pos[0], 0)):
+        a, b = (torch.empty((B * T, 3 * H * D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        c, d = torch.empty_like(q), torch.empty_like(q)
+        L.qkv_forward(None, x, B, T, rope, H, H, tensor, a, ws, ws.numel())
+        L.qkv_forward(None, x, B, T, rope, H, H, tensor.data_ptr(), b, ws, ws.numel(), pos_batch=stride)
+        lib.rope_heads(rope, lib.Heads(q, c), None, tensor)
+        lib.rope_heads(rope, lib.Heads(q, d), None, tensor.data_ptr(), pos_batch=stride)
+        torch.cuda.synchronize()
+        assert torch.equal(a, b) and torch.equal(c, d)
+    with pytest.raises(ValueError, match="pos_batch"):
+        lib.rope_heads(rope, lib.Heads(q, c), None, pos, pos_batch=T * 2)

@@ -457,10 +457,13 @@ class Heads(_Described):
         self._c = HeadsStruct(_ptr(x), _ptr(out), self.heads, *strides(x), *strides(out), _ptr(weight))
 
 
-def _positions(rope: Rope, positions, batch: int, tokens: int) -> int:
-    """Elements between the positions of two sequences (0: shared)."""
+def _positions(rope: Rope, positions, batch: int, tokens: int, pos_batch: int) -> int:
+    """Elements between the positions of two sequences (0: shared), which a raw
+    address takes from the caller."""
     if not _is_tensor(positions):
-        return 0
+        return pos_batch
+    if pos_batch:
+        raise ValueError("pos_batch: for positions given by address; a tensor has its own")
     if not positions.is_cuda or str(positions.dtype) != "torch.float32" or not positions.is_contiguous():
         raise ValueError("positions: must be a contiguous float32 CUDA tensor")
     shape = tuple(positions.shape)
@@ -469,16 +472,17 @@ def _positions(rope: Rope, positions, batch: int, tokens: int) -> int:
     return tokens * rope.axes if len(shape) == 3 and shape[0] > 1 else 0
 
 
-def rope_heads(rope: Rope, q: Heads, k: Optional[Heads], positions, stream=None):
+def rope_heads(rope: Rope, q: Heads, k: Optional[Heads], positions, stream=None, pos_batch: int = 0):
     """Normalise and rotate the heads of q and k (svdq_rope_heads); positions:
-    float32 [token, axis], or [batch, token, axis]."""
+    float32 [token, axis], or [batch, token, axis], or an address with pos_batch
+    elements between two sequences' (0: shared by all)."""
     q_now, k_now = q._now(), None if k is None else k._now()
     for t, what in ((q, "q"), (k, "k")):
         if t is not None and (t.head_dim != rope.head_dim or (t.batch, t.tokens) != (q.batch, q.tokens)):
             raise ValueError(f"{what}: [{t.batch}, {t.tokens}, heads, {t.head_dim}] does not fit the others")
     if (k is not None and k.device != q.device) or (_is_tensor(positions) and positions.get_device() != q.device):
         raise ValueError("q, k and the positions must be on one device")
-    pos_batch = _positions(rope, positions, q.batch, q.tokens)
+    pos_batch = _positions(rope, positions, q.batch, q.tokens, pos_batch)
     _check(load().svdq_rope_heads(rope._ref, q_now, k_now, q.batch, q.tokens,
                                   _ptr(positions), pos_batch, _stream(stream)), "svdq_rope_heads")
 
@@ -682,14 +686,15 @@ class Layer:
 
     def qkv_forward(self, norm: Optional[Norm], X, batch: int, T: int, rope: Rope, q_heads: int, k_heads: int,
                     positions, Y, workspace, workspace_bytes: int, q_weight=None, k_weight=None, stream=None,
-                    flags: int = 0):
+                    flags: int = 0, pos_batch: int = 0):
         """[norm ->] layer -> per-head norm and rotation of the first q_heads +
-        k_heads heads of each row, in place (svdq_qkv_forward)."""
+        k_heads heads of each row, in place (svdq_qkv_forward); positions and
+        pos_batch as for rope_heads."""
         M = batch * T
         self._need_act(M, X=X, Y=Y)
         _on(self._device, X=X, Y=Y, workspace=workspace, positions=positions, q_weight=q_weight, k_weight=k_weight)
         n = None if norm is None else norm._args(self._device, M, self._K)
-        pos_batch = _positions(rope, positions, batch, T) if batch > 0 and T > 0 else 0
+        pos_batch = _positions(rope, positions, batch, T, pos_batch) if batch > 0 and T > 0 else 0
         for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
             if w is not None:
                 if _is_tensor(w):
