@@ -444,3 +444,20 @@ def test_the_forms_above_are_all():
         want |= {(f, 12, 8, n, False), (f, 2, 16, n, False), (f, 4, 16, n, False)}
         want |= {(f, C, 16, n, full) for C in (6, 12) for full in (False, True)}
     assert want == reached
+
+
+@pytest.mark.parametrize("fmt,nmt,K", [("w8a8", 0, 576), ("w8a8", 1, 3072), ("nvfp4", 0, 1472), ("nvfp4", 2, 2944),
+                                       ("int4", 2, 320), ("int4", 0, 14336)])
+def test_rows_of_one_value_have_no_variance(fmt, nmt, K):
+    """Layer norm of a row that holds one value is the shift, exactly: K equal BF16
+    values (8 bits) add up without rounding (K < 2^14), and their sum divided by K
+    is the value again."""
+    import torch
+    L = _layer_of(fmt, nmt, K)
+    vals = syn.to_bf16(np.array([1000.0, -1000.0, 3.14, 1e4, 0.1, 77.7, -1e30, 2.0 ** -20], dtype=np.float32))
+    M = len(vals)
+    d = _inputs(30, M, K, residual=False, mods=1, center=True)
+    d["X"][:] = vals[:, None]
+    got = run(L, d)
+    np.testing.assert_array_equal(got["y"], np.broadcast_to(d["mod"][0, :K], (M, K)))
+    compare_with_first_kernel(L, got, M, K)
