@@ -370,7 +370,8 @@ def launched(fmt, M, K, nmt, sms):
                 l += 1
             c = chunks(l)
             C = 2 if c <= 2 else 4 if c <= 4 else 6 if c <= 6 else 12
-    full = C >= 6 and not (nmt and warps == 8) and K == (256 * C) << l
+    spills = C == 12 and warps == 16 and (fmt == "w8a8" or (fmt == "int4" and nmt == 4))
+    full = C >= 4 and not spills and not (nmt == 0 and warps == 16 and C == 4) and K == (256 * C) << l
     return fmt, C, warps, nmt, full
 
 
@@ -381,9 +382,10 @@ PLAIN = [  # M, K, options; rank 0, no adapter: codes and scales only
     (1201, 512, dict(mods=2, center=True)),
     (1201, 576, dict(weight=False, mods=401, rows_per_mod=3)),   # three or four modulation rows to a tile
     (1300, 128, dict(mods=1300, rows_per_mod=1, center=True)),   # ... one for each token
-    (1201, 1024, dict(residual=False)),
+    (1201, 896, dict(weight=False, mods=2)),
+    (1201, 1024, dict(residual=False)),             # every lane full: from four chunks on
     (1201, 1472, dict(mods=3)),
-    (1201, 1536, dict(mods=2, center=True)),        # every lane full: one, two, four warps to a row
+    (1201, 1536, dict(mods=2, center=True)),        # ... and one, two, four warps to a row
     (650, 3072, dict(mods=4, weight=False, center=True)),
     (300, 6144, dict(residual=False)),
     (300, 8192, dict(mods=2)),
@@ -394,6 +396,7 @@ PLAIN = [  # M, K, options; rank 0, no adapter: codes and scales only
 ]
 PROJECT = [
     (50, 256, dict(mods=2)),
+    (1201, 1920, dict(center=True)),
     (1201, 2048, dict(mods=2, center=True)),
     (1201, 576, dict(weight=False, mods=401, rows_per_mod=3)),
     (1201, 2816, dict(residual=False)),
@@ -401,6 +404,7 @@ PROJECT = [
     (2401, 2944, dict(mods=2)),
     (2401, 3072, dict(mods=2, weight=False, center=True)),
     (1201, 6144, dict(residual=False, mods=1)),
+    (301, 12288, dict(mods=2)),
     (300, 14336, dict(mods=2, center=True)),        # 16 rows do not fit in shared memory: CTAs of 8 warps
 ]
 FORMS = ([(f, 0, M, K, o_) for f in ("nvfp4", "int4", "w8a8") for M, K, o_ in PLAIN]
@@ -437,12 +441,13 @@ def test_the_forms_above_are_all():
     import torch
     sms = torch.cuda.get_device_properties(0).multi_processor_count
     reached = {launched(f, M, K, n, sms) for f, n, M, K, _ in FORMS}
-    plain = [(C, 8, 0, False) for C in (1, 2, 3, 4, 6)] + [(6, 8, 0, True), (4, 16, 0, False), (6, 16, 0, False),
-                                                           (6, 16, 0, True)]
+    plain = [(C, 8, 0, False) for C in (1, 2, 3, 4, 6)] + [(C, 8, 0, True) for C in (4, 6)]
+    plain += [(4, 16, 0, False), (6, 16, 0, False), (6, 16, 0, True)]
     want = {(f,) + v for f in ("nvfp4", "int4", "w8a8") for v in plain}
     for f, n in (("w8a8", 1), ("nvfp4", 2), ("nvfp4", 4), ("int4", 2), ("int4", 4)):
-        want |= {(f, 12, 8, n, False), (f, 2, 16, n, False), (f, 4, 16, n, False)}
-        want |= {(f, C, 16, n, full) for C in (6, 12) for full in (False, True)}
+        want |= {(f, 2, 16, n, False)} | {(f, C, 16, n, full) for C in (4, 6, 12) for full in (False, True)}
+        want |= {(f, 12, 8, n, full) for full in (False, True)}
+    want -= {("w8a8", 12, 16, 1, True), ("int4", 12, 16, 4, True)}
     assert want == reached
 
 

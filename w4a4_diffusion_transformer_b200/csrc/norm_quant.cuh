@@ -473,11 +473,17 @@ cudaError_t launch_t(NormParams& p, int num_sms, cudaStream_t stream) {
 
 template <int kFmt, int C, int kWarps, int kMt>
 cudaError_t launch(NormParams& p, int num_sms, cudaStream_t stream) {
-  // (the unpredicated form of rows with few chunks is not worth its code: with
-  // 12 chunks it took 26.1 instead of 28.6 us for 4608 x 3072 NVFP4 codes and XL)
-  constexpr bool kFull = C >= 6 && kWarps * (kMt > 0) != 8;
+  // Without predicates where every lane is full: 4608 rows of 3072 W8A8 22.0 instead
+  // of 22.7 us, NVFP4 21.1 / 22.5, INT4 24.4 / 25.8; with XL NVFP4 31.2 / 34.5, INT4
+  // 36.7 / 37.3; of 4096 NVFP4 29.5 / 31.4; 2048 of 12288 NVFP4 with XL 109.7 / 125.
+  // Twelve chunks kept as FP32 spill more that way beside W8A8's projection (224
+  // against 28 bytes; 31.6 against 29.0 us, 6144 columns 66.8 / 63.8) and beside 64
+  // XL columns (INT4 45.6 / 44.8).  Rows of up to three chunks gain 0.1 to 0.3 us, not
+  // worth their code; four chunks of 16 warps without a projection are never full.
+  constexpr bool kSpills = C == 12 && kWarps == 16 && (kFmt == kFmtInt8 || (kFmt == kFmtInt4 && kMt == 4));
+  constexpr bool kFull = C >= 4 && !kSpills && !(kMt == 0 && kWarps == 16 && C == 4);
   return kFull && p.K == (256 * C) << p.log2_warps ? launch_t<kFmt, C, kWarps, kMt, kFull>(p, num_sms, stream)
-                                          : launch_t<kFmt, C, kWarps, kMt, false>(p, num_sms, stream);
+                                                   : launch_t<kFmt, C, kWarps, kMt, false>(p, num_sms, stream);
 }
 
 // Chunks of a lane with 2^l warps to a row.
