@@ -466,3 +466,19 @@ def test_rows_of_one_value_have_no_variance(fmt, nmt, K):
     got = run(L, d)
     np.testing.assert_array_equal(got["y"], np.broadcast_to(d["mod"][0, :K], (M, K)))
     compare_with_first_kernel(L, got, M, K)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "int4", "w8a8"])
+@pytest.mark.parametrize("M,K", [(5, 320), (1201, 1024)])
+def test_rows_too_small_for_a_reciprocal(fmt, M, K):
+    """Normalised rows of 1e-36 down to BF16's smallest value: scales that are
+    subnormal, or whose reciprocal is infinite, give the first kernel's codes."""
+    L = _layer_of(fmt, 0, K)
+    for w in (1e-36, 2e-37, 1e-38, 1e-39, 2e-40):
+        d = _inputs(31, M, K)
+        d["X"][0] = 0.0
+        d["weight"] = syn.to_bf16(d["weight"] * np.float32(w))
+        assert np.all(d["weight"][np.abs(d["weight"]) > 0] < 1e-35) and np.any(d["weight"] != 0)
+        got = run(L, d)
+        check(L, d, got)
+        compare_with_first_kernel(L, got, M, K)

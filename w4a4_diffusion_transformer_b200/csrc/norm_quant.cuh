@@ -344,7 +344,18 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) norm_quant_kernel(co
         sx[row] = sc;
         sx[p.mpad + row] = inv;
       }
-      const float2 i2 = make_float2(inv, inv);
+      float2 i2 = make_float2(inv, inv);
+      if (inv > 3.40282347e38f) {
+        // a scale below 2^-128 has no finite reciprocal: everything but zero clamps
+        // to +-127, as in the first kernel
+        i2 = make_float2(1.f, 1.f);
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            f[c][i] = make_float2(f[c][i].x == 0.f ? 0.f : copysignf(127.f, f[c][i].x),
+                                  f[c][i].y == 0.f ? 0.f : copysignf(127.f, f[c][i].y));
+      }
       // stages of 128 codes: chunk q is half of a 16-byte piece of stage q / 16
       uint8_t* o = p.codes + act_tile_offset(row, q0 >> 4, (q0 & 15) >> 1, p.nst) + (lane & 1) * 8;
 #pragma unroll
@@ -354,7 +365,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) norm_quant_kernel(co
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             // the sum with 1.5 * 2^23 holds the rounded integer, two's
-            // complement, in its low byte (|q| <= 127 (1 + 2^-22): no clamp)
+            // complement, in its low byte (|q| <= 127 (1 + 2^-20): no clamp)
             const float2 k = __fmul2_rn(f[c][i], i2);
             t[2 * i] = __float_as_uint(__fadd_rn(k.x, 12582912.0f));
             t[2 * i + 1] = __float_as_uint(__fadd_rn(k.y, 12582912.0f));
