@@ -161,7 +161,7 @@ def _ptr(x) -> Optional[int]:
     """Device/host address of a tensor-like object (data_ptr()), an int, or None."""
     if x is None:
         return None
-    if _plain_tensor(x):
+    if x.__class__ is _torch_tensor:
         return x.data_ptr()
     if isinstance(x, int):
         return x
@@ -192,7 +192,7 @@ def _held_bytes(x, what: str, device: bool) -> Optional[int]:
     return None
 
 
-_torch_tensor = None
+_torch_tensor = None                                   # torch.Tensor, once one was passed
 
 
 def _plain_tensor(x) -> bool:
@@ -206,13 +206,18 @@ def _plain_tensor(x) -> bool:
     return x.__class__ is _torch_tensor
 
 
-def _need(x, nbytes: int, what: str, device: bool = True):
+def _need(x, nbytes: int, what: str, device: bool = True, on: int = -1):
+    """x holds nbytes on a device (or the host); with on >= 0, on that device."""
     # the usual operand, a contiguous tensor in the right place, without detours
-    if _plain_tensor(x) and x.is_cuda is device and x.is_contiguous() and x.nbytes >= nbytes:
+    if x.__class__ is _torch_tensor and x.is_contiguous() and x.nbytes >= nbytes and (
+            x.is_cuda is device if on < 0 else x.get_device() == on):
         return
+    _plain_tensor(x)                                    # (the first call: torch is known from now on)
     have = _held_bytes(x, what, device)
     if have is not None and have < nbytes:
         raise ValueError(f"{what}: holds {have} bytes, the call accesses {nbytes}")
+    if on >= 0 and hasattr(x, "get_device") and x.get_device() != on:
+        raise ValueError(f"{what}: on device {x.get_device()}, the layer is on device {on}")
 
 
 def _stream(s) -> Optional[int]:
@@ -243,15 +248,6 @@ def _bf16_tensor(x, what: str):
             raise ValueError(f"{what}: its storage has been released")
 
 
-def _on(device: int, **operands):
-    """A GPU's layer takes no tensor of another GPU (a host-only layer, -1, none at all)."""
-    if device < 0:
-        return
-    for what, x in operands.items():
-        if (_plain_tensor(x) or hasattr(x, "get_device")) and x.get_device() != device:
-            raise ValueError(f"{what}: on device {x.get_device()}, the layer is on device {device}")
-
-
 class _Described:
     """Operands that the library gets as one struct (_c).  The checks of placement
     and layout run when the struct is filled; a tensor can get another storage
@@ -272,6 +268,7 @@ class _Described:
         if len(on) > 1:
             raise ValueError(f"{type(self).__name__}: its tensors must be on one device, got {sorted(on)}")
         self.device = on.pop() if on else None
+        self._ref_c = ctypes.byref(self._c)
         if not any(hasattr(x, "data_ptr") and not _is_tensor(x) for x in self._keep):   # (those: at every call)
             self._seen = [(x, x.data_ptr(), x.numel(), x.dtype) for x in self._keep if _is_tensor(x)]
 
@@ -285,17 +282,14 @@ class _Described:
                 if x.data_ptr() != ptr or x.numel() != n or x.dtype is not dtype:
                     self._fill()
                     break
-        return ctypes.byref(self._c)
+        return self._ref_c
 
     _ref = property(_now)
 
-    def _for(self, device: int):
-        """The struct for a call of a layer on that device."""
-        now = self._now()
+    def _on(self, device: int):
         if self.device is not None and self.device != device and device >= 0:
             raise ValueError(f"{type(self).__name__}: its tensors are on device {self.device}, the layer is on "
                              f"device {device}")
-        return now
 
 
 class _Rows:
@@ -363,7 +357,8 @@ class Norm(_Described):
 
     def _args(self, device: int, M: int, K: int):
         """The struct for a layer's call over M tokens, sizes checked."""
-        now = self._for(device)
+        now = self._now()
+        self._on(device)
         if M <= 0:
             return now                 # the library answers M <= 0 itself
         for held, one_row, what in self._held:
@@ -395,7 +390,8 @@ class Residual(_Described):
 
     def _args(self, device: int, M: int, N: int):
         """The struct for a layer's call over M tokens, sizes checked."""
-        now = self._for(device)
+        now = self._now()
+        self._on(device)
         if M <= 0:
             return now
         if self._held is not None and self._held < M * N * 2:
@@ -457,6 +453,16 @@ class Heads(_Described):
         self._c = HeadsStruct(_ptr(x), _ptr(out), self.heads, *strides(x), *strides(out), _ptr(weight))
 
 
+_float32 = None                                        # torch.float32, once positions were passed
+
+
+def _is_float32(dtype) -> bool:
+    global _float32
+    if dtype is not _float32 and str(dtype) == "torch.float32":
+        _float32 = dtype
+    return dtype is _float32
+
+
 def _positions(rope: Rope, positions, batch: int, tokens: int, pos_batch: int) -> int:
     """Elements between the positions of two sequences (0: shared), which a raw
     address takes from the caller."""
@@ -464,7 +470,7 @@ def _positions(rope: Rope, positions, batch: int, tokens: int, pos_batch: int) -
         return pos_batch
     if pos_batch:
         raise ValueError("pos_batch: for positions given by address; a tensor has its own")
-    if not positions.is_cuda or str(positions.dtype) != "torch.float32" or not positions.is_contiguous():
+    if not positions.is_cuda or not _is_float32(positions.dtype) or not positions.is_contiguous():
         raise ValueError("positions: must be a contiguous float32 CUDA tensor")
     shape = tuple(positions.shape)
     if shape not in ((tokens, rope.axes), (1, tokens, rope.axes), (batch, tokens, rope.axes)):
@@ -478,7 +484,7 @@ def rope_heads(rope: Rope, q: Heads, k: Optional[Heads], positions, stream=None,
     elements between two sequences' (0: shared by all)."""
     q_now, k_now = q._now(), None if k is None else k._now()
     for t, what in ((q, "q"), (k, "k")):
-        if t is not None and (t.head_dim != rope.head_dim or (t.batch, t.tokens) != (q.batch, q.tokens)):
+        if t is not None and (t.head_dim != rope.head_dim or t.batch != q.batch or t.tokens != q.tokens):
             raise ValueError(f"{what}: [{t.batch}, {t.tokens}, heads, {t.head_dim}] does not fit the others")
     if (k is not None and k.device != q.device) or (_is_tensor(positions) and positions.get_device() != q.device):
         raise ValueError("q, k and the positions must be on one device")
@@ -627,19 +633,19 @@ class Layer:
         _check(load().svdq_act_codes_to_logical(self._h, _ptr(src), M, _ptr(out)), "svdq_act_codes_to_logical")
         return out
 
-    def _need_act(self, M: int, X=None, Y=None, codes=None, scales=None, xl=None):
+    def _need_act(self, M: int, X=None, Y=None, codes=None, scales=None, xl=None, on: int = -1):
         if M <= 0:
             return                     # the library answers M <= 0 itself
         if X is not None:
-            _need(X, M * self._K * 2, "X")
+            _need(X, M * self._K * 2, "X", True, on)
         if Y is not None:
-            _need(Y, M * self._N * 2, "Y")
+            _need(Y, M * self._N * 2, "Y", True, on)
         if codes is not None:
-            _need(codes, self._act_bytes(M)[0], "codes")
+            _need(codes, self._act_bytes(M)[0], "codes", True, on)
         if scales is not None:
-            _need(scales, self._act_bytes(M)[1], "scales")
+            _need(scales, self._act_bytes(M)[1], "scales", True, on)
         if xl is not None:
-            _need(xl, M * self._xl_cols * 2, "xl")
+            _need(xl, M * self._xl_cols * 2, "xl", True, on)
 
     def forward(self, X, M: int, Y, workspace, workspace_bytes: int, stream=None, flags: int = 0):
         self._need_act(M, X=X, Y=Y)
@@ -667,20 +673,18 @@ class Layer:
     def norm_quantize_act(self, norm: Norm, X, M: int, codes, scales, xl, stream=None, Y=None):
         """Normalisation and the first kernel in one pass (svdq_norm_quantize_act);
         Y, if given, receives the normalised rows."""
-        self._need_act(M, X=X, codes=codes, scales=scales, xl=xl)
-        _on(self._device, X=X, codes=codes, scales=scales, xl=xl, Y=Y)
+        self._need_act(M, X=X, codes=codes, scales=scales, xl=xl, on=self._device)
         n = norm._args(self._device, M, self._K)
         if M > 0 and Y is not None:
-            _need(Y, M * self._K * 2, "Y")
+            _need(Y, M * self._K * 2, "Y", True, self._device)
         _check(load().svdq_norm_quantize_act(self._h, n, _ptr(X), M, _ptr(codes), _ptr(scales), _ptr(xl),
                                              _ptr(Y), _stream(stream)), "svdq_norm_quantize_act")
 
     def norm_forward(self, norm: Norm, X, M: int, Y, workspace, workspace_bytes: int, stream=None, flags: int = 0):
         """Normalisation, then the layer (svdq_norm_linear_forward)."""
-        self._need_act(M, X=X, Y=Y)
-        _on(self._device, X=X, Y=Y, workspace=workspace)
+        self._need_act(M, X=X, Y=Y, on=self._device)
         n = norm._args(self._device, M, self._K)
-        _need(workspace, workspace_bytes, "workspace")
+        _need(workspace, workspace_bytes, "workspace", True, self._device)
         _check(load().svdq_norm_linear_forward(self._h, n, _ptr(X), M, _ptr(Y), _ptr(workspace),
                                                workspace_bytes, _stream(stream), flags), "svdq_norm_linear_forward")
 
@@ -691,16 +695,16 @@ class Layer:
         k_heads heads of each row, in place (svdq_qkv_forward); positions and
         pos_batch as for rope_heads."""
         M = batch * T
-        self._need_act(M, X=X, Y=Y)
-        _on(self._device, X=X, Y=Y, workspace=workspace, positions=positions, q_weight=q_weight, k_weight=k_weight)
+        self._need_act(M, X=X, Y=Y, on=self._device)
         n = None if norm is None else norm._args(self._device, M, self._K)
         pos_batch = _positions(rope, positions, batch, T, pos_batch) if batch > 0 and T > 0 else 0
+        _need(positions, 0, "positions", True, self._device)
         for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
             if w is not None:
                 if _is_tensor(w):
                     _bf16_tensor(w, what)
-                _need(w, rope.head_dim * 2, what)
-        _need(workspace, workspace_bytes, "workspace")
+                _need(w, rope.head_dim * 2, what, True, self._device)
+        _need(workspace, workspace_bytes, "workspace", True, self._device)
         _check(load().svdq_qkv_forward(self._h, n, _ptr(X), batch, T, rope._ref,
                                        q_heads, k_heads, _ptr(q_weight), _ptr(k_weight), _ptr(positions), pos_batch,
                                        _ptr(Y), _ptr(workspace), workspace_bytes, _stream(stream), flags),
@@ -708,8 +712,7 @@ class Layer:
 
     def gemm_residual(self, codes, scales, xl, M: int, residual: Residual, Y, stream=None, flags: int = 0):
         """The second kernel with a residual in its epilogue (svdq_gemm_residual)."""
-        self._need_act(M, Y=Y, codes=codes, scales=scales, xl=xl)
-        _on(self._device, Y=Y, codes=codes, scales=scales, xl=xl)
+        self._need_act(M, Y=Y, codes=codes, scales=scales, xl=xl, on=self._device)
         r = residual._args(self._device, M, self._N)
         _check(load().svdq_gemm_residual(self._h, _ptr(codes), _ptr(scales), _ptr(xl), M, r, _ptr(Y),
                                          _stream(stream), flags), "svdq_gemm_residual")
@@ -717,10 +720,9 @@ class Layer:
     def forward_residual(self, X, M: int, residual: Residual, Y, workspace, workspace_bytes: int, stream=None,
                          flags: int = 0):
         """Forward with a residual in the GEMM's epilogue (svdq_linear_forward_residual)."""
-        self._need_act(M, X=X, Y=Y)
-        _on(self._device, X=X, Y=Y, workspace=workspace)
+        self._need_act(M, X=X, Y=Y, on=self._device)
         r = residual._args(self._device, M, self._N)
-        _need(workspace, workspace_bytes, "workspace")
+        _need(workspace, workspace_bytes, "workspace", True, self._device)
         _check(load().svdq_linear_forward_residual(self._h, _ptr(X), M, r, _ptr(Y), _ptr(workspace),
                                                    workspace_bytes, _stream(stream), flags),
                "svdq_linear_forward_residual")
@@ -781,11 +783,10 @@ def mlp_forward(fc1: Layer, fc2: Layer, X, M: int, Y, workspace, workspace_bytes
 def mlp_block_forward(fc1: Layer, fc2: Layer, norm: Optional[Norm], X, M: int, residual: Optional[Residual], Y,
                       workspace, workspace_bytes: int, stream=None, flags: int = 0):
     """[norm ->] fc1 -> [GELU] -> fc2 [-> residual] (svdq_mlp_block_forward)."""
-    fc1._need_act(M, X=X)
-    fc2._need_act(M, Y=Y)
-    _on(fc1._device, X=X, Y=Y, workspace=workspace)
+    fc1._need_act(M, X=X, on=fc1._device)
+    fc2._need_act(M, Y=Y, on=fc2._device)
     n = None if norm is None else norm._args(fc1._device, M, fc1._K)
     r = None if residual is None else residual._args(fc2._device, M, fc2._N)
-    _need(workspace, workspace_bytes, "workspace")
+    _need(workspace, workspace_bytes, "workspace", True, fc1._device)
     _check(load().svdq_mlp_block_forward(fc1._h, fc2._h, n, _ptr(X), M, r, _ptr(Y), _ptr(workspace),
                                          workspace_bytes, _stream(stream), flags), "svdq_mlp_block_forward")
