@@ -482,3 +482,30 @@ def test_rows_too_small_for_a_reciprocal(fmt, M, K):
         got = run(L, d)
         check(L, d, got)
         compare_with_first_kernel(L, got, M, K)
+
+
+def test_an_operand_back_at_its_old_address_is_looked_at_again():
+    """Storages freed and taken again by the allocator: the same address may hold
+    another type or size by then."""
+    import torch
+    L = prepare_gpu(syn.custom_layer(852, M=8, K=1024, N=64), fmt="w8a8", rank=0)
+    M, d = 20, _inputs(13, 20, 1024, residual=False)
+    x, y = torch_bf16(d["X"]), torch.empty((M, 1024), dtype=torch.bfloat16, device="cuda")
+    w = torch.nn.Parameter(torch_bf16(d["weight"]), requires_grad=False)
+    n = lib.Norm(weight=w, eps=EPS)
+    codes = torch.empty(L.act_code_bytes(M), dtype=torch.uint8, device="cuda")
+    scales = torch.empty(L.act_scale_bytes(M), dtype=torch.uint8, device="cuda")
+
+    def call():
+        L.norm_quantize_act(n, x, M, codes, scales, None, Y=y)
+        torch.cuda.synchronize()
+        return to_numpy_f32(y)
+    first = call()
+    for other in (lambda t: t.float()[:512], lambda t: t.half(), lambda t: t[:512]):
+        keep = w.data.cpu()
+        w.data = keep                                   # the GPU's storage may be given back here ...
+        w.data = other(keep).cuda()                     # ... and taken again
+        with pytest.raises(ValueError, match="weight"):
+            call()
+        w.data = keep.cuda()
+        np.testing.assert_array_equal(call(), first)

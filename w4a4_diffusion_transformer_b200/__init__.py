@@ -252,17 +252,19 @@ class _Described:
     """Operands that the library gets as one struct (_c).  The checks of placement
     and layout run when the struct is filled; a tensor can get another storage
     later (tensor.data = ..., a module moved between devices), so every call
-    compares address, number of values and type first, and fills the struct again
-    where one changed.  (Shapes and strides too would cost twice as much, 2 us
-    for the six operands of a rotation; a tensor transposed in place keeps the
-    layout it was described with.)"""
+    compares the addresses first, and fills the struct again where one changed.  An
+    alias of each operand keeps its storage until then, so that the same address is
+    the same memory, whatever happened to the tensor in between.  (Comparing sizes
+    and types at each call too would cost 0.7 us more for a rotation's six operands;
+    a tensor that shows the same memory in another shape keeps the layout it was
+    described with.)"""
 
     def _hold(self, *operands):
         self._keep = operands
         self._fill()
 
     def _fill(self):
-        self._seen = None                              # a refused operand is looked at again
+        self._seen = self._aliases = None              # a refused operand is looked at again
         self._describe()
         on = {x.get_device() for x in self._keep if hasattr(x, "get_device")}
         if len(on) > 1:
@@ -270,7 +272,9 @@ class _Described:
         self.device = on.pop() if on else None
         self._ref_c = ctypes.byref(self._c)
         if not any(hasattr(x, "data_ptr") and not _is_tensor(x) for x in self._keep):   # (those: at every call)
-            self._seen = [(x, x.data_ptr(), x.numel(), x.dtype) for x in self._keep if _is_tensor(x)]
+            tensors = [x for x in self._keep if _is_tensor(x)]
+            self._aliases = [x.detach() for x in tensors if hasattr(x, "detach")]
+            self._seen = [(x, x.data_ptr()) for x in tensors]
 
     def _now(self):
         """The struct as a call's argument, with the operands as they are now."""
@@ -278,8 +282,8 @@ class _Described:
         if seen is None:
             self._fill()
         else:
-            for x, ptr, n, dtype in seen:
-                if x.data_ptr() != ptr or x.numel() != n or x.dtype is not dtype:
+            for x, ptr in seen:
+                if x.data_ptr() != ptr:
                     self._fill()
                     break
         return self._ref_c
