@@ -11,7 +11,9 @@
 //   Y     = bf16([gelu](s_x s_w acc_i + acc_b + b))
 //
 // A and B types differ from the branch's, so the branch cannot share the
-// integer accumulator: TMEM columns 0-255 hold acc_i, 256-511 acc_b.
+// integer accumulator: TMEM columns 0-255 hold acc_i, 256-511 acc_b.  (Where K is
+// split over a cluster, in the calls that allow it, each CTA's share of acc_i is
+// exact; the shares are rounded to FP32, scaled and then added.)
 //
 // Structure (one CTA per SM, persistent over 128 x 256 output tiles, 16 warps):
 //   warp 0     activation producer: per stage of 128 K the 128 x 128-byte code
@@ -84,8 +86,8 @@ __device__ __forceinline__ void record_error(int* err, volatile int* abort_flag,
   *abort_flag = 1;
 }
 
-// kRes: the epilogue adds the gated output to the residual of tm_r (kResGelu:
-// GELU in front of it; without a residual p.gelu says).  kSplit: the CTAs of a
+// kRes: the epilogue adds the gated output to p.res.residual (kResGelu: GELU in
+// front of it; without a residual p.gelu says).  kSplit: the CTAs of a
 // cluster share a tile's K stages (split_k.cuh); the branch is rank 0's.
 template <bool kRes, bool kResGelu, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)

@@ -13,11 +13,12 @@
 // then bit for bit those of the unfused sequence on the same y.  Sums, means
 // and products are FP32.
 //
-// One B200, 4608 x 3072 with a residual: W8A8 22.5 us (4.4 TB/s of what it reads and
-// writes; 18432 rows 70.8 us, 5.6 TB/s; a copy 6.56), NVFP4 codes and XL 32.2,
-// INT4 37.9; one row 3.2 us.  W8A8 is bound by memory latency at the ends of a CTA's
-// few tiles, then by memory; the others by the dependent chains of a tile's
-// phases (40 % of the issue slots), two tiles per SM at this size.
+// One B200, 4608 x 3072 with a residual: codes and scales alone W8A8 22.2 us (4.5
+// TB/s of what it reads and writes; 18432 rows 70.6 us, 5.6 TB/s; a copy 6.56), NVFP4
+// 21.2, INT4 24.5; with XL W8A8 29.1, NVFP4 31.4, INT4 36.8; one row 3.2 us, with XL
+// 5.2 to 5.9.  Without XL it is bound by memory latency at the ends of a CTA's few
+// tiles, then by memory; with XL by the dependent chains of a tile's phases (40 % of
+// the issue slots), two tiles per SM at this size.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -31,14 +32,14 @@ namespace svdq {
 
 namespace {
 
-// A CTA of 8 warps (16 with a projection) handles tiles of 8 / W (16 / W) rows, W
-// warps to a row; a lane of the row's warp w owns the C chunks of 8 values
-// 32 (C w + c) + lane and keeps them in registers, as FP32, from the load to the
+// A CTA of 8 or 16 warps (launch_plain and launch_project below choose) handles
+// tiles of 8 / W or 16 / W rows, W warps to a row; a lane of the row's warp w owns
+// the C chunks of 8 values 32 (C w + c) + lane and keeps them in registers, as FP32, from the load to the
 // codes: unpacking BF16 pairs again for every pass took twice the instructions,
 // and those are what bounds the kernel before memory does.  Twelve chunks of the
 // NVFP4 quantizer do not fit that way; kept as BF16 and unpacked per pass they
 // spill less (4608 x 3072 codes and XL: 24.3 against 26.1 us, with a residual
-// 32.2 against 35.0; INT4 38.2 against 38.0, so it keeps FP32).  Consecutive
+// 32.2 against 35.0 when it was chosen; INT4 38.2 against 38.0, so it keeps FP32).  Consecutive
 // chunks lie a constant apart in every operand and layout, so that their addresses
 // are immediates.  The columns' parameters w (1 + scale), shift and 1/lam sit in
 // shared memory as FP32, filled once per CTA and modulation row; chunk q's eight
